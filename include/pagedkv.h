@@ -74,7 +74,8 @@
 extern "C" {
 #endif
 
-typedef enum { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2 } pkv_dtype;
+/* PKV_KV4: a 4-bit pool (see "4-bit caches" below); only the calls that say so take it. */
+typedef enum { PKV_F32 = 0, PKV_F16 = 1, PKV_BF16 = 2, PKV_KV4 = 3 } pkv_dtype;
 
 typedef enum {
   PKV_OK = 0,
@@ -93,7 +94,7 @@ typedef struct {
   int32_t block_size;   /* tokens per block: 8, 16, 32 or 64 */
   int32_t num_kv_heads;
   int32_t head_dim;     /* 64 or 128 */
-  int32_t dtype;        /* pkv_dtype of the caches, q, k and v */
+  int32_t dtype;        /* pkv_dtype of the caches, q, k and v (PKV_KV4: of the caches) */
 } pkv_cache_desc;
 
 /* Decode path selection and split-K partition size (NULL config = automatic: tensor
@@ -290,6 +291,50 @@ pkv_status paged_kv_gather(const void* k_cache, const void* v_cache, const int32
                            int32_t max_blocks_per_seq, const int32_t* context_lens,
                            int32_t num_seqs, int32_t max_context_len, void* k_out, void* v_out,
                            const pkv_cache_desc* cache, void* stream);
+
+/* ----------------------------------------------------------------------------------
+ * 4-bit caches.  The pages have no counterpart: a smaller form of the same cache, for more
+ * context in the same memory.
+ *
+ * A pool with dtype PKV_KV4 is [num_blocks][num_kv_heads][block_size][head_dim * 5 / 8]
+ * bytes (5 bits per value; 3.2 times the tokens of a 16-bit pool).  A row holds its D
+ * values as D / 2 bytes of codes -- byte i: value 2i in the low half, 2i + 1 in the high
+ * half -- and then D / 32 pairs (step, lo) of fp16, one for each group of 32 values.
+ * Code c of a group stands for fp16(lo + c * step), rounded once (to nearest even).
+ * paged_block_copy and paged_block_swap_out / _in take these pools like any other.
+ * ---------------------------------------------------------------------------------- */
+
+/*
+ * paged_kv4_append -- round new tokens' K and V to 4 bits and write them into their slots
+ * of a 4-bit pool (paged_kv_append for PKV_KV4 pools; same slots, same padding).
+ *
+ * k, v: device [num_tokens][num_kv_heads][head_dim] of kv_dtype (f32, f16 or bf16).  For
+ * each group x[0..31], all operations rounded to nearest even:
+ *   lo = fp16(min x), step = fp16(fp32(fp32(max x - lo) / 15)) (0 if negative),
+ *   code = fp32(x - lo) / step to the nearest integer (the quotient exact), held within
+ *   0..15; step 0 gives code 0.
+ * Values beyond +-65408 are stored as +-65408.  A group with a NaN or an infinity gets
+ * step = lo = NaN: all its 32 values read as NaN.
+ * Slots must be distinct (duplicates race); negative slots are skipped; a slot
+ * >= num_blocks * block_size sets the device index flag and is skipped.
+ */
+pkv_status paged_kv4_append(const void* k, const void* v, int32_t kv_dtype, const int64_t* slot_mapping,
+                            int32_t num_tokens, void* k_cache, void* v_cache, const pkv_cache_desc* cache,
+                            void* stream);
+
+/*
+ * paged_kv4_expand -- widen 4-bit blocks: block dst of the out pools becomes the values of
+ * block src of the 4-bit pools (all KV heads and rows), for each pair.  What
+ * paged_attention_prefill reads when earlier chunks are held in 4 bits.
+ *
+ * src_dst_pairs: device int64 [num_pairs][2]; destinations distinct (duplicates race).
+ * out_cache: the out pools' geometry; block_size, num_kv_heads and head_dim as cache's,
+ * dtype f32, f16 or bf16 (f32 and f16 hold the values exactly, bf16 rounds them to nearest
+ * even).  Out-of-range ids set the device index flag and are skipped.
+ */
+pkv_status paged_kv4_expand(const int64_t* src_dst_pairs, int32_t num_pairs, const void* k_cache,
+                            const void* v_cache, const pkv_cache_desc* cache, void* k_out, void* v_out,
+                            const pkv_cache_desc* out_cache, void* stream);
 
 /* ----------------------------------------------------------------------------------
  * Host block manager: which physical block every token lives in.

@@ -9,6 +9,11 @@ supplies device memory and the current stream.  The calls mirror the C ABI in
 * :func:`paged_attention_decode` -- single-token decode attention through block tables
 * :func:`paged_kv_gather`        -- the block-table gather alone (indexing checks)
 
+and, for caches held in 4 bits (uint8 pools, 5 bytes for 8 values):
+
+* :func:`paged_kv4_append`       -- new tokens' K/V rounded to 4 bits into their slots
+* :func:`paged_kv4_expand`       -- 4-bit blocks widened into blocks of another pool
+
 If the library has not been built the import still succeeds, but every call raises:
 there is no CPU fallback.
 """
@@ -27,6 +32,7 @@ __all__ = [
     "paged_attention_workspace_bytes", "paged_attention_decode_no_alloc", "paged_attention_no_alloc_limit",
     "paged_kv_gather", "paged_block_swap_out", "paged_block_swap_in", "paged_attention_prefill", "device_error", "declared_functions",
     "PATH_AUTO", "PATH_CUDA_CORE", "PATH_TENSOR_CORE",
+    "paged_kv4_append", "paged_kv4_expand",
     "PreparedCall", "prepare_kv_append", "prepare_block_copy", "prepare_attention_decode", "set_wait_limit",
 ]
 
@@ -34,7 +40,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libpagedkv.so")
 HEADER = os.path.join(os.path.dirname(_HERE), "include", "pagedkv.h")
 
-F32, F16, BF16 = 0, 1, 2
+F32, F16, BF16, KV4 = 0, 1, 2, 3
 DTYPE_CODE = {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}
 PATH_AUTO, PATH_CUDA_CORE, PATH_TENSOR_CORE = 0, 1, 2
 
@@ -93,6 +99,8 @@ def library():
             "paged_attention_plan": [i32, i32, i32, desc_p, cfg_p, ctypes.POINTER(DecodePlan)],
             "paged_attention_decode": [vp, vp, vp, vp, i32, vp, i32, i32, i32, ctypes.c_float, vp, i32,
                                        vp, sz, desc_p, cfg_p, vp],
+            "paged_kv4_append": [vp, vp, i32, vp, i32, vp, vp, desc_p, vp],
+            "paged_kv4_expand": [vp, i32, vp, vp, desc_p, vp, vp, desc_p, vp],
             "paged_kv_gather": [vp, vp, vp, i32, vp, i32, i32, vp, vp, desc_p, vp],
             "paged_block_swap_out": [vp, i32, vp, vp, vp, vp, desc_p, vp],
             "paged_attention_prefill": [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, i32,
@@ -141,10 +149,15 @@ def _need_cuda(*ts):
 
 
 def cache_desc(k_cache: torch.Tensor) -> CacheDesc:
-    """Descriptor of a pool shaped [num_blocks, num_kv_heads, block_size, head_dim]."""
+    """Descriptor of a pool shaped [num_blocks, num_kv_heads, block_size, head_dim], or of a
+    4-bit pool: uint8, [num_blocks, num_kv_heads, block_size, head_dim * 5 / 8]."""
     if k_cache.dim() != 4:
         raise PagedKVError(1, "cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
     nb, hkv, bs, d = k_cache.shape
+    if k_cache.dtype == torch.uint8:
+        if d % 5:
+            raise PagedKVError(1, "rows of a 4-bit pool hold head_dim * 5 / 8 bytes")
+        return CacheDesc(nb, bs, hkv, d // 5 * 8, KV4)
     if k_cache.dtype not in DTYPE_CODE:
         raise PagedKVError(2, f"cache dtype {k_cache.dtype}")
     return CacheDesc(nb, bs, hkv, d, DTYPE_CODE[k_cache.dtype])
@@ -431,6 +444,69 @@ def paged_kv_gather(k_cache, v_cache, block_tables, context_lens, k_out, v_out, 
     _check(library().paged_kv_gather(_ptr(k_cache), _ptr(v_cache), _ptr(block_tables), block_tables.shape[1],
                                      _ptr(context_lens), S, max_context_len, _ptr(k_out), _ptr(v_out),
                                      ctypes.byref(desc), _stream(k_cache)))
+
+
+# ---- 4-bit caches and eviction: the tensors of a call share one device, which need not be
+# the current one, and a workspace that is not given comes from PyTorch's allocator at every
+# call (ordered on the call's stream and, inside a capture, kept by the graph).
+
+
+def _one_device(*ts):
+    _need_cuda(*ts)
+    if len({t.device for t in ts if t is not None}) != 1:
+        raise PagedKVError(1, "tensors must be on one device")
+
+
+def _call(fn, tensor, *args) -> None:
+    """fn(*args, stream) with tensor's device current, on that device's current stream."""
+    if tensor.device.index == torch.cuda.current_device():
+        status = fn(*args, _stream(tensor))
+    else:
+        with torch.cuda.device(tensor.device):
+            status = fn(*args, _stream(tensor))
+    _check(status)
+
+
+def _kv4_desc(k_cache, v_cache) -> CacheDesc:
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8 or k_cache.shape != v_cache.shape:
+        raise PagedKVError(1, "the 4-bit pools must be uint8 and of one shape")
+    return cache_desc(k_cache)
+
+
+def _dtype_code(t, what) -> int:
+    code = DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise PagedKVError(2, f"{what} dtype {t.dtype}")
+    return code
+
+
+def paged_kv4_append(k, v, slot_mapping, k_cache, v_cache) -> None:
+    """k, v [T, Hkv, D] (f32, f16 or bf16) rounded to 4 bits -> the rows of the 4-bit pools
+    (uint8 [NB, Hkv, bs, D * 5 / 8]) given by slot_mapping (int64 [T]; negative: skipped)."""
+    _one_device(k, v, slot_mapping, k_cache, v_cache)
+    desc = _kv4_desc(k_cache, v_cache)
+    if slot_mapping.dtype != torch.int64 or v.dtype != k.dtype:
+        raise PagedKVError(1, "slot_mapping must be int64 and k and v of one dtype")
+    if k.shape != v.shape or k.dim() != 3 or k.shape[0] != slot_mapping.numel() \
+            or tuple(k.shape[1:]) != (desc.num_kv_heads, desc.head_dim):
+        raise PagedKVError(1, "shape mismatch between k, v, slot_mapping and the caches")
+    _call(library().paged_kv4_append, k_cache, _ptr(k), _ptr(v), _dtype_code(k, "k/v"), _ptr(slot_mapping),
+          slot_mapping.numel(), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc))
+
+
+def paged_kv4_expand(src_dst_pairs, k_cache, v_cache, k_out, v_out) -> None:
+    """Block dst of the pools k_out/v_out [NB', Hkv, bs, D] (f32, f16 or bf16) becomes the
+    values of block src of the 4-bit pools, for each row of src_dst_pairs (int64 [n, 2])."""
+    _one_device(src_dst_pairs, k_cache, v_cache, k_out, v_out)
+    desc = _kv4_desc(k_cache, v_cache)
+    if src_dst_pairs.dtype != torch.int64 or src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
+        raise PagedKVError(1, "src_dst_pairs must be int64 [n, 2]")
+    if v_out.dtype != k_out.dtype or v_out.shape != k_out.shape:
+        raise PagedKVError(1, "k_out and v_out must be of one dtype and shape")
+    _dtype_code(k_out, "out pool")
+    out_desc = cache_desc(k_out)
+    _call(library().paged_kv4_expand, k_cache, _ptr(src_dst_pairs), src_dst_pairs.shape[0], _ptr(k_cache),
+          _ptr(v_cache), ctypes.byref(desc), _ptr(k_out), _ptr(v_out), ctypes.byref(out_desc))
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:

@@ -7,6 +7,7 @@
 #include <mutex>
 #include <string>
 
+#include "api_util.h"
 #include "common.cuh"
 #include "launch.h"
 
@@ -18,6 +19,16 @@ namespace {
 __device__ int g_device_error;
 
 thread_local std::string t_last_error;
+
+// Bound of the decode and prefill kernels' pipeline waits (kWaitLimitNs unless a test
+// lowers it with paged_kv_set_wait_limit); read once per launch.
+std::atomic<uint64_t> g_wait_limit_ns{kWaitLimitNs};
+
+constexpr int kMaxDevices = 64;
+std::mutex g_flag_mutex;
+int* g_flag_ptr[kMaxDevices] = {};
+
+}  // namespace
 
 pkv_status fail(pkv_status st, const char* fmt, ...) {
   char buf[512];
@@ -33,15 +44,6 @@ pkv_status cuda_fail(cudaError_t e, const char* what) {
   return fail(PKV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
 
-// Bound of the decode and prefill kernels' pipeline waits (kWaitLimitNs unless a test
-// lowers it with paged_kv_set_wait_limit); read once per launch.
-std::atomic<uint64_t> g_wait_limit_ns{kWaitLimitNs};
-
-constexpr int kMaxDevices = 64;
-std::mutex g_flag_mutex;
-int* g_flag_ptr[kMaxDevices] = {};
-
-// Device address of g_device_error on the current device (looked up once per device).
 pkv_status device_flag(int** out) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -58,13 +60,9 @@ pkv_status device_flag(int** out) {
   return PKV_OK;
 }
 
-size_t elem_bytes(int dtype) { return dtype == PKV_F32 ? 4 : 2; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-pkv_status check_cache(const pkv_cache_desc* c) {
+pkv_status check_cache(const pkv_cache_desc* c, bool kv4) {
   if (!c) return fail(PKV_ERR_INVALID_ARG, "cache descriptor is NULL");
-  if (c->dtype < PKV_F32 || c->dtype > PKV_BF16)
+  if (c->dtype < PKV_F32 || c->dtype > (kv4 ? PKV_KV4 : PKV_BF16))
     return fail(PKV_ERR_UNSUPPORTED, "cache dtype %d", c->dtype);
   if (c->num_blocks <= 0 || c->num_kv_heads <= 0)
     return fail(PKV_ERR_INVALID_ARG, "num_blocks %d, num_kv_heads %d must be positive",
@@ -76,6 +74,8 @@ pkv_status check_cache(const pkv_cache_desc* c) {
   if (c->num_kv_heads > 65535) return fail(PKV_ERR_UNSUPPORTED, "num_kv_heads %d", c->num_kv_heads);
   return PKV_OK;
 }
+
+namespace {
 
 struct DecodePlan {
   int path;         // PKV_PATH_CUDA_CORE or PKV_PATH_TENSOR_CORE
@@ -241,7 +241,7 @@ pkv_status paged_kv_append(const void* k, const void* v, const int64_t* slot_map
 pkv_status paged_block_copy(const int64_t* src_dst_pairs, const int64_t* host_pairs,
                             int32_t num_pairs, void* k_cache, void* v_cache,
                             const pkv_cache_desc* cache, void* stream) {
-  if (pkv_status st = check_cache(cache)) return st;
+  if (pkv_status st = check_cache(cache, true)) return st;
   if (num_pairs < 0 || num_pairs > 65535)
     return fail(PKV_ERR_INVALID_ARG, "num_pairs %d outside [0, 65535]", num_pairs);
   if (num_pairs == 0) return PKV_OK;
@@ -268,9 +268,7 @@ pkv_status paged_block_copy(const int64_t* src_dst_pairs, const int64_t* host_pa
   }
   int* flag = nullptr;
   if (pkv_status st = device_flag(&flag)) return st;
-  const int64_t block_bytes = static_cast<int64_t>(cache->num_kv_heads) * cache->block_size *
-                              cache->head_dim * elem_bytes(cache->dtype);
-  cudaError_t e = launch_block_copy(src_dst_pairs, num_pairs, k_cache, v_cache, block_bytes,
+  cudaError_t e = launch_block_copy(src_dst_pairs, num_pairs, k_cache, v_cache, block_bytes(cache),
                                     cache->num_blocks, flag, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "block copy launch");
 }
@@ -314,7 +312,7 @@ pkv_status device_view(const void* host, void** out) {
 
 pkv_status swap(bool out, const int64_t* ids, int32_t n, void* k_cache, void* v_cache, const void* stage_k,
                 const void* stage_v, const pkv_cache_desc* cache, void* stream) {
-  if (pkv_status st = check_cache(cache)) return st;
+  if (pkv_status st = check_cache(cache, true)) return st;
   if (n < 0 || n > 65535) return fail(PKV_ERR_INVALID_ARG, "num_ids %d outside [0, 65535]", n);
   if (n == 0) return PKV_OK;
   if (!ids || !k_cache || !v_cache || !stage_k || !stage_v) return fail(PKV_ERR_INVALID_ARG, "NULL pointer argument");
@@ -325,9 +323,7 @@ pkv_status swap(bool out, const int64_t* ids, int32_t n, void* k_cache, void* v_
   if (pkv_status st = device_view(stage_v, &dv)) return st;
   int* flag = nullptr;
   if (pkv_status st = device_flag(&flag)) return st;
-  const int64_t block_bytes = static_cast<int64_t>(cache->num_kv_heads) * cache->block_size *
-                              cache->head_dim * elem_bytes(cache->dtype);
-  cudaError_t e = launch_swap(out, ids, n, k_cache, v_cache, dk, dv, block_bytes, cache->num_blocks, flag,
+  cudaError_t e = launch_swap(out, ids, n, k_cache, v_cache, dk, dv, block_bytes(cache), cache->num_blocks, flag,
                               static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "swap launch");
 }

@@ -95,4 +95,29 @@ cudaError_t launch_gather(const void* k_cache, const void* v_cache, const int32_
                           int32_t num_kv_heads, int32_t block_size, int32_t row_bytes,
                           int32_t num_blocks, int* err, cudaStream_t stream);
 
+// ---- 4-bit caches (PKV_KV4 pools)
+struct Kv4AppendParams {
+  const void* k;
+  const void* v;
+  const int64_t* slots;
+  void* k_cache;
+  void* v_cache;
+  int* err;
+  int64_t num_slots;
+  int32_t num_tokens, num_kv_heads, block_size, head_dim;
+};
+cudaError_t launch_kv4_append(const Kv4AppendParams& p, int dtype, cudaStream_t stream);
+
+struct Kv4ExpandParams {
+  const int64_t* pairs;
+  const void* k_cache;  // 4-bit pools
+  const void* v_cache;
+  void* k_out;  // pools of the wide dtype
+  void* v_out;
+  int* err;
+  int32_t num_pairs, num_blocks, num_out_blocks, num_kv_heads, block_size, head_dim;
+  int32_t pairs_per_cta;  // set by the launcher
+};
+cudaError_t launch_kv4_expand(Kv4ExpandParams p, int dtype, cudaStream_t stream);
+
 }  // namespace pkv
