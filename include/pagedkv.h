@@ -336,6 +336,30 @@ pkv_status paged_kv4_expand(const int64_t* src_dst_pairs, int32_t num_pairs, con
                             const void* v_cache, const pkv_cache_desc* cache, void* k_out, void* v_out,
                             const pkv_cache_desc* out_cache, void* stream);
 
+/*
+ * paged_attention_decode_kv4 -- single-token decode attention over a 4-bit pool:
+ * paged_attention_decode with K_j and V_j the values that the rows stand for.
+ *
+ * q: device [num_seqs][num_q_heads][head_dim] of q_dtype (f32, f16 or bf16); out: q's
+ * dtype or f32; query-head groups up to 16.  Softmax, sums and products in fp32: q in fp16
+ * (f32 q in two fp16 parts) after a power-of-two scaling of each head's row, weights in
+ * two fp16 parts, so the result is good to a few 2^-22 before the output's rounding.
+ * n == 0 gives zeros.  A NaN or infinity in a query row, or a NaN in a row attended to,
+ * gives NaN as the formula does.  partition_tokens: tokens per split-K partition, 0 =
+ * automatic (256 to 4096, aiming at eight CTAs per SM), else a multiple of 128 <= 16384.
+ * workspace: at least paged_attention_decode_kv4_workspace_bytes(...) bytes (0 when every
+ * sequence fits one partition), 256-byte aligned, one per call in flight.  The result does
+ * not depend on which physical blocks hold a sequence.  out must not alias any input.
+ */
+size_t paged_attention_decode_kv4_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
+                                                  const pkv_cache_desc* cache, int32_t partition_tokens);
+pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                      int32_t max_context_len, float scale, void* out, int32_t out_dtype,
+                                      void* workspace, size_t workspace_bytes, const pkv_cache_desc* cache,
+                                      int32_t partition_tokens, void* stream);
+
 /* ----------------------------------------------------------------------------------
  * Host block manager: which physical block every token lives in.
  * Pages: note-023, Method (allocate on demand as a sequence grows, free when it

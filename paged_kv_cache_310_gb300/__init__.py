@@ -13,6 +13,7 @@ and, for caches held in 4 bits (uint8 pools, 5 bytes for 8 values):
 
 * :func:`paged_kv4_append`       -- new tokens' K/V rounded to 4 bits into their slots
 * :func:`paged_kv4_expand`       -- 4-bit blocks widened into blocks of another pool
+* :func:`paged_attention_decode_kv4` -- single-token decode attention over a 4-bit pool
 
 If the library has not been built the import still succeeds, but every call raises:
 there is no CPU fallback.
@@ -32,7 +33,7 @@ __all__ = [
     "paged_attention_workspace_bytes", "paged_attention_decode_no_alloc", "paged_attention_no_alloc_limit",
     "paged_kv_gather", "paged_block_swap_out", "paged_block_swap_in", "paged_attention_prefill", "device_error", "declared_functions",
     "PATH_AUTO", "PATH_CUDA_CORE", "PATH_TENSOR_CORE",
-    "paged_kv4_append", "paged_kv4_expand",
+    "paged_kv4_append", "paged_kv4_expand", "paged_attention_decode_kv4", "paged_attention_decode_kv4_workspace_bytes",
     "PreparedCall", "prepare_kv_append", "prepare_block_copy", "prepare_attention_decode", "set_wait_limit",
 ]
 
@@ -100,6 +101,9 @@ def library():
             "paged_attention_decode": [vp, vp, vp, vp, i32, vp, i32, i32, i32, ctypes.c_float, vp, i32,
                                        vp, sz, desc_p, cfg_p, vp],
             "paged_kv4_append": [vp, vp, i32, vp, i32, vp, vp, desc_p, vp],
+            "paged_attention_decode_kv4_workspace_bytes": [i32, i32, i32, desc_p, i32],
+            "paged_attention_decode_kv4": [vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, ctypes.c_float, vp, i32,
+                                           vp, sz, desc_p, i32, vp],
             "paged_kv4_expand": [vp, i32, vp, vp, desc_p, vp, vp, desc_p, vp],
             "paged_kv_gather": [vp, vp, vp, i32, vp, i32, i32, vp, vp, desc_p, vp],
             "paged_block_swap_out": [vp, i32, vp, vp, vp, vp, desc_p, vp],
@@ -123,6 +127,7 @@ def library():
         lib.paged_attention_workspace_bytes.restype = sz
         lib.paged_attention_no_alloc_limit.restype = sz
         lib.paged_attention_prefill_workspace_bytes.restype = sz
+        lib.paged_attention_decode_kv4_workspace_bytes.restype = sz
         lib.paged_kv_last_error.restype = ctypes.c_char_p
         lib.paged_kv_version.restype = ctypes.c_char_p
         _lib = lib
@@ -507,6 +512,55 @@ def paged_kv4_expand(src_dst_pairs, k_cache, v_cache, k_out, v_out) -> None:
     out_desc = cache_desc(k_out)
     _call(library().paged_kv4_expand, k_cache, _ptr(src_dst_pairs), src_dst_pairs.shape[0], _ptr(k_cache),
           _ptr(v_cache), ctypes.byref(desc), _ptr(k_out), _ptr(v_out), ctypes.byref(out_desc))
+
+
+def _scratch(workspace, need: int, device):
+    """(pointer, bytes) of a call's workspace, and the tensor that holds it."""
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    return _ptr(workspace), nbytes, workspace
+
+
+def paged_attention_decode_kv4_workspace_bytes(num_seqs, num_q_heads, max_context_len, k_cache, *,
+                                               partition_tokens=0) -> int:
+    return int(library().paged_attention_decode_kv4_workspace_bytes(
+        num_seqs, num_q_heads, max_context_len, ctypes.byref(_kv4_desc(k_cache, k_cache)), partition_tokens))
+
+
+def paged_attention_decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out, *,
+                               max_context_len: int | None = None, workspace: torch.Tensor | None = None,
+                               partition_tokens: int = 0) -> torch.Tensor:
+    """out[s, h] = softmax(scale * q[s, h] . K_j) V_j over the context_lens[s] tokens of s, with
+    K and V held in 4-bit pools (uint8 [NB, Hkv, bs, D * 5 / 8]).
+
+    q [S, Hq, D] f32, f16 or bf16; block_tables int32 [S, max_blocks]; context_lens int32
+    [S]; out [S, Hq, D] in q's dtype or float32.  max_context_len: host upper bound on
+    context_lens (computed with a device sync when omitted).  workspace: uint8 device buffer
+    of paged_attention_decode_kv4_workspace_bytes, allocated for the call when omitted.
+    """
+    _one_device(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    desc = _kv4_desc(k_cache, v_cache)
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise PagedKVError(1, "block_tables and context_lens must be int32")
+    if q.dim() != 3 or out.shape != q.shape or q.shape[2] != desc.head_dim:
+        raise PagedKVError(1, "shape mismatch between q, out and the caches")
+    S, Hq, _ = q.shape
+    if context_lens.numel() != S or block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise PagedKVError(1, "block_tables must be [S, max_blocks] and context_lens [S]")
+    q_code, out_code = _dtype_code(q, "q"), _dtype_code(out, "out")
+    if max_context_len is None:
+        max_context_len = int(context_lens.max()) if S else 0
+    lib = library()
+    need = 0
+    if workspace is None:
+        need = int(lib.paged_attention_decode_kv4_workspace_bytes(S, Hq, max_context_len, ctypes.byref(desc),
+                                                                  partition_tokens))
+    ws, ws_bytes, workspace = _scratch(workspace, need, q.device)
+    _call(lib.paged_attention_decode_kv4, q, _ptr(q), q_code, _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+          block_tables.shape[1], _ptr(context_lens), S, Hq, max_context_len, float(scale), _ptr(out), out_code, ws,
+          ws_bytes, ctypes.byref(desc), partition_tokens)
+    return out
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:

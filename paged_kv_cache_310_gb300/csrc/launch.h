@@ -120,4 +120,9 @@ struct Kv4ExpandParams {
 };
 cudaError_t launch_kv4_expand(Kv4ExpandParams p, int dtype, cudaStream_t stream);
 
+// Single-token attention over 4-bit pools (head_dim 64/128, group <= 16); partitions are
+// merged by launch_merge.
+constexpr int kKv4MaxGroup = 16;
+cudaError_t launch_decode_kv4(const DecodeParams& p, int q_dtype, int out_dtype, cudaStream_t stream);
+
 }  // namespace pkv

@@ -41,8 +41,8 @@ def quantise(x) -> np.ndarray:
     out[:, :d // 2] = codes[:, 0::2] | (codes[:, 1::2] << 4)
     bits = pairs.view(np.uint16).copy()
     bits[np.isnan(pairs)] = 0x7E00
-    out[:, d // 2:] = bits.reshape(flat.shape[0], -1).view(np.uint8)
-    return out.reshape(*x.shape[:-1], -1)
+    out[:, d // 2:] = bits.reshape(flat.shape[0], d // 16).view(np.uint8)
+    return out.reshape(*x.shape[:-1], d * 5 // 8)
 
 
 def widen(rows) -> np.ndarray:
