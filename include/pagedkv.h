@@ -361,6 +361,63 @@ pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void
                                       int32_t partition_tokens, void* stream);
 
 /* ----------------------------------------------------------------------------------
+ * Eviction by accumulated attention weight.  The pages have no counterpart (they evict
+ * whole blocks of preempted sequences); this shortens a sequence in place of preempting it:
+ * the tokens that attention has used least leave, per KV head.
+ * ---------------------------------------------------------------------------------- */
+
+/*
+ * paged_attention_weights -- add a decode step's attention weights to per-token
+ * accumulators.  For every sequence s, KV head g and token j < n = context_lens[s]:
+ *   weights_out[s][g][j] = (j < tracked_lens[s] ? weights[s][g][j] : 0)
+ *                          + sum over g's query heads h of softmax_j(scale * q[s][h] . K_j).
+ * Rows j >= n are not written.  tracked_lens (device int32 [num_seqs], or NULL = every
+ * row): how many of a sequence's rows have an accumulator yet; the newer ones start at 0.
+ * weights, weights_out: device f32 [num_seqs][num_kv_heads][weights_width],
+ * weights_width >= max_context_len; they may be the same buffer.
+ * q: device [num_seqs][num_q_heads][head_dim] of q_dtype, which is the cache's dtype; a
+ * PKV_KV4 pool takes f32, f16 or bf16.  Query-head groups up to 16.  fp32 throughout
+ * (products of 16-bit operands are exact).  A sequence longer than max_context_len sets
+ * the device index flag and is skipped.  workspace: at least
+ * paged_attention_weights_workspace_bytes(...) bytes, 256-byte aligned, one per call in
+ * flight.
+ */
+size_t paged_attention_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
+                                               const pkv_cache_desc* cache);
+pkv_status paged_attention_weights(const void* q, int32_t q_dtype, const void* k_cache, const int32_t* block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                   const int32_t* tracked_lens, int32_t num_seqs, int32_t num_q_heads,
+                                   int32_t max_context_len, float scale, const float* weights, float* weights_out,
+                                   int64_t weights_width, void* workspace, size_t workspace_bytes,
+                                   const pkv_cache_desc* cache, void* stream);
+
+/*
+ * paged_kv_evict -- shorten sequences to the rows that matter.  For every sequence s and
+ * KV head g, of n = context_lens[s] rows k = min(keep_lens[s], n) are kept: the last
+ * r = min(recent, k), and of rows 0 .. n - r - 1 the k - r with the largest
+ * weights[s][g][j] (NaN counts as -infinity; equal weights: the lowest j first).  Kept rows
+ * keep their order: row i of the shortened sequence is row j = kept[s][g][i],
+ *   K/V row i of new_tables[s] = K/V row j of block_tables[s]  (bit-exact),
+ *   weights_out[s][g][i] = weights[s][g][j],   i < k;
+ * rows past k of kept, weights_out and the new blocks are not written, and the old blocks
+ * are left as they are (so shared blocks may be evicted from).  Attend to the result with
+ * new_tables and lengths k.  Heads choose on their own: K rows must carry their position
+ * (rotary embeddings applied before the append), since row numbers change.
+ *
+ * Pools of any dtype, PKV_KV4 too.  weights, weights_out: device f32
+ * [num_seqs][num_kv_heads][weights_width], not overlapping; kept: device int32
+ * [num_seqs][num_kv_heads][max_keep]; keep_lens: device int32 [num_seqs], k <= max_keep;
+ * new_tables: device int32 [num_seqs][max_new_blocks] of blocks that no listed sequence
+ * reads or shares (pkv_bm_compact gives them).  A sequence whose lengths break these bounds
+ * sets the device index flag and is skipped, as are rows with a block id out of range.
+ */
+pkv_status paged_kv_evict(const float* weights, float* weights_out, int64_t weights_width, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* keep_lens,
+                          int32_t recent, const int32_t* new_tables, int32_t max_new_blocks, int32_t num_seqs,
+                          int32_t max_context_len, int32_t max_keep, int32_t* kept, void* k_cache, void* v_cache,
+                          const pkv_cache_desc* cache, void* stream);
+
+/* ----------------------------------------------------------------------------------
  * Host block manager: which physical block every token lives in.
  * Pages: note-023, Method (allocate on demand as a sequence grows, free when it
  * finishes, share blocks between sequences with identical prefixes, copy on write when
@@ -423,6 +480,18 @@ pkv_status pkv_bm_swap_out(pkv_block_manager* manager, int64_t seq_id, int32_t* 
  * the pool cannot hold it (nothing changes). */
 pkv_status pkv_bm_swap_in(pkv_block_manager* manager, int64_t seq_id, int32_t* blocks_out, int32_t capacity,
                           int32_t* num_out);
+
+/*
+ * Eviction: the sequence gets ceil(new_len / block_size) fresh private blocks, listed in
+ * logical order in blocks_out (capacity entries, *num_out set), none of them one it held,
+ * and drops its references to the old ones (blocks nobody else holds become free).  Take
+ * its old table first; paged_kv_evict then moves the kept rows from there.  new_len at most
+ * its length.  The old blocks may be handed out again at once: issue the eviction before
+ * anything that writes to them on the same stream.  PKV_ERR_OUT_OF_BLOCKS if the pool
+ * cannot hold the fresh blocks beside the old ones (nothing changes).
+ */
+pkv_status pkv_bm_compact(pkv_block_manager* manager, int64_t seq_id, int64_t new_len, int32_t* blocks_out,
+                          int32_t capacity, int32_t* num_out);
 
 /* Rows of block_tables ([n][max_blocks], -1 padded) and context_lens for n sequences. */
 pkv_status pkv_bm_block_tables(const pkv_block_manager* manager, const int64_t* seq_ids, int32_t n,

@@ -123,6 +123,20 @@ class BlockManagerModel:
         self.add_sequence(seq, n)
         return list(self.tables[seq])
 
+    def compact(self, seq: int, new_len: int) -> list[int]:
+        """Evicted down to new_len tokens: fresh private blocks, then the old ones released."""
+        need = -(-new_len // self.block_size)
+        if need > len(self.free):
+            raise OutOfBlocks
+        fresh = []
+        for i in range(need):
+            b = self._take()
+            self.filled[b] = min(self.block_size, new_len - i * self.block_size)
+            fresh.append(b)
+        self.free_sequence(seq)
+        self.tables[seq], self.lens[seq] = fresh, new_len
+        return list(fresh)
+
     def stats(self) -> dict:
         used = [b for b in range(self.num_blocks) if self.refs[b] > 0]
         return dict(num_blocks=self.num_blocks, free_blocks=len(self.free), used_blocks=len(used),

@@ -15,6 +15,11 @@ and, for caches held in 4 bits (uint8 pools, 5 bytes for 8 values):
 * :func:`paged_kv4_expand`       -- 4-bit blocks widened into blocks of another pool
 * :func:`paged_attention_decode_kv4` -- single-token decode attention over a 4-bit pool
 
+and, to shorten sequences by what attention uses least:
+
+* :func:`paged_attention_weights` -- a decode step's attention weights, added per token
+* :func:`paged_kv_evict`         -- the heaviest and the most recent rows kept, in fresh blocks
+
 If the library has not been built the import still succeeds, but every call raises:
 there is no CPU fallback.
 """
@@ -34,6 +39,7 @@ __all__ = [
     "paged_kv_gather", "paged_block_swap_out", "paged_block_swap_in", "paged_attention_prefill", "device_error", "declared_functions",
     "PATH_AUTO", "PATH_CUDA_CORE", "PATH_TENSOR_CORE",
     "paged_kv4_append", "paged_kv4_expand", "paged_attention_decode_kv4", "paged_attention_decode_kv4_workspace_bytes",
+    "paged_attention_weights", "paged_attention_weights_workspace_bytes", "paged_kv_evict",
     "PreparedCall", "prepare_kv_append", "prepare_block_copy", "prepare_attention_decode", "set_wait_limit",
 ]
 
@@ -104,6 +110,10 @@ def library():
             "paged_attention_decode_kv4_workspace_bytes": [i32, i32, i32, desc_p, i32],
             "paged_attention_decode_kv4": [vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, ctypes.c_float, vp, i32,
                                            vp, sz, desc_p, i32, vp],
+            "paged_attention_weights_workspace_bytes": [i32, i32, i32, desc_p],
+            "paged_attention_weights": [vp, i32, vp, vp, i32, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp, i64, vp, sz,
+                                        desc_p, vp],
+            "paged_kv_evict": [vp, vp, i64, vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, vp, vp, vp, desc_p, vp],
             "paged_kv4_expand": [vp, i32, vp, vp, desc_p, vp, vp, desc_p, vp],
             "paged_kv_gather": [vp, vp, vp, i32, vp, i32, i32, vp, vp, desc_p, vp],
             "paged_block_swap_out": [vp, i32, vp, vp, vp, vp, desc_p, vp],
@@ -128,6 +138,7 @@ def library():
         lib.paged_attention_no_alloc_limit.restype = sz
         lib.paged_attention_prefill_workspace_bytes.restype = sz
         lib.paged_attention_decode_kv4_workspace_bytes.restype = sz
+        lib.paged_attention_weights_workspace_bytes.restype = sz
         lib.paged_kv_last_error.restype = ctypes.c_char_p
         lib.paged_kv_version.restype = ctypes.c_char_p
         _lib = lib
@@ -561,6 +572,87 @@ def paged_attention_decode_kv4(q, k_cache, v_cache, block_tables, context_lens, 
           block_tables.shape[1], _ptr(context_lens), S, Hq, max_context_len, float(scale), _ptr(out), out_code, ws,
           ws_bytes, ctypes.byref(desc), partition_tokens)
     return out
+
+
+def paged_attention_weights_workspace_bytes(num_seqs, num_q_heads, max_context_len, k_cache) -> int:
+    return int(library().paged_attention_weights_workspace_bytes(num_seqs, num_q_heads, max_context_len,
+                                                                 ctypes.byref(cache_desc(k_cache))))
+
+
+def paged_attention_weights(q, k_cache, block_tables, context_lens, scale, weights, *,
+                            weights_out: torch.Tensor | None = None, tracked_lens: torch.Tensor | None = None,
+                            max_context_len: int | None = None,
+                            workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """weights_out[s, g, j] = weights[s, g, j] + the softmax weights that the query heads of KV
+    head g give token j, for j < context_lens[s]; other rows are left as they are.
+
+    q [S, Hq, D] in the pool's dtype (a 4-bit pool takes f32, f16 or bf16); weights and
+    weights_out float32 [S, Hkv, W], W >= max_context_len; weights_out defaults to weights
+    (in place).  tracked_lens (int32 [S], optional): rows j >= tracked_lens[s] start at 0.
+    max_context_len: host upper bound on context_lens (computed with a device sync when
+    omitted).  workspace: uint8 device buffer, allocated for the call when omitted.
+    """
+    out = weights if weights_out is None else weights_out
+    _one_device(q, k_cache, block_tables, context_lens, weights, out, tracked_lens, workspace)
+    desc = cache_desc(k_cache)
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 \
+            or (tracked_lens is not None and tracked_lens.dtype != torch.int32):
+        raise PagedKVError(1, "block_tables, context_lens and tracked_lens must be int32")
+    if q.dim() != 3 or q.shape[2] != desc.head_dim:
+        raise PagedKVError(1, "q must be [S, Hq, D] with the cache's head_dim")
+    S, Hq, _ = q.shape
+    if context_lens.numel() != S or block_tables.dim() != 2 or block_tables.shape[0] != S \
+            or (tracked_lens is not None and tracked_lens.numel() != S):
+        raise PagedKVError(1, "block_tables must be [S, max_blocks], context_lens and tracked_lens [S]")
+    if weights.dtype != torch.float32 or out.dtype != torch.float32 or weights.dim() != 3 \
+            or out.shape != weights.shape or tuple(weights.shape[:2]) != (S, desc.num_kv_heads):
+        raise PagedKVError(1, "weights and weights_out must be float32 [S, Hkv, W]")
+    q_code = _dtype_code(q, "q")
+    if max_context_len is None:
+        max_context_len = int(context_lens.max()) if S else 0
+    lib = library()
+    need = 0
+    if workspace is None:
+        need = int(lib.paged_attention_weights_workspace_bytes(S, Hq, max_context_len, ctypes.byref(desc)))
+    ws, ws_bytes, workspace = _scratch(workspace, need, q.device)
+    _call(lib.paged_attention_weights, q, _ptr(q), q_code, _ptr(k_cache), _ptr(block_tables), block_tables.shape[1],
+          _ptr(context_lens), _ptr(tracked_lens), S, Hq, max_context_len, float(scale), _ptr(weights), _ptr(out),
+          weights.shape[2], ws, ws_bytes, ctypes.byref(desc))
+    return out
+
+
+def paged_kv_evict(weights, block_tables, context_lens, keep_lens, new_tables, k_cache, v_cache, weights_out, kept, *,
+                   recent: int = 0, max_context_len: int | None = None) -> None:
+    """Shorten each sequence to k = min(keep_lens[s], context_lens[s]) rows: per KV head, the
+    last min(recent, k) and the heaviest others (ties: lowest row first), in order, moved
+    into the blocks of new_tables (int32 [S, max_new_blocks]; blocks that no listed sequence
+    reads).  kept[s, g, i] is the row that became row i, weights_out[s, g, i] its weight;
+    places past k are left as they are.
+
+    weights, weights_out float32 [S, Hkv, W] (not overlapping); kept int32 [S, Hkv,
+    max_keep]; block_tables, context_lens, keep_lens int32; the pools are of any dtype.
+    max_context_len: host upper bound on context_lens (computed with a device sync when
+    omitted).
+    """
+    _one_device(weights, block_tables, context_lens, keep_lens, new_tables, k_cache, v_cache, weights_out, kept)
+    desc = cache_desc(k_cache)
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise PagedKVError(1, "the caches must be of one shape and dtype")
+    for t in (block_tables, context_lens, keep_lens, new_tables, kept):
+        if t.dtype != torch.int32:
+            raise PagedKVError(1, "block_tables, context_lens, keep_lens, new_tables and kept must be int32")
+    S, heads = context_lens.numel(), desc.num_kv_heads
+    if keep_lens.numel() != S or block_tables.dim() != 2 or block_tables.shape[0] != S or new_tables.dim() != 2 \
+            or new_tables.shape[0] != S or kept.dim() != 3 or tuple(kept.shape[:2]) != (S, heads):
+        raise PagedKVError(1, "tables must be [S, blocks], lengths [S] and kept [S, Hkv, max_keep]")
+    if weights.dtype != torch.float32 or weights_out.dtype != torch.float32 or weights.dim() != 3 \
+            or weights_out.shape != weights.shape or tuple(weights.shape[:2]) != (S, heads):
+        raise PagedKVError(1, "weights and weights_out must be float32 [S, Hkv, W]")
+    if max_context_len is None:
+        max_context_len = int(context_lens.max()) if S else 0
+    _call(library().paged_kv_evict, k_cache, _ptr(weights), _ptr(weights_out), weights.shape[2], _ptr(block_tables),
+          block_tables.shape[1], _ptr(context_lens), _ptr(keep_lens), recent, _ptr(new_tables), new_tables.shape[1], S,
+          max_context_len, kept.shape[2], _ptr(kept), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc))
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:

@@ -38,9 +38,10 @@ def _lib():
         lib.pkv_bm_stats.argtypes = [vp, ctypes.POINTER(BlockStats)]
         lib.pkv_bm_swap_out.argtypes = [vp, i64, vp, i32, ctypes.POINTER(i32)]
         lib.pkv_bm_swap_in.argtypes = [vp, i64, vp, i32, ctypes.POINTER(i32)]
+        lib.pkv_bm_compact.argtypes = [vp, i64, i64, vp, i32, ctypes.POINTER(i32)]
         for n in ("pkv_bm_create", "pkv_bm_add_sequence", "pkv_bm_fork", "pkv_bm_append",
                   "pkv_bm_free_sequence", "pkv_bm_block_tables", "pkv_bm_stats", "pkv_bm_swap_out",
-                  "pkv_bm_swap_in"):
+                  "pkv_bm_swap_in", "pkv_bm_compact"):
             getattr(lib, n).restype = ctypes.c_int
         lib._bm_bound = True
     return lib
@@ -101,6 +102,15 @@ class BlockManager:
     def swap_in(self, seq_id: int) -> list:
         """Restore into fresh blocks (copy the data back with paged_block_swap_in)."""
         return self._blocks_call(self._lib.pkv_bm_swap_in, seq_id)
+
+    def compact(self, seq_id: int, new_len: int) -> list:
+        """Evict down to new_len tokens: the sequence's fresh blocks (take its old table first,
+        then move the kept rows with paged_kv_evict); the old blocks are released."""
+        cap = self.num_blocks
+        out = torch.empty(cap, dtype=torch.int32)
+        n = ctypes.c_int32(0)
+        _check(self._lib.pkv_bm_compact(self._h, seq_id, new_len, out.data_ptr(), cap, ctypes.byref(n)))
+        return out[:n.value].tolist()
 
     def block_tables(self, seq_ids, max_blocks: int | None = None):
         """(block_tables int32 [n, max_blocks] padded with -1, context_lens int32 [n])."""

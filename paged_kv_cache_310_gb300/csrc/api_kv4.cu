@@ -76,6 +76,34 @@ pkv_status check_table_width(int32_t max_blocks, int32_t tokens, int32_t block_s
   return PKV_OK;
 }
 
+struct WeightsPlan {
+  int part_tokens, max_parts;
+  size_t ml_bytes, workspace;
+};
+
+// Partitions of the scores kernel: about twelve CTAs per SM, of 256 to 2,048 tokens.
+pkv_status plan_weights(int32_t num_seqs, int32_t num_q_heads, int32_t max_len, const pkv_cache_desc* c,
+                        WeightsPlan* plan) {
+  if (pkv_status st = check_cache(c, true)) return st;
+  if (num_seqs < 0 || num_seqs > 65535) return fail(PKV_ERR_INVALID_ARG, "num_seqs %d outside [0, 65535]", num_seqs);
+  if (num_q_heads <= 0 || num_q_heads % c->num_kv_heads)
+    return fail(PKV_ERR_INVALID_ARG, "num_q_heads %d is not a positive multiple of num_kv_heads %d", num_q_heads,
+                c->num_kv_heads);
+  if (num_q_heads / c->num_kv_heads > kWeightsMaxGroup)
+    return fail(PKV_ERR_UNSUPPORTED, "attention weights support query-head groups <= %d (group %d)", kWeightsMaxGroup,
+                num_q_heads / c->num_kv_heads);
+  if (max_len < 0) return fail(PKV_ERR_INVALID_ARG, "max_context_len %d < 0", max_len);
+  if (max_len > (1 << 30)) return fail(PKV_ERR_UNSUPPORTED, "max_context_len %d above 2^30", max_len);
+  const int64_t work = static_cast<int64_t>(num_seqs) * c->num_kv_heads * (max_len / 2 + 1);
+  const int64_t per_cta = work / (12 * 152) + 1;
+  plan->part_tokens = static_cast<int>(per_cta < 256 ? 256 : per_cta > 2048 ? 2048 : (per_cta + 127) / 128 * 128);
+  plan->max_parts = max_len == 0 ? 1 : (max_len + plan->part_tokens - 1) / plan->part_tokens;
+  const size_t heads = static_cast<size_t>(num_seqs) * num_q_heads;
+  plan->ml_bytes = (heads * plan->max_parts * 2 * sizeof(float) + 255) / 256 * 256;
+  plan->workspace = num_seqs == 0 || max_len == 0 ? 0 : plan->ml_bytes + heads * max_len * sizeof(float);
+  return PKV_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -201,6 +229,123 @@ pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void
   if (e != cudaSuccess) return cuda_fail(e, "4-bit decode launch");
   e = launch_merge(p, out_dtype, s);
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "merge launch");
+}
+
+size_t paged_attention_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
+                                               const pkv_cache_desc* cache) {
+  WeightsPlan plan;
+  if (plan_weights(num_seqs, num_q_heads, max_context_len, cache, &plan) != PKV_OK) return 0;
+  return plan.workspace;
+}
+
+pkv_status paged_attention_weights(const void* q, int32_t q_dtype, const void* k_cache, const int32_t* block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t* context_lens,
+                                   const int32_t* tracked_lens, int32_t num_seqs, int32_t num_q_heads,
+                                   int32_t max_context_len, float scale, const float* weights, float* weights_out,
+                                   int64_t weights_width, void* workspace, size_t workspace_bytes,
+                                   const pkv_cache_desc* cache, void* stream) {
+  WeightsPlan plan;
+  if (pkv_status st = plan_weights(num_seqs, num_q_heads, max_context_len, cache, &plan)) return st;
+  if (!is_wide(q_dtype)) return fail(PKV_ERR_UNSUPPORTED, "q dtype %d", q_dtype);
+  if (cache->dtype != PKV_KV4 && q_dtype != cache->dtype)
+    return fail(PKV_ERR_INVALID_ARG, "q dtype %d differs from the cache's %d", q_dtype, cache->dtype);
+  if (num_seqs == 0 || max_context_len == 0) return PKV_OK;
+  if (!q || !k_cache || !block_tables || !context_lens || !weights || !weights_out)
+    return fail(PKV_ERR_INVALID_ARG, "NULL pointer argument");
+  if (!aligned16(q) || !aligned16(k_cache)) return fail(PKV_ERR_INVALID_ARG, "q and the cache must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(weights_out)) & 3u)
+    return fail(PKV_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+  if (!std::isfinite(scale)) return fail(PKV_ERR_INVALID_ARG, "scale is not finite");
+  if (weights_width < max_context_len)
+    return fail(PKV_ERR_INVALID_ARG, "weights_width %lld < max_context_len %d", static_cast<long long>(weights_width),
+                max_context_len);
+  if (pkv_status st = check_table_width(max_blocks_per_seq, max_context_len, cache->block_size, "max_blocks_per_seq"))
+    return st;
+  if (pkv_status st = check_workspace(workspace, workspace_bytes, plan.workspace)) return st;
+  int* flag = nullptr;
+  if (pkv_status st = device_flag(&flag)) return st;
+  WeightsParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.tracked_lens = tracked_lens;
+  p.weights = weights;
+  p.weights_out = weights_out;
+  p.ws_ml = static_cast<float*>(workspace);
+  p.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.ml_bytes);
+  p.err = flag;
+  p.width = weights_width;
+  p.q_dtype = q_dtype;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.group = num_q_heads / cache->num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.block_size = cache->block_size;
+  p.num_blocks = cache->num_blocks;
+  p.head_dim = cache->head_dim;
+  p.max_len = max_context_len;
+  p.part_tokens = plan.part_tokens;
+  p.max_parts = plan.max_parts;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  cudaError_t e = launch_weights(p, cache->dtype, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "attention weights launch");
+}
+
+pkv_status paged_kv_evict(const float* weights, float* weights_out, int64_t weights_width, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* keep_lens,
+                          int32_t recent, const int32_t* new_tables, int32_t max_new_blocks, int32_t num_seqs,
+                          int32_t max_context_len, int32_t max_keep, int32_t* kept, void* k_cache, void* v_cache,
+                          const pkv_cache_desc* cache, void* stream) {
+  if (pkv_status st = check_cache(cache, true)) return st;
+  if (num_seqs < 0 || num_seqs > 65535) return fail(PKV_ERR_INVALID_ARG, "num_seqs %d outside [0, 65535]", num_seqs);
+  if (max_context_len < 0 || max_keep < 0 || recent < 0)
+    return fail(PKV_ERR_INVALID_ARG, "max_context_len %d, max_keep %d, recent %d: none may be negative", max_context_len,
+                max_keep, recent);
+  if (max_context_len > (1 << 30)) return fail(PKV_ERR_UNSUPPORTED, "max_context_len %d above 2^30", max_context_len);
+  if (num_seqs == 0 || max_context_len == 0) return PKV_OK;
+  if (!weights || !weights_out || !block_tables || !context_lens || !keep_lens || !k_cache || !v_cache ||
+      (max_keep > 0 && (!new_tables || !kept)))
+    return fail(PKV_ERR_INVALID_ARG, "NULL pointer argument");
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return fail(PKV_ERR_INVALID_ARG, "the caches must be 16-byte aligned");
+  if (weights_width < max_context_len)
+    return fail(PKV_ERR_INVALID_ARG, "weights_width %lld < max_context_len %d", static_cast<long long>(weights_width),
+                max_context_len);
+  const uintptr_t a = reinterpret_cast<uintptr_t>(weights), b = reinterpret_cast<uintptr_t>(weights_out);
+  const size_t bytes = static_cast<size_t>(num_seqs) * cache->num_kv_heads * weights_width * sizeof(float);
+  if ((a | b) & 3u) return fail(PKV_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+  if (a < b + bytes && b < a + bytes) return fail(PKV_ERR_INVALID_ARG, "weights_out overlaps weights");
+  if (pkv_status st = check_table_width(max_blocks_per_seq, max_context_len, cache->block_size, "max_blocks_per_seq"))
+    return st;
+  const int32_t most = max_keep < max_context_len ? max_keep : max_context_len;  // rows a sequence may keep
+  if (pkv_status st = check_table_width(max_new_blocks, most, cache->block_size, "max_new_blocks")) return st;
+  int* flag = nullptr;
+  if (pkv_status st = device_flag(&flag)) return st;
+  EvictParams p{};
+  p.weights = weights;
+  p.weights_out = weights_out;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.keep_lens = keep_lens;
+  p.new_tables = new_tables;
+  p.kept = kept;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.err = flag;
+  p.width = weights_width;
+  p.num_seqs = num_seqs;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.max_new_blocks = max_new_blocks;
+  p.block_size = cache->block_size;
+  p.num_blocks = cache->num_blocks;
+  p.row_bytes = static_cast<int32_t>(row_bytes(cache));
+  p.max_len = max_context_len;
+  p.max_keep = max_keep;
+  p.recent = recent;
+  cudaError_t e = launch_evict(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "evict launch");
 }
 
 }  // extern "C"

@@ -217,6 +217,32 @@ pkv_status pkv_bm_swap_in(pkv_block_manager* m, int64_t seq_id, int32_t* blocks_
   return PKV_OK;
 }
 
+pkv_status pkv_bm_compact(pkv_block_manager* m, int64_t seq_id, int64_t new_len, int32_t* blocks_out, int32_t capacity,
+                          int32_t* num_out) {
+  if (!m || !num_out) return err(PKV_ERR_INVALID_ARG, "NULL argument");
+  auto it = m->seqs.find(seq_id);
+  if (it == m->seqs.end()) return err(PKV_ERR_INVALID_ARG, "unknown (or swapped) sequence id");
+  auto& s = it->second;
+  if (new_len < 0 || new_len > s.len) return err(PKV_ERR_INVALID_ARG, "new_len outside 0 .. the sequence's length");
+  const int64_t need = blocks_for(new_len, m->block_size);
+  if (need > capacity || (need > 0 && !blocks_out)) return err(PKV_ERR_INVALID_ARG, "blocks_out too small");
+  if (need > static_cast<int64_t>(m->free_stack.size()))
+    return err(PKV_ERR_OUT_OF_BLOCKS, "not enough free blocks for the shortened sequence");
+  // the fresh blocks first, so that none of them is an old one; need <= the number of old
+  // blocks, so their list takes the fresh ones without growing, and the pushes onto the free
+  // stack stay within the capacity it was created with: nothing here allocates or throws
+  for (int64_t i = 0; i < need; ++i) blocks_out[i] = take_block(m);
+  for (auto b = s.blocks.rbegin(); b != s.blocks.rend(); ++b) release_block(m, *b);
+  s.blocks.resize(static_cast<size_t>(need));
+  for (int64_t i = 0; i < need; ++i) {
+    s.blocks[i] = blocks_out[i];
+    m->filled[blocks_out[i]] = static_cast<int32_t>(std::min<int64_t>(m->block_size, new_len - i * m->block_size));
+  }
+  s.len = new_len;
+  *num_out = static_cast<int32_t>(need);
+  return PKV_OK;
+}
+
 pkv_status pkv_bm_block_tables(const pkv_block_manager* m, const int64_t* seq_ids, int32_t n,
                                int32_t max_blocks, int32_t* tables, int32_t* lens) {
   if (!m || (n > 0 && (!seq_ids || !tables || !lens))) return err(PKV_ERR_INVALID_ARG, "NULL argument");

@@ -125,4 +125,41 @@ cudaError_t launch_kv4_expand(Kv4ExpandParams p, int dtype, cudaStream_t stream)
 constexpr int kKv4MaxGroup = 16;
 cudaError_t launch_decode_kv4(const DecodeParams& p, int q_dtype, int out_dtype, cudaStream_t stream);
 
+// ---- attention weights and eviction
+struct WeightsParams {
+  const void* q;
+  const void* k_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* tracked_lens;  // NULL: every row has an accumulator
+  const float* weights;         // [S][Hkv][width]
+  float* weights_out;           // may be weights
+  float* scores;                // workspace [S][Hkv][max_len][G]: log2-domain scores
+  float* ws_ml;                 // workspace [S][Hq][max_parts][2]
+  int* err;
+  int64_t width;
+  int32_t q_dtype, num_seqs, num_q_heads, num_kv_heads, group, max_blocks_per_seq;
+  int32_t block_size, num_blocks, head_dim, max_len, part_tokens, max_parts;
+  float scale_log2;
+};
+constexpr int kWeightsMaxGroup = 16;
+cudaError_t launch_weights(const WeightsParams& p, int dtype, cudaStream_t stream);
+
+struct EvictParams {
+  const float* weights;  // [S][Hkv][width]
+  float* weights_out;    // same shape
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* keep_lens;
+  const int32_t* new_tables;
+  int32_t* kept;  // [S][Hkv][max_keep]
+  void* k_cache;
+  void* v_cache;
+  int* err;
+  int64_t width;
+  int32_t num_seqs, num_kv_heads, max_blocks_per_seq, max_new_blocks;
+  int32_t block_size, num_blocks, row_bytes, max_len, max_keep, recent;
+};
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+
 }  // namespace pkv
