@@ -10,6 +10,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "launch.h"
 
 namespace pkv {
 
@@ -24,30 +25,31 @@ struct Kv4Row {
   static constexpr int kCodes = D / 2;  // bytes of codes; the (step, lo) pairs follow
 };
 
-__device__ __forceinline__ uint32_t lop_and_or(uint32_t a, uint32_t mask, uint32_t bits) {
-  return (a & mask) | bits;  // one lop3
-}
-
 __device__ __forceinline__ __half2 as_half2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 __device__ __forceinline__ uint32_t as_u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
-// The exact integers of half-bytes 0 and 4 (bits 0-3 and 16-19) of w as fp16: 0x6400 is
-// 1024, whose last bits are units.
-__device__ __forceinline__ __half2 low_codes(uint32_t w) {
-  return __hsub2(as_half2(lop_and_or(w, 0x000f000fu, 0x64006400u)), as_half2(0x64006400u));
+__device__ __forceinline__ uint32_t and_or(uint32_t w, uint32_t mask, uint32_t bits) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(bits));
+  return d;
+}
+
+// The exact integers of half-bytes 0 and 4 (bits 0-3 and 16-19) of w as fp16.
+__device__ __forceinline__ __half2 low_codes(uint32_t w, const Kv4Bits& k) {
+  return __hsub2(as_half2(and_or(w, k.low, k.one)), as_half2(0x64006400u));
 }
 // ... of half-bytes 1 and 5 (bits 4-7 and 20-23): 1024 + 16 c, times 1/16, minus 64 (exact).
-__device__ __forceinline__ __half2 high_codes(uint32_t w) {
-  return __hfma2(as_half2(lop_and_or(w, 0x00f000f0u, 0x64006400u)), as_half2(0x2c002c00u), as_half2(0xd400d400u));
+__device__ __forceinline__ __half2 high_codes(uint32_t w, const Kv4Bits& k) {
+  return __hfma2(as_half2(and_or(w, k.high, k.one)), as_half2(0x2c002c00u), as_half2(0xd400d400u));
 }
 
 // The eight values of a word of codes: out[i] = (value i, value i + 4).
-__device__ __forceinline__ void kv4_word(uint32_t w, __half2 step, __half2 lo, uint32_t (&out)[4]) {
-  out[0] = as_u32(__hfma2(low_codes(w), step, lo));
-  out[1] = as_u32(__hfma2(high_codes(w), step, lo));
+__device__ __forceinline__ void kv4_word(uint32_t w, __half2 step, __half2 lo, const Kv4Bits& k, uint32_t (&out)[4]) {
+  out[0] = as_u32(__hfma2(low_codes(w, k), step, lo));
+  out[1] = as_u32(__hfma2(high_codes(w, k), step, lo));
   w >>= 8;
-  out[2] = as_u32(__hfma2(low_codes(w), step, lo));
-  out[3] = as_u32(__hfma2(high_codes(w), step, lo));
+  out[2] = as_u32(__hfma2(low_codes(w, k), step, lo));
+  out[3] = as_u32(__hfma2(high_codes(w, k), step, lo));
 }
 
 // Eight values of one group, held by four neighbouring lanes with eight each: returns the

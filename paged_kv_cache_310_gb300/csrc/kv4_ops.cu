@@ -121,9 +121,9 @@ __global__ void __launch_bounds__(kThreads) kv4_expand_kernel(const __grid_const
     const __half2 pv = as_half2(static_cast<const uint32_t*>(p.v_cache)[pair]);
     const int64_t to = (dst * rows + row) * p.head_dim + c * 8;
     uint32_t out[4];
-    kv4_word(wk, __low2half2(pk), __high2half2(pk), out);
+    kv4_word(wk, __low2half2(pk), __high2half2(pk), p.bits, out);
     store8(static_cast<T*>(p.k_out) + to, out);
-    kv4_word(wv, __low2half2(pv), __high2half2(pv), out);
+    kv4_word(wv, __low2half2(pv), __high2half2(pv), p.bits, out);
     store8(static_cast<T*>(p.v_out) + to, out);
   }
 }

@@ -96,6 +96,16 @@ cudaError_t launch_gather(const void* k_cache, const void* v_cache, const int32_
                           int32_t num_blocks, int* err, cudaStream_t stream);
 
 // ---- 4-bit caches (PKV_KV4 pools)
+
+// The bit patterns that widening 4-bit codes uses.  Kernels get them as an argument: as
+// literals the assembler splits (w & mask) | bits into two instructions (a lop3 takes one
+// literal), and the integer pipe is what widening is bound by.
+struct Kv4Bits {
+  uint32_t low = 0x000f000fu;   // half-bytes 0 and 4 of a word
+  uint32_t high = 0x00f000f0u;  // half-bytes 1 and 5
+  uint32_t one = 0x64006400u;   // fp16 1024, whose last bits are units, twice
+};
+
 struct Kv4AppendParams {
   const void* k;
   const void* v;
@@ -117,6 +127,7 @@ struct Kv4ExpandParams {
   int* err;
   int32_t num_pairs, num_blocks, num_out_blocks, num_kv_heads, block_size, head_dim;
   int32_t pairs_per_cta;  // set by the launcher
+  Kv4Bits bits;
 };
 cudaError_t launch_kv4_expand(Kv4ExpandParams p, int dtype, cudaStream_t stream);
 
@@ -141,6 +152,7 @@ struct WeightsParams {
   int32_t q_dtype, num_seqs, num_q_heads, num_kv_heads, group, max_blocks_per_seq;
   int32_t block_size, num_blocks, head_dim, max_len, part_tokens, max_parts;
   float scale_log2;
+  Kv4Bits bits;
 };
 constexpr int kWeightsMaxGroup = 16;
 cudaError_t launch_weights(const WeightsParams& p, int dtype, cudaStream_t stream);

@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
           const int pair = D / 2 + 4 * (t * D / 128), word = t * (D / 8) + 4 * i;
           const __half2 p0 = *reinterpret_cast<const __half2*>(r0 + pair);
           const __half2 p1 = *reinterpret_cast<const __half2*>(r0 + C::kHalf + pair);
-          kv4_word(*reinterpret_cast<const uint32_t*>(r0 + word), __low2half2(p0), __high2half2(p0), a);
-          kv4_word(*reinterpret_cast<const uint32_t*>(r0 + C::kHalf + word), __low2half2(p1), __high2half2(p1), b);
+          kv4_word(*reinterpret_cast<const uint32_t*>(r0 + word), __low2half2(p0), __high2half2(p0), p.bits, a);
+          kv4_word(*reinterpret_cast<const uint32_t*>(r0 + C::kHalf + word), __low2half2(p1), __high2half2(p1), p.bits, b);
         } else {
           const uint4 v0 = *reinterpret_cast<const uint4*>(ks + C::place(g * C::kRowChunks + t + 4 * i));
           const uint4 v1 = *reinterpret_cast<const uint4*>(ks + C::place((g + 8) * C::kRowChunks + t + 4 * i));
