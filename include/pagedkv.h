@@ -345,20 +345,22 @@ pkv_status paged_kv4_expand(const int64_t* src_dst_pairs, int32_t num_pairs, con
  * (f32 q in two fp16 parts) after a power-of-two scaling of each head's row, weights in
  * two fp16 parts, so the result is good to a few 2^-22 before the output's rounding.
  * n == 0 gives zeros.  A NaN or infinity in a query row, or a NaN in a row attended to,
- * gives NaN as the formula does.  partition_tokens: tokens per split-K partition, 0 =
- * automatic (256 to 4096, aiming at eight CTAs per SM), else a multiple of 128 <= 16384.
- * workspace: at least paged_attention_decode_kv4_workspace_bytes(...) bytes (0 when every
- * sequence fits one partition), 256-byte aligned, one per call in flight.  The result does
- * not depend on which physical blocks hold a sequence.  out must not alias any input.
+ * gives NaN as the formula does.  A sequence longer than max_context_len sets the device
+ * index flag and is skipped.  The batch's tokens are shared out evenly among the CTAs,
+ * whatever the lengths; sequences that cross a CTA's share are joined by a second kernel.
+ * workspace: at least paged_attention_decode_kv4_workspace_bytes(...) bytes (0 when
+ * max_context_len <= 128), 256-byte aligned, one per call in flight; its size does not grow
+ * with the batch or the lengths past a limit of some 20 MB.  The result does not depend on
+ * which physical blocks hold a sequence.  out must not alias any input.
  */
 size_t paged_attention_decode_kv4_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
-                                                  const pkv_cache_desc* cache, int32_t partition_tokens);
+                                                  int32_t q_dtype, const pkv_cache_desc* cache);
 pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
                                       const int32_t* block_tables, int32_t max_blocks_per_seq,
                                       const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
                                       int32_t max_context_len, float scale, void* out, int32_t out_dtype,
                                       void* workspace, size_t workspace_bytes, const pkv_cache_desc* cache,
-                                      int32_t partition_tokens, void* stream);
+                                      void* stream);
 
 /* ----------------------------------------------------------------------------------
  * Eviction by accumulated attention weight.  The pages have no counterpart (they evict

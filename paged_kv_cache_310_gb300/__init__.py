@@ -107,9 +107,9 @@ def library():
             "paged_attention_decode": [vp, vp, vp, vp, i32, vp, i32, i32, i32, ctypes.c_float, vp, i32,
                                        vp, sz, desc_p, cfg_p, vp],
             "paged_kv4_append": [vp, vp, i32, vp, i32, vp, vp, desc_p, vp],
-            "paged_attention_decode_kv4_workspace_bytes": [i32, i32, i32, desc_p, i32],
+            "paged_attention_decode_kv4_workspace_bytes": [i32, i32, i32, i32, desc_p],
             "paged_attention_decode_kv4": [vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, ctypes.c_float, vp, i32,
-                                           vp, sz, desc_p, i32, vp],
+                                           vp, sz, desc_p, vp],
             "paged_attention_weights_workspace_bytes": [i32, i32, i32, desc_p],
             "paged_attention_weights": [vp, i32, vp, vp, i32, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp, i64, vp, sz,
                                         desc_p, vp],
@@ -533,15 +533,15 @@ def _scratch(workspace, need: int, device):
     return _ptr(workspace), nbytes, workspace
 
 
-def paged_attention_decode_kv4_workspace_bytes(num_seqs, num_q_heads, max_context_len, k_cache, *,
-                                               partition_tokens=0) -> int:
+def paged_attention_decode_kv4_workspace_bytes(num_seqs, num_q_heads, max_context_len, q_dtype, k_cache) -> int:
+    """q_dtype: torch.float32, torch.float16 or torch.bfloat16."""
     return int(library().paged_attention_decode_kv4_workspace_bytes(
-        num_seqs, num_q_heads, max_context_len, ctypes.byref(_kv4_desc(k_cache, k_cache)), partition_tokens))
+        num_seqs, num_q_heads, max_context_len, DTYPE_CODE[q_dtype], ctypes.byref(_kv4_desc(k_cache, k_cache))))
 
 
 def paged_attention_decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out, *,
-                               max_context_len: int | None = None, workspace: torch.Tensor | None = None,
-                               partition_tokens: int = 0) -> torch.Tensor:
+                               max_context_len: int | None = None,
+                               workspace: torch.Tensor | None = None) -> torch.Tensor:
     """out[s, h] = softmax(scale * q[s, h] . K_j) V_j over the context_lens[s] tokens of s, with
     K and V held in 4-bit pools (uint8 [NB, Hkv, bs, D * 5 / 8]).
 
@@ -565,12 +565,11 @@ def paged_attention_decode_kv4(q, k_cache, v_cache, block_tables, context_lens, 
     lib = library()
     need = 0
     if workspace is None:
-        need = int(lib.paged_attention_decode_kv4_workspace_bytes(S, Hq, max_context_len, ctypes.byref(desc),
-                                                                  partition_tokens))
+        need = int(lib.paged_attention_decode_kv4_workspace_bytes(S, Hq, max_context_len, q_code, ctypes.byref(desc)))
     ws, ws_bytes, workspace = _scratch(workspace, need, q.device)
     _call(lib.paged_attention_decode_kv4, q, _ptr(q), q_code, _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
           block_tables.shape[1], _ptr(context_lens), S, Hq, max_context_len, float(scale), _ptr(out), out_code, ws,
-          ws_bytes, ctypes.byref(desc), partition_tokens)
+          ws_bytes, ctypes.byref(desc))
     return out
 
 

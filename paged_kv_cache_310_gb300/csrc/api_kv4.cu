@@ -21,41 +21,34 @@ pkv_status check_kv4(const pkv_cache_desc* c) {
 }
 
 struct Kv4Plan {
-  int part_tokens, max_parts;
-  size_t ml_bytes, workspace;
+  int ctas;
+  size_t ml_at, o_at, workspace;  // offsets of the workspace's parts; 0 bytes: no item is ever split
 };
 
-// Partitions of a 4-bit decode: a CTA of four warps per partition, eight or so per SM over
-// the batch (four are resident; lengths are assumed to average half of max_len).
-pkv_status plan_kv4(int32_t num_seqs, int32_t num_q_heads, int32_t max_len, const pkv_cache_desc* c, int32_t part,
+pkv_status plan_kv4(int32_t num_seqs, int32_t num_q_heads, int32_t max_len, int32_t q_dtype, const pkv_cache_desc* c,
                     Kv4Plan* plan) {
   if (pkv_status st = check_kv4(c)) return st;
   if (num_seqs < 0 || num_seqs > 65535) return fail(PKV_ERR_INVALID_ARG, "num_seqs %d outside [0, 65535]", num_seqs);
   if (num_q_heads <= 0 || num_q_heads % c->num_kv_heads)
     return fail(PKV_ERR_INVALID_ARG, "num_q_heads %d is not a positive multiple of num_kv_heads %d", num_q_heads,
                 c->num_kv_heads);
-  if (num_q_heads / c->num_kv_heads > kKv4MaxGroup)
-    return fail(PKV_ERR_UNSUPPORTED, "4-bit decode supports query-head groups <= %d (group %d)", kKv4MaxGroup,
-                num_q_heads / c->num_kv_heads);
+  const int group = num_q_heads / c->num_kv_heads;
+  if (group > kKv4MaxGroup)
+    return fail(PKV_ERR_UNSUPPORTED, "4-bit decode supports query-head groups <= %d (group %d)", kKv4MaxGroup, group);
+  if (!is_wide(q_dtype)) return fail(PKV_ERR_UNSUPPORTED, "q dtype %d", q_dtype);
   if (max_len < 0) return fail(PKV_ERR_INVALID_ARG, "max_context_len %d < 0", max_len);
-  if (part < 0 || part % 128 || part > 16384)
-    return fail(PKV_ERR_INVALID_ARG, "partition_tokens %d: need 0 or a multiple of 128 <= 16384", part);
-  if (part == 0) {
-    const int64_t work = static_cast<int64_t>(num_seqs) * c->num_kv_heads * (max_len / 2 + 1);
-    int64_t per_cta = work / (8 * 152) + 1;
-    per_cta = per_cta < 256 ? 256 : per_cta > 4096 ? 4096 : (per_cta + 127) / 128 * 128;
-    const int64_t whole = max_len < 128 ? 128 : (static_cast<int64_t>(max_len) + 127) / 128 * 128;
-    part = static_cast<int>(whole < per_cta ? whole : per_cta);
-  }
-  plan->part_tokens = part;
-  plan->max_parts = max_len == 0 ? 1 : static_cast<int>((static_cast<int64_t>(max_len) + part - 1) / part);
-  plan->ml_bytes = plan->workspace = 0;
-  if (static_cast<int64_t>(plan->max_parts) * part > INT32_MAX)
-    return fail(PKV_ERR_UNSUPPORTED, "max_context_len %d: token positions past 32 bits", max_len);
-  if (plan->max_parts > 1) {
-    const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads * plan->max_parts;
-    plan->ml_bytes = (rows * 2 * sizeof(float) + 255) / 256 * 256;
-    plan->workspace = plan->ml_bytes + rows * c->head_dim * sizeof(float);
+  if (max_len > (1 << 30)) return fail(PKV_ERR_UNSUPPORTED, "max_context_len %d above 2^30", max_len);
+  const int64_t units = (static_cast<int64_t>(max_len) + kKv4Unit - 1) / kKv4Unit;
+  const int64_t most = units * num_seqs * c->num_kv_heads;
+  if (most > (int64_t{1} << 50)) return fail(PKV_ERR_UNSUPPORTED, "%lld units of work", static_cast<long long>(most));
+  const int64_t items = static_cast<int64_t>(num_seqs) * c->num_kv_heads;
+  plan->ctas = kv4_decode_ctas(c->head_dim, group, q_dtype, most, items < 1 ? 1 : items);
+  plan->ml_at = plan->o_at = plan->workspace = 0;
+  if (units > 1 && plan->ctas > 1 && num_seqs > 0) {
+    const size_t rows = static_cast<size_t>(2) * plan->ctas * group;
+    plan->ml_at = (plan->ctas * 16 + 255) / 256 * 256;
+    plan->o_at = plan->ml_at + (rows * 8 + 255) / 256 * 256;
+    plan->workspace = plan->o_at + rows * c->head_dim * sizeof(float);
   }
   return PKV_OK;
 }
@@ -170,9 +163,9 @@ pkv_status paged_kv4_expand(const int64_t* src_dst_pairs, int32_t num_pairs, con
 }
 
 size_t paged_attention_decode_kv4_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
-                                                  const pkv_cache_desc* cache, int32_t partition_tokens) {
+                                                  int32_t q_dtype, const pkv_cache_desc* cache) {
   Kv4Plan plan;
-  if (plan_kv4(num_seqs, num_q_heads, max_context_len, cache, partition_tokens, &plan) != PKV_OK) return 0;
+  if (plan_kv4(num_seqs, num_q_heads, max_context_len, q_dtype, cache, &plan) != PKV_OK) return 0;
   return plan.workspace;
 }
 
@@ -181,10 +174,9 @@ pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void
                                       const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
                                       int32_t max_context_len, float scale, void* out, int32_t out_dtype,
                                       void* workspace, size_t workspace_bytes, const pkv_cache_desc* cache,
-                                      int32_t partition_tokens, void* stream) {
+                                      void* stream) {
   Kv4Plan plan;
-  if (pkv_status st = plan_kv4(num_seqs, num_q_heads, max_context_len, cache, partition_tokens, &plan)) return st;
-  if (!is_wide(q_dtype)) return fail(PKV_ERR_UNSUPPORTED, "q dtype %d", q_dtype);
+  if (pkv_status st = plan_kv4(num_seqs, num_q_heads, max_context_len, q_dtype, cache, &plan)) return st;
   if (out_dtype != q_dtype && out_dtype != PKV_F32)
     return fail(PKV_ERR_UNSUPPORTED, "out dtype %d (must be q's dtype or f32)", out_dtype);
   if (num_seqs == 0) return PKV_OK;
@@ -199,18 +191,22 @@ pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void
   int* flag = nullptr;
   if (pkv_status st = device_flag(&flag)) return st;
 
-  DecodeParams p{};
+  Kv4DecodeParams p{};
   p.q = q;
   p.k_cache = k_cache;
   p.v_cache = v_cache;
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.out = out;
-  if (plan.max_parts > 1) {
-    p.ws_ml = static_cast<float*>(workspace);
-    p.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.ml_bytes);
+  if (plan.workspace > 0) {
+    char* base = static_cast<char*>(workspace);
+    p.desc = reinterpret_cast<int4*>(base);
+    p.ws_ml = reinterpret_cast<float2*>(base + plan.ml_at);
+    p.ws_o = reinterpret_cast<float*>(base + plan.o_at);
   }
   p.err = flag;
+  p.q_dtype = q_dtype;
+  p.out_dtype = out_dtype;
   p.num_seqs = num_seqs;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = cache->num_kv_heads;
@@ -219,16 +215,11 @@ pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void
   p.block_size = cache->block_size;
   p.num_blocks = cache->num_blocks;
   p.head_dim = cache->head_dim;
-  p.part_tokens = plan.part_tokens;
-  p.max_parts = plan.max_parts;
-  p.heads_per_item = 1;
-  p.out_f32 = out_dtype == PKV_F32 ? 1 : 0;
+  p.max_len = max_context_len;
+  p.ctas = plan.ctas;
   p.scale_log2 = scale * 1.4426950408889634f;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = launch_decode_kv4(p, q_dtype, out_dtype, s);
-  if (e != cudaSuccess) return cuda_fail(e, "4-bit decode launch");
-  e = launch_merge(p, out_dtype, s);
-  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "merge launch");
+  cudaError_t e = launch_decode_kv4(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "4-bit decode launch");
 }
 
 size_t paged_attention_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,

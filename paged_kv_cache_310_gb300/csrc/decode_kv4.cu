@@ -21,12 +21,20 @@
 //    head the second part takes columns 4..7 (q's columns are doubled, so the lanes there
 //    hold the same p); above, a second MMA.
 //
-// Work: one CTA per (partition, KV head, sequence); its warps take every fourth tile of 16
-// tokens and run alone: each has its own ring of cp.async stages (lanes 0-15 bring the
-// tile's first eight rows of K and V, lanes 16-31 the others), its own running maximum
-// (raised only when a score exceeds it by 8, log2 domain), sum and O, combined through
-// shared memory at the end in a fixed order.  Waits are cp.async.wait_group only.
-// Partitions are merged as for the other caches.
+// Work: a unit is 128 tokens of one (sequence, KV head), an item all units of one.  The
+// batch's items, in order of sequence and head, each with its units and kItemCost more for
+// itself, are cut into spans of equal cost, one per CTA, whatever the lengths are; a CTA
+// works through its span item by item.  An item that lies in one span is
+// written out at once; of one that does not, each CTA leaves (maximum, sum, O) in the
+// workspace -- at most two per CTA, its first and its last item -- and a second kernel
+// joins them.  (A grid over (partition, head, sequence) instead kept an SM busy for 0.83
+// of the time: the last wave's CTAs end at different times.)
+//
+// Each of a CTA's four warps takes 32 of a unit's 128 tokens and runs alone: it has its own
+// ring of cp.async stages (lanes 0-7 bring K and V of the tile's first eight rows, 8-15 of
+// the next, ...), its own running maximum (raised only when a score exceeds it by 8,
+// log2 domain), sum and O, combined through shared memory at the item's end in a fixed
+// order.  Waits are cp.async.wait_group only.
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -38,7 +46,14 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;          // tokens per warp tile
+constexpr int kSub = 2;            // MMA tiles of 16 tokens per step: two independent chains of work
+constexpr int kTile = 16 * kSub;   // tokens per warp and step
+constexpr int kEighths = kTile / 8;  // groups of eight rows: never more than one block each
+constexpr int kUnit = kWarps * kTile;  // tokens per unit of work
+static_assert(kUnit == kKv4Unit, "the host sizes the grid by it");
+constexpr int kItemCost = 2;       // an item's queries, first copies and sums cost about this many units
+constexpr int kMinCost = 3;        // per CTA at least
+constexpr int kOffs = 16;          // tiles whose block offsets a warp holds at a time
 constexpr float kSlack = 8.f;      // a score may exceed the running maximum by this much
 constexpr float kLift = 6.f;       // p = 2^(x - m + 6): small weights stay normal fp16 numbers
 
@@ -47,18 +62,27 @@ constexpr float kLift = 6.f;       // p = 2^(x - m + 6): small weights stay norm
 template <int D, int NB, bool kDup, bool kSplit>
 struct Kv4 {
   static constexpr int kRow = Kv4Row<D>::kBytes;
-  static constexpr int kHalf = 8 * kRow;             // eight rows: never more than one block
-  static constexpr int kStage = 4 * kHalf;           // K then V of rows 0-7, K then V of rows 8-15
+  static constexpr int kHalf = 8 * kRow;             // bytes of eight rows
+  static constexpr int kStage = kEighths * 2 * kHalf;  // K then V of rows 0-7, of rows 8-15, ...
   static constexpr int kHalfPieces = kHalf / 16;
-  static constexpr int kCopies = (2 * kHalfPieces + 15) / 16;  // per lane: 16 lanes bring K and V of a half
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kLanes = 32 / kEighths;       // lanes that bring K and V of eight rows
+  static constexpr int kCopies = (2 * kHalfPieces + kLanes - 1) / kLanes;
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kRingBytes = kWarps * kStages * kStage;
   static constexpr int kCols = 8 * NB;
   // the sums at the end take the ring's place: per warp (max, sum) of the columns, O fragments
   static constexpr int kReduceBytes = kWarps * (kCols * 8 + NB * (D / 16) * 32 * 16);
   static constexpr int kMainBytes = kRingBytes > kReduceBytes ? kRingBytes : kReduceBytes;
+  static constexpr int kCtasPerSm = NB == 2 ? (D == 128 ? 2 : 3) : 4;
   static constexpr int kQueryBytes = NB * (kSplit ? 2 : 1) * (D / 32) * 32 * 16 + kCols * 4;
+  static constexpr int kSmemBytes = kMainBytes + kQueryBytes + kWarps * kOffs * kEighths * 8;
 };
+
+// What a sequence costs per KV head, in units: its units and what an item costs of its own
+// (none where the length is 0 or out of range).
+__device__ __forceinline__ int cost_of(int len, int max_len) {
+  return len <= 0 || len > max_len ? 0 : (len + kUnit - 1) / kUnit + kItemCost;
+}
 
 // Query fragments of 4-bit K rows in shared memory: piece [w][4 g + t] (16 bytes) is lane
 // (g, t)'s B fragment of steps 2w and 2w + 1 for query head g of a block of eight columns.
@@ -132,92 +156,170 @@ __device__ __forceinline__ void store_pair(void* out, size_t i, float x, float y
 }
 
 template <int D, int NB, bool kDup, bool kSplit>
-__global__ void __launch_bounds__(kThreads) decode_kv4_kernel(const __grid_constant__ DecodeParams p, int q_dtype,
-                                                              int out_dtype, const Kv4Bits bits) {
+__global__ void __launch_bounds__(kThreads, Kv4<D, NB, kDup, kSplit>::kCtasPerSm)
+decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
   using C = Kv4<D, NB, kDup, kSplit>;
   extern __shared__ __align__(128) unsigned char smem[];
-  if (p.max_parts > 1) grid_dependents_launch();  // the merge, which waits for this grid
+  __shared__ int64_t scan[kThreads / 32 + 1];
+  __shared__ int64_t start_before;  // units of a KV head in the sequences before start_seq
+  __shared__ int start_seq;
+  __shared__ volatile uint32_t bit_patterns[3];
+  grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
+  grid_dependents_launch();  // the join, which waits for this grid
 
-  const int part = blockIdx.x, kvh = blockIdx.y, s = blockIdx.z;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int G = p.group;
-  const int L = p.context_lens[s];
-  if (L < 0 || L > p.max_parts * p.part_tokens) {
-    if (part == 0 && threadIdx.x == 0) set_error(p.err, kErrLength);
-    return;
+
+  // The bit patterns of widening in registers: the compiler would read them from constant
+  // memory at every use, and that port is slower (128 sequences, 64/8 heads: 92 us against 89).
+  if (threadIdx.x == 0) {
+    bit_patterns[0] = p.bits.low;
+    bit_patterns[1] = p.bits.high;
+    bit_patterns[2] = p.bits.one;
   }
-  const size_t out_row = static_cast<size_t>(s) * p.num_q_heads + static_cast<size_t>(kvh) * G;
-  if (L == 0) {  // empty context: the neutral output
-    if (part == 0)
-      for (int i = threadIdx.x; i < G * D; i += kThreads) store_any(p.out, out_row * D + i, 0.f, out_dtype);
-    return;
+  __syncthreads();
+  Kv4Bits bits;
+  bits.low = bit_patterns[0];
+  bits.high = bit_patterns[1];
+  bits.one = bit_patterns[2];
+
+  // ---- empty sequences get the neutral output; lengths out of range are reported
+  for (int s = blockIdx.x; s < p.num_seqs; s += gridDim.x) {
+    const int L = p.context_lens[s];
+    if (L == 0) {
+      for (int i = threadIdx.x; i < p.num_q_heads * D; i += kThreads)
+        store_any(p.out, static_cast<size_t>(s) * p.num_q_heads * D + i, 0.f, p.out_dtype);
+    } else if ((L < 0 || L > p.max_len) && threadIdx.x == 0) {
+      set_error(p.err, kErrLength);
+    }
   }
-  const int t0 = part * p.part_tokens;
-  if (t0 >= L) return;
-  const int ntok = min(p.part_tokens, L - t0);
-  const int nparts = (L + p.part_tokens - 1) / p.part_tokens;
+
+  // ---- this CTA's span of the batch's units
+  int64_t total = 0;
+  for (int s = threadIdx.x; s < p.num_seqs; s += kThreads) total += cost_of(p.context_lens[s], p.max_len);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  if (lane == 0) scan[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) total += scan[w];
+  __syncthreads();
+  const int64_t units = total * p.num_kv_heads;  // the batch's cost
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (units + kMinCost - 1) / kMinCost);
+  if (threadIdx.x == 0 && p.desc) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (static_cast<int64_t>(blockIdx.x) >= ctas) return;
+  const int64_t begin = blockIdx.x * units / ctas, end = (blockIdx.x + 1) * units / ctas;
+
+  // ---- the sequence it starts in: the last one with (cost before it) * heads <= begin
+  {
+    int64_t before = 0;
+    for (int base = 0; base < p.num_seqs; base += kThreads) {
+      const int s = base + threadIdx.x;
+      const int mine = s < p.num_seqs ? cost_of(p.context_lens[s], p.max_len) : 0;
+      int64_t incl = mine;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += x;
+      }
+      if (lane == 31) scan[warp] = incl;
+      __syncthreads();
+      int64_t all = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) incl += scan[w];
+        all += scan[w];
+      }
+      incl += before;
+      if (mine > 0 && (incl - mine) * p.num_kv_heads <= begin && begin < incl * p.num_kv_heads) {
+        start_seq = s;
+        start_before = incl - mine;
+      }
+      before += all;
+      __syncthreads();
+      if (begin < before * p.num_kv_heads) break;  // found: begin < units, so it always is
+    }
+  }
+  int s = start_seq, L = p.context_lens[s], cost = cost_of(L, p.max_len);
+  int kvh, at_cost;  // KV head of the item, and where in its cost the span begins
+  {
+    const int64_t r = begin - start_before * p.num_kv_heads;
+    kvh = static_cast<int>(r / cost);
+    at_cost = static_cast<int>(r - static_cast<int64_t>(kvh) * cost);
+  }
 
   uint4* q_frag = reinterpret_cast<uint4*>(smem + C::kMainBytes);
   float* q_undo = reinterpret_cast<float*>(smem + C::kMainBytes + C::kQueryBytes - C::kCols * 4);
-  // ---- where each eight tokens' rows of this KV head start in the pools, in bytes
-  int64_t* offs = reinterpret_cast<int64_t*>(smem + C::kMainBytes + C::kQueryBytes);
-  {
-    const int bs_log2 = 31 - __clz(p.block_size);
-    const int64_t tile_bytes = static_cast<int64_t>(p.block_size) * C::kRow;
-    const int32_t* row = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
-    for (int i = threadIdx.x; i < (ntok + 7) / 8; i += kThreads) {
-      const int tok = t0 + 8 * i, col = tok >> bs_log2;
-      int b = col < p.max_blocks_per_seq ? row[col] : -1;
-      if (b < 0 || b >= p.num_blocks) {
-        set_error(p.err, kErrIndex);
-        b = 0;  // keep the copy in bounds; the flag reports the bad table
-      }
-      offs[i] = (static_cast<int64_t>(b) * p.num_kv_heads + kvh) * tile_bytes + (tok & (p.block_size - 1)) * C::kRow;
-    }
-  }
-  __syncthreads();
+  // where each eight rows of this warp's next tiles start in the pools, in bytes
+  int64_t* offs = reinterpret_cast<int64_t*>(smem + C::kMainBytes + C::kQueryBytes) + warp * kOffs * kEighths;
+  const int bs_log2 = 31 - __clz(p.block_size);
+  const int64_t block_rows = static_cast<int64_t>(p.block_size) * C::kRow;
 
-  // ---- this lane's share of a tile's copies: pieces (lane & 15) + 16 i of its half
+  // this lane's share of a tile's copies: pieces piece + kLanes i of its eight rows
   unsigned char* ring = smem + warp * (C::kStages * C::kStage);
-  const int half = lane >> 4, piece = lane & 15;
-  const uint32_t ring_addr = smem_addr(ring) + half * 2 * C::kHalf + piece * 16;
-  constexpr int kMixed = C::kHalfPieces / 16;  // the copy that brings the end of K and the start of V
+  const int eighth = lane / C::kLanes, piece = lane % C::kLanes;
+  const uint32_t ring_addr = smem_addr(ring) + eighth * 2 * C::kHalf + piece * 16;
+  constexpr int kMixed = C::kHalfPieces / C::kLanes;  // the copy that brings the end of K and the start of V
   const unsigned char* kbase = static_cast<const unsigned char*>(p.k_cache) + piece * 16;
   const unsigned char* vbase = static_cast<const unsigned char*>(p.v_cache) + piece * 16 - C::kHalf;
-  const unsigned char* mbase = 16 * kMixed + piece < C::kHalfPieces ? kbase : vbase;
-  auto issue = [&](int tile, uint32_t to) {
-    if (tile * kTile + kTile <= ntok) {
-      const int64_t off = offs[2 * tile + half];
+  const unsigned char* mbase = C::kLanes * kMixed + piece < C::kHalfPieces ? kbase : vbase;
+
+  for (int64_t cur = begin; cur < end;) {
+  // the part of the item here: its own cost comes first, then its units
+  const int taken = static_cast<int>(min(static_cast<int64_t>(cost - at_cost), end - cur));
+  const int n_units = cost - kItemCost, u0 = max(0, at_cost - kItemCost);
+  const int count = at_cost + taken - kItemCost - u0;
+  if (count > 0) {
+  const size_t out_row = static_cast<size_t>(s) * p.num_q_heads + static_cast<size_t>(kvh) * G;
+  // this warp's tiles: from token first + i * kUnit on, i < tiles
+  const int first = u0 * kUnit + warp * kTile;
+  const int tiles = min(count, (L - first + kUnit - 1) / kUnit);  // may be <= 0 in an item's last unit
+  const int full = min(tiles, (L - first - kTile + kUnit) / kUnit);  // of them, tiles that end within the context
+
+  auto locate = [&](int i0) {  // tiles i0 .. i0 + kOffs - 1
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < C::kCopies; ++i)
-        if (16 * (i + 1) <= 2 * C::kHalfPieces || 16 * i + piece < 2 * C::kHalfPieces)
-          cp_async16(to + i * 256, (i < kMixed ? kbase : i == kMixed ? mbase : vbase) + off + i * 256);
-    } else if (tile * kTile < ntok) {  // the last tile: a half past the end is filled with zeros
-      const bool have = tile * kTile + 8 * half < ntok;
-      const int64_t off = offs[have ? 2 * tile + half : 2 * tile];
+    for (int e = lane; e < kOffs * kEighths; e += 32) {
+      const int tok = first + (i0 + e / kEighths) * kUnit + e % kEighths * 8;
+      int64_t off = 0;  // rows past the end are not read
+      if (i0 + e / kEighths < tiles && tok < L) {
+        const int col = tok >> bs_log2;
+        int b = col < p.max_blocks_per_seq ? p.block_tables[static_cast<size_t>(s) * p.max_blocks_per_seq + col] : -1;
+        if (b < 0 || b >= p.num_blocks) {
+          set_error(p.err, kErrIndex);
+          b = 0;  // keep the copy in bounds; the flag reports the bad table
+        }
+        off = (static_cast<int64_t>(b) * p.num_kv_heads + kvh) * block_rows + (tok & (p.block_size - 1)) * C::kRow;
+      }
+      offs[e] = off;
+    }
+    __syncwarp();
+  };
+  auto issue = [&](int i, uint32_t to) {
+    if (i < tiles) {
+      if (i % kOffs == 0) locate(i);
+      const int64_t off = offs[(i % kOffs) * kEighths + eighth];
+      const uint32_t bytes = i < full || first + i * kUnit + 8 * eighth < L ? 16u : 0u;  // past the end: zeros
 #pragma unroll
-      for (int i = 0; i < C::kCopies; ++i)
-        if (16 * (i + 1) <= 2 * C::kHalfPieces || 16 * i + piece < 2 * C::kHalfPieces)
-          cp_async16(to + i * 256, (i < kMixed ? kbase : i == kMixed ? mbase : vbase) + off + i * 256, have ? 16u : 0u);
+      for (int e = 0; e < C::kCopies; ++e)
+        if (C::kLanes * (e + 1) <= 2 * C::kHalfPieces || C::kLanes * e + piece < 2 * C::kHalfPieces)
+          cp_async16(to + e * C::kLanes * 16, (e < kMixed || C::kLanes * (e + 1) <= C::kHalfPieces ? kbase : e == kMixed ? mbase : vbase) +
+                                                  off + e * C::kLanes * 16, bytes);
     }
     cp_async_commit();  // one group per call, empty past the end: the waits below count them
   };
 #pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) issue(warp + i * kWarps, ring_addr + i * C::kStage);
+  for (int i = 0; i < C::kStages - 1; ++i) issue(i, ring_addr + i * C::kStage);
 
   // ---- queries
-  stage_queries<D, NB, kSplit>(p.q, q_dtype, out_row, G, q_frag, q_undo);
+  stage_queries<D, NB, kSplit>(p.q, p.q_dtype, out_row, G, q_frag, q_undo);
   __syncthreads();
-  uint4 qh[NB][D / 32], ql[NB][kSplit ? D / 32 : 1];
+  // (the fragments stay there: four 16-byte loads per step cost less than their registers)
+  const uint4* q_lane = q_frag + (kDup ? (g & 3) * 4 + t : lane);
   float sc[NB][2];
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    const int at = kDup ? (g & 3) * 4 + t : lane;
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      qh[nb][w] = q_frag[(nb * (kSplit ? 2 : 1) * (D / 32) + w) * 32 + at];
-      if (kSplit) ql[nb][w] = q_frag[((nb * 2 + 1) * (D / 32) + w) * 32 + at];
-    }
     const int col = kDup ? 2 * (t & 1) : nb * 8 + 2 * t;
     sc[nb][0] = q_undo[col] * p.scale_log2;
     sc[nb][1] = q_undo[col + 1] * p.scale_log2;
@@ -233,36 +335,38 @@ __global__ void __launch_bounds__(kThreads) decode_kv4_kernel(const __grid_const
   }
 
   uint32_t at = 0, refill = (C::kStages - 1) * C::kStage;  // stages, as offsets into the ring
-  auto step = [&](int tile, auto last) {
+  auto step = [&](int i_tile, auto last) {
     constexpr bool kLast = decltype(last)::value;  // the tile may end past the context
     cp_async_wait<C::kStages - 2>();
     __syncwarp();  // the other lanes' copies too; and everybody has left the stage refilled next
-    issue(tile + (C::kStages - 1) * kWarps, ring_addr + refill);
+    issue(i_tile + C::kStages - 1, ring_addr + refill);
     refill = at;
     const unsigned char* ks = ring + at;
     at = at == (C::kStages - 1) * C::kStage ? 0 : at + C::kStage;
-    const int left = kLast ? ntok - tile * kTile : kTile;  // tokens of this tile
+    const int left = kLast ? L - first - i_tile * kUnit : kTile;  // tokens of this tile
 
     // ---- scores
-    float c[NB][2][4];
-    {
+    float c[NB][kSub][2][4];
+#pragma unroll
+    for (int u = 0; u < kSub; ++u) {
       constexpr int kWords = D / 32;
       uint32_t w0[kWords], w1[kWords];
-      const unsigned char* r0 = ks + g * C::kRow;
+      const unsigned char* r0 = ks + u * 4 * C::kHalf + g * C::kRow;
+      const unsigned char* r1 = r0 + 2 * C::kHalf;
       if constexpr (kWords == 4) {
         const uint4 a = *reinterpret_cast<const uint4*>(r0 + t * 16);
-        const uint4 b = *reinterpret_cast<const uint4*>(r0 + 2 * C::kHalf + t * 16);
+        const uint4 b = *reinterpret_cast<const uint4*>(r1 + t * 16);
         w0[0] = a.x; w0[1] = a.y; w0[2] = a.z; w0[3] = a.w;
         w1[0] = b.x; w1[1] = b.y; w1[2] = b.z; w1[3] = b.w;
       } else {
         const uint2 a = *reinterpret_cast<const uint2*>(r0 + t * 8);
-        const uint2 b = *reinterpret_cast<const uint2*>(r0 + 2 * C::kHalf + t * 8);
+        const uint2 b = *reinterpret_cast<const uint2*>(r1 + t * 8);
         w0[0] = a.x; w0[1] = a.y;
         w1[0] = b.x; w1[1] = b.y;
       }
       const int pair = D / 2 + 4 * (t * D / 128);
       const __half2 p0 = *reinterpret_cast<const __half2*>(r0 + pair);
-      const __half2 p1 = *reinterpret_cast<const __half2*>(r0 + 2 * C::kHalf + pair);
+      const __half2 p1 = *reinterpret_cast<const __half2*>(r1 + pair);
 #pragma unroll
       for (int i = 0; i < kWords; ++i) {
         uint32_t a[4], b[4];
@@ -270,126 +374,148 @@ __global__ void __launch_bounds__(kThreads) decode_kv4_kernel(const __grid_const
         kv4_word(w1[i], __low2half2(p1), __high2half2(p1), bits, b);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+          const uint4 q = q_lane[(nb * (kSplit ? 2 : 1) * (D / 32) + i) * 32];
           if (i == 0) {
-            mma_f16_first(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][i].x, qh[nb][i].y);
-            mma_f16_first(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][i].z, qh[nb][i].w);
+            mma_f16_first(c[nb][u][0], a[0], b[0], a[1], b[1], q.x, q.y);
+            mma_f16_first(c[nb][u][1], a[2], b[2], a[3], b[3], q.z, q.w);
           } else {
-            mma_f16(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][i].x, qh[nb][i].y);
-            mma_f16(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][i].z, qh[nb][i].w);
+            mma_f16(c[nb][u][0], a[0], b[0], a[1], b[1], q.x, q.y);
+            mma_f16(c[nb][u][1], a[2], b[2], a[3], b[3], q.z, q.w);
           }
           if (kSplit) {
-            mma_f16(c[nb][0], a[0], b[0], a[1], b[1], ql[nb][i].x, ql[nb][i].y);
-            mma_f16(c[nb][1], a[2], b[2], a[3], b[3], ql[nb][i].z, ql[nb][i].w);
+            const uint4 r = q_lane[((nb * 2 + 1) * (D / 32) + i) * 32];
+            mma_f16(c[nb][u][0], a[0], b[0], a[1], b[1], r.x, r.y);
+            mma_f16(c[nb][u][1], a[2], b[2], a[3], b[3], r.z, r.w);
           }
         }
       }
     }
 
+    // V's codes and pairs of rows 2t, 2t + 1 of a tile's first eight and of its last, asked for
+    // before the softmax (its vote keeps the compiler from doing so)
+    constexpr int kVWords = D / 64;  // of codes per row and lane
+    uint32_t vw[kSub][4][kVWords], pr[kSub][4];
+    auto load_v = [&](int u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned char* row = ks + (u * 4 + (i & 2) + 1) * C::kHalf + (2 * t + (i & 1)) * C::kRow;
+        if constexpr (kVWords == 2) {
+          const uint2 a = *reinterpret_cast<const uint2*>(row + g * 8);
+          vw[u][i][0] = a.x;
+          vw[u][i][1] = a.y;
+        } else {
+          vw[u][i][0] = *reinterpret_cast<const uint32_t*>(row + g * 4);
+        }
+        pr[u][i] = *reinterpret_cast<const uint32_t*>(row + D / 2 + 4 * (g * D / 256));
+        // past the end a row holds anything, NaN too: step = lo = 0 makes it zero
+        if (kLast && u * 16 + 2 * t + (i & 1) + (i & 2) * 4 >= left) pr[u][i] = 0u;
+      }
+    };
+    load_v(0);
+
     // ---- softmax; tokens past the end get -inf
-    uint32_t ph[NB][2], pl[NB][2];  // P^T fragments: tokens 0-7 and 8-15
+    uint32_t ph[NB][kSub][2], pl[NB][kSub][2];  // P^T fragments: tokens 0-7 and 8-15
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      float x[4];  // score - m + 6
+      float x[kSub][4];  // score - m + 6
       const float ma = kLift - m[nb][0], mb = kLift - m[nb][1];
+      float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = fmaf(c[nb][0][i] + c[nb][1][i], sc[nb][i & 1], i & 1 ? mb : ma);
-      if (kLast) {
-        if (g >= left) x[0] = x[1] = -INFINITY;
-        if (g + 8 >= left) x[2] = x[3] = -INFINITY;
-      }
-      if (__any_sync(0xffffffffu, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) > kLift + kSlack)) {
-        // raise both columns' maxima: scores again (m = -inf makes x = inf), their largest
-        float y[4];
+      for (int u = 0; u < kSub; ++u)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          y[i] = kLast && g + (i & 2) * 4 >= left ? -INFINITY : (c[nb][0][i] + c[nb][1][i]) * sc[nb][i & 1];
-        float a = fmaxf(y[0], y[2]), b = fmaxf(y[1], y[3]);
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-          b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, off));
+        for (int i = 0; i < 4; ++i) {
+          x[u][i] = fmaf(c[nb][u][0][i] + c[nb][u][1][i], sc[nb][i & 1], i & 1 ? mb : ma);
+          if (kLast && u * 16 + g + (i & 2) * 4 >= left) x[u][i] = -INFINITY;
+          top = fmaxf(top, x[u][i]);
         }
-        a = fmaxf(a, m[nb][0]);
-        b = fmaxf(b, m[nb][1]);
-        // a column that saw nothing but NaN yet keeps m = -inf, and its NaN sum
-        const float fa = a == m[nb][0] ? 1.f : exp2_approx(m[nb][0] - a);
-        const float fb = b == m[nb][1] ? 1.f : exp2_approx(m[nb][1] - b);
-        m[nb][0] = a;
-        m[nb][1] = b;
-        l[nb][0] *= fa;
-        l[nb][1] *= fb;
+      if (__any_sync(0xffffffffu, top > kLift + kSlack)) {
+        // raise both columns' maxima: scores again (m = -inf makes x = inf), their largest
+        float top2[2] = {m[nb][0], m[nb][1]};
+#pragma unroll
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[u][i] = (c[nb][u][0][i] + c[nb][u][1][i]) * sc[nb][i & 1];
+            if (kLast && u * 16 + g + (i & 2) * 4 >= left) x[u][i] = -INFINITY;
+            top2[i & 1] = fmaxf(top2[i & 1], x[u][i]);
+          }
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) top2[e] = fmaxf(top2[e], __shfl_xor_sync(0xffffffffu, top2[e], off));
+          // a column that saw nothing but NaN yet keeps m = -inf, and its NaN sum
+          f[e] = top2[e] == m[nb][e] ? 1.f : exp2_approx(m[nb][e] - top2[e]);
+          m[nb][e] = top2[e];
+          l[nb][e] *= f[e];
+        }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
-          o[nb][i][0] *= fa;
-          o[nb][i][1] *= fb;
-          o[nb][i][2] *= fa;
-          o[nb][i][3] *= fb;
+          o[nb][i][0] *= f[0];
+          o[nb][i][1] *= f[1];
+          o[nb][i][2] *= f[0];
+          o[nb][i][3] *= f[1];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = y[i] - (i & 1 ? b : a) + kLift;
+        for (int u = 0; u < kSub; ++u)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[u][i] = x[u][i] - m[nb][i & 1] + kLift;
       }
-      const float e0 = exp2_approx(x[0]), e1 = exp2_approx(x[1]), e2 = exp2_approx(x[2]), e3 = exp2_approx(x[3]);
-      l[nb][0] += e0 + e2;
-      l[nb][1] += e1 + e3;
-      uint32_t h0 = pack_half2(e0, e1), h1 = pack_half2(e2, e3);
-      const uint32_t r0 = pack_half2_rest(e0, e1, h0), r1 = pack_half2_rest(e2, e3, h1);
-      if (kDup) {
-        if (t >= 2) {
-          h0 = r0;
-          h1 = r1;
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = exp2_approx(x[u][i]);
+        l[nb][0] += e[0] + e[2];
+        l[nb][1] += e[1] + e[3];
+        uint32_t h0 = pack_half2(e[0], e[1]), h1 = pack_half2(e[2], e[3]);
+        const uint32_t r0 = pack_half2_rest(e[0], e[1], h0), r1 = pack_half2_rest(e[2], e[3], h1);
+        if (kDup) {
+          if (t >= 2) {
+            h0 = r0;
+            h1 = r1;
+          }
+        } else {
+          pl[nb][u][0] = movmatrix_trans(r0);
+          pl[nb][u][1] = movmatrix_trans(r1);
         }
-      } else {
-        pl[nb][0] = movmatrix_trans(r0);
-        pl[nb][1] = movmatrix_trans(r1);
+        ph[nb][u][0] = movmatrix_trans(h0);
+        ph[nb][u][1] = movmatrix_trans(h1);
       }
-      ph[nb][0] = movmatrix_trans(h0);
-      ph[nb][1] = movmatrix_trans(h1);
     }
 
     // ---- output
-    {
-      constexpr int kWords = D / 64;  // of codes per row and lane
-      uint32_t w[4][kWords];
-      uint32_t pr[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 2 * t + (i & 1) + (i & 2) * 4;  // rows 2t, 2t+1 of either half
-        const unsigned char* row = ks + (i & 2 ? 3 : 1) * C::kHalf + (2 * t + (i & 1)) * C::kRow;
-        if (kWords == 2) {
-          const uint2 a = *reinterpret_cast<const uint2*>(row + g * 8);
-          w[i][0] = a.x;
-          w[i][kWords - 1] = a.y;
-        } else {
-          w[i][0] = *reinterpret_cast<const uint32_t*>(row + g * 4);
-        }
-        pr[i] = *reinterpret_cast<const uint32_t*>(row + D / 2 + 4 * (g * D / 256));
-        // past the end a row holds anything, NaN too: step = lo = 0 makes it zero
-        if (kLast && r >= left) pr[i] = 0u;
-      }
-      const __half2 step0 = as_half2(__byte_perm(pr[0], pr[1], 0x5410)), lo0 = as_half2(__byte_perm(pr[0], pr[1], 0x7632));
-      const __half2 step1 = as_half2(__byte_perm(pr[2], pr[3], 0x5410)), lo1 = as_half2(__byte_perm(pr[2], pr[3], 0x7632));
+    for (int u = 1; u < kSub; ++u) load_v(u);
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) {
+    for (int u = 0; u < kSub; ++u) {
+      const __half2 step0 = as_half2(__byte_perm(pr[u][0], pr[u][1], 0x5410));
+      const __half2 lo0 = as_half2(__byte_perm(pr[u][0], pr[u][1], 0x7632));
+      const __half2 step1 = as_half2(__byte_perm(pr[u][2], pr[u][3], 0x5410));
+      const __half2 lo1 = as_half2(__byte_perm(pr[u][2], pr[u][3], 0x7632));
+#pragma unroll
+      for (int i = 0; i < kVWords; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t sel = 0x4400u + 0x1111u * j;  // byte j of both words, twice each
-          const uint32_t x0 = __byte_perm(w[0][i], w[1][i], sel), x1 = __byte_perm(w[2][i], w[3][i], sel);
+          const uint32_t x0 = __byte_perm(vw[u][0][i], vw[u][1][i], sel);
+          const uint32_t x1 = __byte_perm(vw[u][2][i], vw[u][3][i], sel);
           const uint32_t a0 = as_u32(__hfma2(low_codes(x0, bits), step0, lo0));
           const uint32_t a1 = as_u32(__hfma2(high_codes(x0, bits), step0, lo0));
           const uint32_t a2 = as_u32(__hfma2(low_codes(x1, bits), step1, lo1));
           const uint32_t a3 = as_u32(__hfma2(high_codes(x1, bits), step1, lo1));
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            mma_f16(o[nb][4 * i + j], a0, a1, a2, a3, ph[nb][0], ph[nb][1]);
-            if (!kDup) mma_f16(o[nb][4 * i + j], a0, a1, a2, a3, pl[nb][0], pl[nb][1]);
+            mma_f16(o[nb][4 * i + j], a0, a1, a2, a3, ph[nb][u][0], ph[nb][u][1]);
+            if (!kDup) mma_f16(o[nb][4 * i + j], a0, a1, a2, a3, pl[nb][u][0], pl[nb][u][1]);
           }
         }
       }
     }
   };
-  int tile = warp;
-  for (; (tile + 1) * kTile <= ntok; tile += kWarps) step(tile, std::false_type{});
-  if (tile * kTile < ntok) step(tile, std::true_type{});
+  int i_tile = 0;
+  for (; i_tile < full; ++i_tile) step(i_tile, std::false_type{});
+  if (i_tile < tiles) step(i_tile, std::true_type{});
   cp_async_wait<0>();
   __syncthreads();  // every warp has left its ring: the sums take its place
 
@@ -433,6 +559,7 @@ __global__ void __launch_bounds__(kThreads) decode_kv4_kernel(const __grid_const
       }
     }
     const int h = kDup ? 2 * (t & 1) : nb * 8 + 2 * t;  // heads h and h + 1
+    const int slot = 2 * blockIdx.x + (u0 == 0);  // of an item that is not all here
 #pragma unroll
     for (int i = warp; i < D / 16; i += kWarps) {
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -456,46 +583,117 @@ __global__ void __launch_bounds__(kThreads) decode_kv4_kernel(const __grid_const
         if ((kDup && t >= 2) || h + e >= G) continue;
         const float a = e ? acc.y : acc.x, b = e ? acc.w : acc.z;
         const size_t row = out_row + h + e;
-        if (nparts == 1) {
-          store_pair(p.out, row * D + d, a / lsum[e], b / lsum[e], out_dtype);
+        if (count == n_units) {
+          store_pair(p.out, row * D + d, a / lsum[e], b / lsum[e], p.out_dtype);
         } else {
-          const size_t k = row * p.max_parts + part;
+          const size_t k = static_cast<size_t>(slot) * G + h + e;
           *reinterpret_cast<float2*>(p.ws_o + k * D + d) = make_float2(a, b);
-          if (i == 0 && g == 0) {
-            p.ws_ml[2 * k] = M[e];
-            p.ws_ml[2 * k + 1] = lsum[e];
-          }
+          if (i == 0 && g == 0) p.ws_ml[k] = make_float2(M[e], lsum[e]);
         }
       }
     }
   }
+  if (threadIdx.x == 0 && u0 == 0 && count < n_units) {
+    // the item ends in the span of the last CTA c with c * units / ctas <= its last place
+    const int64_t last = cur - at_cost + cost - 1;
+    p.desc[blockIdx.x] = make_int4(s, kvh, static_cast<int>(((last + 1) * ctas + units - 1) / units - 1), 0);
+  }
+  __syncthreads();  // the sums have been read: the ring and the queries take their place
+  }
+
+  // ---- the next item
+  cur += taken;
+  at_cost = 0;
+  if (cur < end && ++kvh == p.num_kv_heads) {
+    kvh = 0;
+    do {
+      if (++s >= p.num_seqs) return;  // not reached: the span has cost left
+      L = p.context_lens[s];
+      cost = cost_of(L, p.max_len);
+    } while (cost == 0);
+  }
+  }
+}
+
+// One CTA per span: joins the item that starts in it and ends in a later one, if there is
+// one.  Its pieces are the span's last item (slot 2c + 1) and the first ones of the spans up
+// to the item's end (slots 2c).  A warp per head at a time: lanes take a piece each for the
+// factors 2^(m - M), then two (D 64) or four dimensions each for the sum.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) join_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
+  grid_dependency_wait();
+  const int4 d = p.desc[blockIdx.x];
+  if (d.x < 0) return;
+  const int c = blockIdx.x, n = d.z - c + 1, G = p.group, D = p.head_dim;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const size_t out = (static_cast<size_t>(d.x) * p.num_q_heads + static_cast<size_t>(d.y) * G) * D;
+  auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * G; };
+  const int parts = D / 64;  // 64 dimensions of a head per warp and round
+  for (int x = warp; x < G * parts; x += kJoinThreads / 32) {
+    const int h = x / parts, e = x % parts * 64 + 2 * lane;
+    float M = -INFINITY;
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.ws_ml[slot(i) + h].x);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float lsum = 0.f, a = 0.f, b = 0.f;
+    for (int base = 0; base < n; base += 32) {
+      float f = 0.f;
+      if (base + lane < n) {
+        const float2 ml = p.ws_ml[slot(base + lane) + h];
+        f = exp2_approx(ml.x - M);
+        lsum = fmaf(f, ml.y, lsum);
+      }
+      const int here = min(32, n - base);
+#pragma unroll 8
+      for (int i = 0; i < here; ++i) {
+        const float2 o = *reinterpret_cast<const float2*>(p.ws_o + (slot(base + i) + h) * D + e);
+        const float w = __shfl_sync(0xffffffffu, f, i);
+        a = fmaf(w, o.x, a);
+        b = fmaf(w, o.y, b);
+      }
+    }
+    lsum = group_sum<32>(lsum);
+    store_pair(p.out, out + h * D + e, a / lsum, b / lsum, p.out_dtype);
+  }
 }
 
 template <int D, int NB, bool kDup, bool kSplit>
-cudaError_t launch_t(const DecodeParams& p, int q_dtype, int out_dtype, cudaStream_t stream) {
+cudaError_t launch_t(const Kv4DecodeParams& p, cudaStream_t stream) {
   using C = Kv4<D, NB, kDup, kSplit>;
-  const size_t smem = C::kMainBytes + C::kQueryBytes + static_cast<size_t>(p.part_tokens / 8) * 8;
   static std::atomic<unsigned long long> configured{0};
-  cudaError_t e = ensure_smem_limit(decode_kv4_kernel<D, NB, kDup, kSplit>, 100 * 1024, configured);
+  cudaError_t e = ensure_smem_limit(decode_kv4_kernel<D, NB, kDup, kSplit>, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
-  dim3 grid(p.max_parts, p.num_kv_heads, p.num_seqs);
-  decode_kv4_kernel<D, NB, kDup, kSplit><<<grid, kThreads, smem, stream>>>(p, q_dtype, out_dtype, Kv4Bits{});
-  return cudaGetLastError();
+  return launch_dependent(decode_kv4_kernel<D, NB, kDup, kSplit>, p.ctas, kThreads, C::kSmemBytes, stream, p);
 }
 
 template <int D, bool kSplit>
-cudaError_t launch_g(const DecodeParams& p, int q_dtype, int out_dtype, cudaStream_t stream) {
-  if (p.group <= 4) return launch_t<D, 1, true, kSplit>(p, q_dtype, out_dtype, stream);
-  if (p.group <= 8) return launch_t<D, 1, false, kSplit>(p, q_dtype, out_dtype, stream);
-  return launch_t<D, 2, false, kSplit>(p, q_dtype, out_dtype, stream);
+cudaError_t launch_g(const Kv4DecodeParams& p, cudaStream_t stream) {
+  if (p.group <= 4) return launch_t<D, 1, true, kSplit>(p, stream);
+  if (p.group <= 8) return launch_t<D, 1, false, kSplit>(p, stream);
+  return launch_t<D, 2, false, kSplit>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_kv4(const DecodeParams& p, int q_dtype, int out_dtype, cudaStream_t stream) {
-  if (q_dtype == PKV_F32)
-    return p.head_dim == 64 ? launch_g<64, true>(p, q_dtype, out_dtype, stream) : launch_g<128, true>(p, q_dtype, out_dtype, stream);
-  return p.head_dim == 64 ? launch_g<64, false>(p, q_dtype, out_dtype, stream) : launch_g<128, false>(p, q_dtype, out_dtype, stream);
+int kv4_decode_ctas(int head_dim, int group, int q_dtype, int64_t max_units, int64_t items) {
+  int per_sm;
+  if (head_dim == 128)
+    per_sm = group <= 8 ? Kv4<128, 1, false, false>::kCtasPerSm
+                        : q_dtype == PKV_F32 ? Kv4<128, 2, false, true>::kCtasPerSm : Kv4<128, 2, false, false>::kCtasPerSm;
+  else
+    per_sm = group <= 8 ? Kv4<64, 1, false, false>::kCtasPerSm : Kv4<64, 2, false, false>::kCtasPerSm;
+  const int64_t most = (max_units + items * kItemCost + kMinCost - 1) / kMinCost;
+  return static_cast<int>(most < 152 * per_sm ? most : 152 * per_sm);
+}
+
+cudaError_t launch_decode_kv4(const Kv4DecodeParams& p, cudaStream_t stream) {
+  cudaError_t e;
+  if (p.q_dtype == PKV_F32)
+    e = p.head_dim == 64 ? launch_g<64, true>(p, stream) : launch_g<128, true>(p, stream);
+  else
+    e = p.head_dim == 64 ? launch_g<64, false>(p, stream) : launch_g<128, false>(p, stream);
+  if (e != cudaSuccess || !p.desc) return e;
+  return launch_dependent(join_kv4_kernel, p.ctas, kJoinThreads, 0, stream, p);
 }
 
 }  // namespace pkv

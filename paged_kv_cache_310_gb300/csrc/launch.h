@@ -131,10 +131,28 @@ struct Kv4ExpandParams {
 };
 cudaError_t launch_kv4_expand(Kv4ExpandParams p, int dtype, cudaStream_t stream);
 
-// Single-token attention over 4-bit pools (head_dim 64/128, group <= 16); partitions are
-// merged by launch_merge.
+// Single-token attention over 4-bit pools (head_dim 64/128, group <= 16).
+struct Kv4DecodeParams {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  void* out;
+  int4* desc;    // workspace [ctas]: the item a CTA's span leaves unfinished; NULL: none can be
+  float2* ws_ml; // workspace [2 ctas][G]: (maximum, sum) of an unfinished item
+  float* ws_o;   // workspace [2 ctas][G][D]: its un-normalised output
+  int* err;
+  int32_t q_dtype, out_dtype, num_seqs, num_q_heads, num_kv_heads, group, max_blocks_per_seq;
+  int32_t block_size, num_blocks, head_dim, max_len, ctas;
+  float scale_log2;
+  Kv4Bits bits;
+};
 constexpr int kKv4MaxGroup = 16;
-cudaError_t launch_decode_kv4(const DecodeParams& p, int q_dtype, int out_dtype, cudaStream_t stream);
+constexpr int kKv4Unit = 128;  // tokens of one unit of work
+// CTAs of a call over at most max_units units in `items` (sequence, KV head) items.
+int kv4_decode_ctas(int head_dim, int group, int q_dtype, int64_t max_units, int64_t items);
+cudaError_t launch_decode_kv4(const Kv4DecodeParams& p, cudaStream_t stream);
 
 // ---- attention weights and eviction
 struct WeightsParams {

@@ -146,9 +146,9 @@ def test_decode_checks(lib):
     d = desc()
 
     def run(d=d, q=A, q_dtype=pkv.BF16, kc=A, vc=A, tables=A, width=256, lens=A, S=4, Hq=32, L=4096, scale=0.1, out=A,
-            out_dtype=pkv.BF16, ws=A, nbytes=1 << 30, part=0):
+            out_dtype=pkv.BF16, ws=A, nbytes=1 << 30):
         return lib.paged_attention_decode_kv4(q, q_dtype, kc, vc, tables, width, lens, S, Hq, L, scale, out, out_dtype, ws,
-                                              nbytes, ctypes.byref(d), part, None)
+                                              nbytes, ctypes.byref(d), None)
 
     assert run(S=0) == 0
     for bad in (dict(q=None), dict(kc=None), dict(vc=None), dict(tables=None), dict(lens=None), dict(out=None)):
@@ -162,14 +162,12 @@ def test_decode_checks(lib):
     assert run(S=-1) == 1 and run(S=65536) == 1 and run(L=-1) == 1
     assert run(width=255) == 1 and b"max_blocks_per_seq" in lib.paged_kv_last_error()
     assert run(scale=float("nan")) == 1 and run(scale=float("inf")) == 1
-    for part in (100, -128, 16512):
-        assert run(part=part) == 1
-    need = lib.paged_attention_decode_kv4_workspace_bytes(4, 32, 4096, ctypes.byref(d), 128)
-    rows = 4 * 32 * 32
-    assert need == -(-rows * 8 // 256) * 256 + rows * 128 * 4
-    assert run(part=128, ws=None) == 3 and run(part=128, nbytes=need - 1) == 3
-    assert run(part=128, ws=ctypes.c_void_p(0x10080)) == 1
-    assert lib.paged_attention_decode_kv4_workspace_bytes(4, 32, 200, ctypes.byref(d), 0) == 0   # one partition
-    assert lib.paged_attention_decode_kv4_workspace_bytes(4, 30, 4096, ctypes.byref(d), 0) == 0  # invalid
-    # token positions stay within 32 bits
-    assert run(L=2**31 - 1, width=2**27, part=16384) == 2
+    need = lib.paged_attention_decode_kv4_workspace_bytes(4, 32, 4096, pkv.BF16, ctypes.byref(d))
+    assert 0 < need < 32 << 20
+    assert run(ws=None) == 3 and run(nbytes=need - 1) == 3 and run(ws=ctypes.c_void_p(0x10080)) == 1
+    big = lib.paged_attention_decode_kv4_workspace_bytes(512, 32, 1 << 20, pkv.BF16, ctypes.byref(d))
+    assert big == lib.paged_attention_decode_kv4_workspace_bytes(64, 32, 1 << 18, pkv.BF16, ctypes.byref(d)) < 32 << 20
+    assert lib.paged_attention_decode_kv4_workspace_bytes(4, 32, 64, pkv.BF16, ctypes.byref(d)) == 0    # no split
+    assert lib.paged_attention_decode_kv4_workspace_bytes(4, 30, 4096, pkv.BF16, ctypes.byref(d)) == 0  # invalid
+    assert run(L=(1 << 30) + 1, width=1 << 30) == 2
+    assert run(L=1 << 30, S=65535, d=desc(num_kv_heads=65535, head_dim=64, block_size=8), Hq=65535, width=1 << 30) == 2

@@ -6,7 +6,7 @@ Tolerance (f32 output): with X = the largest scale * sum_d |q_d k_d| of the case
 D products are off by at most (D + 4) 2^-23 X (accumulators may truncate, so a step counts
 2^-23), q's second fp16 part leaves 2^-21 X, and a score error e moves the weights' sum of
 absolute changes by at most 2 e.  Weights in two fp16 parts, exp2 and the sums of a warp's
-n/64 tiles, of lanes, warps and partitions add (n/16 + 64) 2^-23.  All of it times max |V|.
+n/64 tiles, of lanes, warps and CTAs' shares add (n/16 + 64) 2^-23.  All of it times max |V|.
 A 16-bit output adds half a step of the value: 2^-8 (bf16) or 2^-11 (f16) of it."""
 import numpy as np
 import pytest
@@ -99,10 +99,9 @@ class Case:
 def test_parity(q_dtype, d, bs, group, hkv):
     lens = [1, 0, 15, 16, 17, 33, 64, 127, 129, 300, 2, 8]
     c = Case(310_800 + d + bs + group, lens, group * hkv, hkv, d, bs, q_dtype)
-    one = c.check("f32")
+    out = c.check("f32")
     c.check(q_dtype)
-    split = c.check("f32", partition_tokens=128)
-    assert (one[1] == 0).all() and (split[1] == 0).all()
+    assert (out[1] == 0).all()
 
 
 @pytest.mark.parametrize("lens,hq,hkv,d,bs", [([4097, 1, 5000], 8, 2, 128, 16), ([9001], 4, 1, 64, 8),
@@ -110,8 +109,21 @@ def test_parity(q_dtype, d, bs, group, hkv):
 def test_long_contexts(lens, hq, hkv, d, bs):
     c = Case(310_830 + len(lens), lens, hq, hkv, d, bs, "f32")
     c.check("f32")
-    c.check("f32", partition_tokens=4096)
-    c.check("f32", partition_tokens=16384)
+    c.check("f32", max_context_len=c.tables.shape[1] * bs)
+
+
+@pytest.mark.parametrize("lens,hkv", [([64] * 5, 3), ([128] * 3, 1), ([65, 1, 64, 127], 1), ([1], 1), ([128], 1), ([192], 1),
+                                      ([64 * 9] * 4 + [0] * 200 + [63] * 70 + [1] * 60, 2), ([0] * 300 + [700], 2)])
+def test_shares_that_begin_and_end_anywhere(lens, hkv):
+    # a CTA's share is at least two units of 64 tokens: items that fill one, cross one, share one
+    Case(310_835 + len(lens), lens, 4 * hkv, hkv, 64, 8, "f16").check("f32")
+
+
+def test_more_units_than_ctas():
+    # 40 sequences x 16 heads: each CTA has several whole items and two parts
+    gen = torch.Generator().manual_seed(310_836)
+    lens = torch.randint(1, 1500, (40,), generator=gen).tolist()
+    Case(310_837, lens, 16, 16, 64, 16, "bf16").check("f32")
 
 
 @pytest.mark.parametrize("group", [1, 4, 8, 16])
@@ -126,7 +138,6 @@ def test_running_maximum_rising(group, d):
     rows = [torch.from_numpy(model.quantise((grow + 0.05 * torch.randn(n, d, generator=gen))[None].double().numpy()))]
     c = Case(310_841, [n], group, 1, d, 16, "f32", k_rows=rows, q=q)
     c.check("f32")
-    c.check("f32", partition_tokens=128)
 
 
 def test_scaled_queries_keep_their_precision():
@@ -151,27 +162,26 @@ def test_placement_and_repeats_do_not_change_a_bit():
         c.v = c.k.clone()
         fill(c.k, c.tables, lens, k)
         fill(c.v, c.tables, lens, v)
-        outs += [c.run(partition_tokens=256) for _ in range(3)]
+        outs += [c.run() for _ in range(3)]
     torch.cuda.synchronize()
     assert all(torch.equal(outs[0], o) for o in outs[1:])
 
 
 def test_non_finite_inputs_reach_only_what_attends_to_them():
     gen = torch.Generator().manual_seed(310_870)
-    lens = [40, 40, 40]
+    lens = [400, 400, 400]                                  # split over CTAs
     rows = kv_rows(gen, lens, 2, 64)
     rows[1][0, 7, 32:] = 255                                # K of sequence 1, KV head 0, token 7: NaN
     c = Case(310_871, lens, 4, 2, 64, 16, "f32", k_rows=rows)
     c.v[c.tables[2, 1], 1, 3, 32:36] = 255                  # V of sequence 2, KV head 1, token 19: dims 0..31
     c.q[0, 3, 5] = float("inf")                             # a query of sequence 0, KV head 1
-    for part in (0, 128):
-        out = c.run(partition_tokens=part).cpu()
-        assert pkv.device_error() == 0
-        want = torch.zeros(3, 4, 64, dtype=torch.bool)
-        want[0, 3] = True
-        want[1, :2] = True
-        want[2, 2:, :32] = True
-        assert torch.equal(out.isnan(), want)
+    out = c.run().cpu()
+    assert pkv.device_error() == 0
+    want = torch.zeros(3, 4, 64, dtype=torch.bool)
+    want[0, 3] = True
+    want[1, :2] = True
+    want[2, 2:, :32] = True
+    assert torch.equal(out.isnan(), want)
 
 
 def test_bad_tables_and_lengths_set_the_flag():
@@ -182,12 +192,8 @@ def test_bad_tables_and_lengths_set_the_flag():
     c.tables[0, 3] = -7
     c.run()
     assert pkv.device_error() == 5
-    c = Case(310_881, [100, 20], 8, 2, 128, 16, "f16")
-    out = c.run(max_context_len=64, partition_tokens=128)   # within the partition's room: attended in full
-    out = c.run(max_context_len=20, partition_tokens=128)
-    pkv.device_error()
-    c = Case(310_882, [300, 20], 8, 2, 128, 16, "f16")
-    out = c.run(max_context_len=128, partition_tokens=128)
+    c = Case(310_882, [300, 20, 0], 8, 2, 128, 16, "f16")
+    out = c.run(max_context_len=299)
     assert pkv.device_error() == 5
     assert (out[0] == 7).all()                              # left as it was; the other one is done
     ref, tol = c.reference()
@@ -210,7 +216,7 @@ def test_replays_in_graphs_that_share_nothing_but_inputs():
     outs = [torch.empty(q.shape, device="cuda") for _ in range(3)]
 
     def call(out):
-        pkv.paged_attention_decode_kv4(q, k, v, tables, lens, c.scale, out, max_context_len=900, partition_tokens=128)
+        pkv.paged_attention_decode_kv4(q, k, v, tables, lens, c.scale, out, max_context_len=900)
 
     call(outs[2])
     torch.cuda.synchronize()
@@ -237,7 +243,7 @@ def test_replays_in_graphs_that_share_nothing_but_inputs():
 
 def test_calls_on_two_streams_at_once():
     cases = [Case(310_910 + i, [1500 + i, 37], 8, 2, 128, 16, "f16") for i in range(2)]
-    want = [c.run(partition_tokens=128) for c in cases]
+    want = [c.run() for c in cases]
     torch.cuda.synchronize()
     dev = [c.device() for c in cases]
     outs = [torch.empty(d[0].shape, device="cuda") for d in dev]
@@ -248,7 +254,7 @@ def test_calls_on_two_streams_at_once():
             with torch.cuda.stream(st):
                 q, k, v, tables, lens = dev[i]
                 pkv.paged_attention_decode_kv4(q, k, v, tables, lens, cases[i].scale, outs[i],
-                                               max_context_len=cases[i].max_len, partition_tokens=128)
+                                               max_context_len=cases[i].max_len)
     torch.cuda.synchronize()
     assert pkv.device_error() == 0
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
