@@ -26,6 +26,7 @@ there is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -91,6 +92,8 @@ def declared_functions(header: str = HEADER) -> list[str]:
 def library():
     """The loaded libpagedkv.so (raises if it was never built)."""
     global _lib
+    if _lib is not None:  # set once, complete
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -464,29 +467,46 @@ def paged_kv_gather(k_cache, v_cache, block_tables, context_lens, k_out, v_out, 
 
 # ---- 4-bit caches and eviction: the tensors of a call share one device, which need not be
 # the current one, and a workspace that is not given comes from PyTorch's allocator at every
-# call (ordered on the call's stream and, inside a capture, kept by the graph).
+# call (ordered on the call's stream and, inside a capture, kept by the graph).  These calls
+# are short on the GPU, so the binding passes plain integers and asks PyTorch little.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # handle alone: 2 us less than the Stream object
 
 
-def _one_device(*ts):
-    _need_cuda(*ts)
-    if len({t.device for t in ts if t is not None}) != 1:
-        raise PagedKVError(1, "tensors must be on one device")
+def _one_device(first, *rest) -> int:
+    """The index of the CUDA device that all the (contiguous) tensors are on."""
+    device = first.get_device()
+    if device < 0 or not first.is_contiguous():
+        raise PagedKVError(1, "tensors must be contiguous CUDA tensors")
+    for t in rest:
+        if t is not None and (t.get_device() != device or not t.is_contiguous()):
+            raise PagedKVError(1, "tensors must be contiguous CUDA tensors on one device")
+    return device
 
 
-def _call(fn, tensor, *args) -> None:
-    """fn(*args, stream) with tensor's device current, on that device's current stream."""
-    if tensor.device.index == torch.cuda.current_device():
-        status = fn(*args, _stream(tensor))
+def _call(fn, device: int, *args) -> None:
+    """fn(*args, stream) with `device` current, on that device's current stream."""
+    stream = _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
+    if device == torch.cuda.current_device():
+        status = fn(*args, stream)
     else:
-        with torch.cuda.device(tensor.device):
-            status = fn(*args, _stream(tensor))
-    _check(status)
+        with torch.cuda.device(device):
+            status = fn(*args, stream)
+    if status:
+        _check(status)
 
 
-def _kv4_desc(k_cache, v_cache) -> CacheDesc:
+@functools.lru_cache(maxsize=512)
+def _desc_of(shape, dtype):
+    """A descriptor (never changed) of a pool of this shape and dtype, and a reference to it."""
+    desc = cache_desc(torch.empty(shape, dtype=dtype, device="meta"))
+    return desc, ctypes.byref(desc)
+
+
+def _kv4_desc(k_cache, v_cache):
     if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8 or k_cache.shape != v_cache.shape:
         raise PagedKVError(1, "the 4-bit pools must be uint8 and of one shape")
-    return cache_desc(k_cache)
+    return _desc_of(k_cache.shape, torch.uint8)
 
 
 def _dtype_code(t, what) -> int:
@@ -496,47 +516,48 @@ def _dtype_code(t, what) -> int:
     return code
 
 
+def _scratch(workspace, need: int, device: int):
+    """(address, bytes) of a call's workspace, and the tensor that holds it."""
+    if workspace is None:
+        if not need:
+            return 0, 0, None
+        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", device))
+        return workspace.data_ptr(), need, workspace
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
 def paged_kv4_append(k, v, slot_mapping, k_cache, v_cache) -> None:
     """k, v [T, Hkv, D] (f32, f16 or bf16) rounded to 4 bits -> the rows of the 4-bit pools
     (uint8 [NB, Hkv, bs, D * 5 / 8]) given by slot_mapping (int64 [T]; negative: skipped)."""
-    _one_device(k, v, slot_mapping, k_cache, v_cache)
-    desc = _kv4_desc(k_cache, v_cache)
+    device = _one_device(k, v, slot_mapping, k_cache, v_cache)
+    desc, desc_ref = _kv4_desc(k_cache, v_cache)
     if slot_mapping.dtype != torch.int64 or v.dtype != k.dtype:
         raise PagedKVError(1, "slot_mapping must be int64 and k and v of one dtype")
-    if k.shape != v.shape or k.dim() != 3 or k.shape[0] != slot_mapping.numel() \
-            or tuple(k.shape[1:]) != (desc.num_kv_heads, desc.head_dim):
+    tokens = slot_mapping.numel()
+    if k.shape != v.shape or tuple(k.shape) != (tokens, desc.num_kv_heads, desc.head_dim):
         raise PagedKVError(1, "shape mismatch between k, v, slot_mapping and the caches")
-    _call(library().paged_kv4_append, k_cache, _ptr(k), _ptr(v), _dtype_code(k, "k/v"), _ptr(slot_mapping),
-          slot_mapping.numel(), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc))
+    _call(library().paged_kv4_append, device, k.data_ptr(), v.data_ptr(), _dtype_code(k, "k/v"),
+          slot_mapping.data_ptr(), tokens, k_cache.data_ptr(), v_cache.data_ptr(), desc_ref)
 
 
 def paged_kv4_expand(src_dst_pairs, k_cache, v_cache, k_out, v_out) -> None:
     """Block dst of the pools k_out/v_out [NB', Hkv, bs, D] (f32, f16 or bf16) becomes the
     values of block src of the 4-bit pools, for each row of src_dst_pairs (int64 [n, 2])."""
-    _one_device(src_dst_pairs, k_cache, v_cache, k_out, v_out)
-    desc = _kv4_desc(k_cache, v_cache)
+    device = _one_device(src_dst_pairs, k_cache, v_cache, k_out, v_out)
+    _, desc_ref = _kv4_desc(k_cache, v_cache)
     if src_dst_pairs.dtype != torch.int64 or src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
         raise PagedKVError(1, "src_dst_pairs must be int64 [n, 2]")
     if v_out.dtype != k_out.dtype or v_out.shape != k_out.shape:
         raise PagedKVError(1, "k_out and v_out must be of one dtype and shape")
     _dtype_code(k_out, "out pool")
-    out_desc = cache_desc(k_out)
-    _call(library().paged_kv4_expand, k_cache, _ptr(src_dst_pairs), src_dst_pairs.shape[0], _ptr(k_cache),
-          _ptr(v_cache), ctypes.byref(desc), _ptr(k_out), _ptr(v_out), ctypes.byref(out_desc))
-
-
-def _scratch(workspace, need: int, device):
-    """(pointer, bytes) of a call's workspace, and the tensor that holds it."""
-    if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return _ptr(workspace), nbytes, workspace
+    _call(library().paged_kv4_expand, device, src_dst_pairs.data_ptr(), src_dst_pairs.shape[0], k_cache.data_ptr(),
+          v_cache.data_ptr(), desc_ref, k_out.data_ptr(), v_out.data_ptr(), _desc_of(k_out.shape, k_out.dtype)[1])
 
 
 def paged_attention_decode_kv4_workspace_bytes(num_seqs, num_q_heads, max_context_len, q_dtype, k_cache) -> int:
     """q_dtype: torch.float32, torch.float16 or torch.bfloat16."""
     return int(library().paged_attention_decode_kv4_workspace_bytes(
-        num_seqs, num_q_heads, max_context_len, DTYPE_CODE[q_dtype], ctypes.byref(_kv4_desc(k_cache, k_cache))))
+        num_seqs, num_q_heads, max_context_len, DTYPE_CODE[q_dtype], _kv4_desc(k_cache, k_cache)[1]))
 
 
 def paged_attention_decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out, *,
@@ -550,8 +571,8 @@ def paged_attention_decode_kv4(q, k_cache, v_cache, block_tables, context_lens, 
     context_lens (computed with a device sync when omitted).  workspace: uint8 device buffer
     of paged_attention_decode_kv4_workspace_bytes, allocated for the call when omitted.
     """
-    _one_device(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
-    desc = _kv4_desc(k_cache, v_cache)
+    device = _one_device(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    desc, desc_ref = _kv4_desc(k_cache, v_cache)
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise PagedKVError(1, "block_tables and context_lens must be int32")
     if q.dim() != 3 or out.shape != q.shape or q.shape[2] != desc.head_dim:
@@ -565,17 +586,17 @@ def paged_attention_decode_kv4(q, k_cache, v_cache, block_tables, context_lens, 
     lib = library()
     need = 0
     if workspace is None:
-        need = int(lib.paged_attention_decode_kv4_workspace_bytes(S, Hq, max_context_len, q_code, ctypes.byref(desc)))
-    ws, ws_bytes, workspace = _scratch(workspace, need, q.device)
-    _call(lib.paged_attention_decode_kv4, q, _ptr(q), q_code, _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-          block_tables.shape[1], _ptr(context_lens), S, Hq, max_context_len, float(scale), _ptr(out), out_code, ws,
-          ws_bytes, ctypes.byref(desc))
+        need = lib.paged_attention_decode_kv4_workspace_bytes(S, Hq, max_context_len, q_code, desc_ref)
+    ws, ws_bytes, workspace = _scratch(workspace, need, device)
+    _call(lib.paged_attention_decode_kv4, device, q.data_ptr(), q_code, k_cache.data_ptr(), v_cache.data_ptr(),
+          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, Hq, max_context_len, float(scale),
+          out.data_ptr(), out_code, ws, ws_bytes, desc_ref)
     return out
 
 
 def paged_attention_weights_workspace_bytes(num_seqs, num_q_heads, max_context_len, k_cache) -> int:
     return int(library().paged_attention_weights_workspace_bytes(num_seqs, num_q_heads, max_context_len,
-                                                                 ctypes.byref(cache_desc(k_cache))))
+                                                                 _desc_of(k_cache.shape, k_cache.dtype)[1]))
 
 
 def paged_attention_weights(q, k_cache, block_tables, context_lens, scale, weights, *,
@@ -592,8 +613,8 @@ def paged_attention_weights(q, k_cache, block_tables, context_lens, scale, weigh
     omitted).  workspace: uint8 device buffer, allocated for the call when omitted.
     """
     out = weights if weights_out is None else weights_out
-    _one_device(q, k_cache, block_tables, context_lens, weights, out, tracked_lens, workspace)
-    desc = cache_desc(k_cache)
+    device = _one_device(q, k_cache, block_tables, context_lens, weights, out, tracked_lens, workspace)
+    desc, desc_ref = _desc_of(k_cache.shape, k_cache.dtype)
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 \
             or (tracked_lens is not None and tracked_lens.dtype != torch.int32):
         raise PagedKVError(1, "block_tables, context_lens and tracked_lens must be int32")
@@ -612,11 +633,11 @@ def paged_attention_weights(q, k_cache, block_tables, context_lens, scale, weigh
     lib = library()
     need = 0
     if workspace is None:
-        need = int(lib.paged_attention_weights_workspace_bytes(S, Hq, max_context_len, ctypes.byref(desc)))
-    ws, ws_bytes, workspace = _scratch(workspace, need, q.device)
-    _call(lib.paged_attention_weights, q, _ptr(q), q_code, _ptr(k_cache), _ptr(block_tables), block_tables.shape[1],
-          _ptr(context_lens), _ptr(tracked_lens), S, Hq, max_context_len, float(scale), _ptr(weights), _ptr(out),
-          weights.shape[2], ws, ws_bytes, ctypes.byref(desc))
+        need = lib.paged_attention_weights_workspace_bytes(S, Hq, max_context_len, desc_ref)
+    ws, ws_bytes, workspace = _scratch(workspace, need, device)
+    _call(lib.paged_attention_weights, device, q.data_ptr(), q_code, k_cache.data_ptr(), block_tables.data_ptr(),
+          block_tables.shape[1], context_lens.data_ptr(), 0 if tracked_lens is None else tracked_lens.data_ptr(), S, Hq,
+          max_context_len, float(scale), weights.data_ptr(), out.data_ptr(), weights.shape[2], ws, ws_bytes, desc_ref)
     return out
 
 
@@ -633,8 +654,8 @@ def paged_kv_evict(weights, block_tables, context_lens, keep_lens, new_tables, k
     max_context_len: host upper bound on context_lens (computed with a device sync when
     omitted).
     """
-    _one_device(weights, block_tables, context_lens, keep_lens, new_tables, k_cache, v_cache, weights_out, kept)
-    desc = cache_desc(k_cache)
+    device = _one_device(weights, block_tables, context_lens, keep_lens, new_tables, k_cache, v_cache, weights_out, kept)
+    desc, desc_ref = _desc_of(k_cache.shape, k_cache.dtype)
     if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
         raise PagedKVError(1, "the caches must be of one shape and dtype")
     for t in (block_tables, context_lens, keep_lens, new_tables, kept):
@@ -649,9 +670,10 @@ def paged_kv_evict(weights, block_tables, context_lens, keep_lens, new_tables, k
         raise PagedKVError(1, "weights and weights_out must be float32 [S, Hkv, W]")
     if max_context_len is None:
         max_context_len = int(context_lens.max()) if S else 0
-    _call(library().paged_kv_evict, k_cache, _ptr(weights), _ptr(weights_out), weights.shape[2], _ptr(block_tables),
-          block_tables.shape[1], _ptr(context_lens), _ptr(keep_lens), recent, _ptr(new_tables), new_tables.shape[1], S,
-          max_context_len, kept.shape[2], _ptr(kept), _ptr(k_cache), _ptr(v_cache), ctypes.byref(desc))
+    _call(library().paged_kv_evict, device, weights.data_ptr(), weights_out.data_ptr(), weights.shape[2],
+          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), keep_lens.data_ptr(), recent,
+          new_tables.data_ptr(), new_tables.shape[1], S, max_context_len, kept.shape[2], kept.data_ptr(),
+          k_cache.data_ptr(), v_cache.data_ptr(), desc_ref)
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:
