@@ -71,10 +71,11 @@ pkv_status check_table_width(int32_t max_blocks, int32_t tokens, int32_t block_s
 
 struct WeightsPlan {
   int part_tokens, max_parts;
+  int64_t ld;  // of a query head's row of scores: whole 128-byte lines
   size_t ml_bytes, workspace;
 };
 
-// Partitions of the scores kernel: about twelve CTAs per SM, of 256 to 2,048 tokens.
+// Partitions of the scores kernel: about six CTAs per SM (two to six are resident), of 256 to 4,096 tokens.
 pkv_status plan_weights(int32_t num_seqs, int32_t num_q_heads, int32_t max_len, const pkv_cache_desc* c,
                         WeightsPlan* plan) {
   if (pkv_status st = check_cache(c, true)) return st;
@@ -88,12 +89,13 @@ pkv_status plan_weights(int32_t num_seqs, int32_t num_q_heads, int32_t max_len, 
   if (max_len < 0) return fail(PKV_ERR_INVALID_ARG, "max_context_len %d < 0", max_len);
   if (max_len > (1 << 30)) return fail(PKV_ERR_UNSUPPORTED, "max_context_len %d above 2^30", max_len);
   const int64_t work = static_cast<int64_t>(num_seqs) * c->num_kv_heads * (max_len / 2 + 1);
-  const int64_t per_cta = work / (12 * 152) + 1;
-  plan->part_tokens = static_cast<int>(per_cta < 256 ? 256 : per_cta > 2048 ? 2048 : (per_cta + 127) / 128 * 128);
+  const int64_t per_cta = work / (6 * 152) + 1;
+  plan->part_tokens = static_cast<int>(per_cta < 256 ? 256 : per_cta > 4096 ? 4096 : (per_cta + 127) / 128 * 128);
   plan->max_parts = max_len == 0 ? 1 : (max_len + plan->part_tokens - 1) / plan->part_tokens;
   const size_t heads = static_cast<size_t>(num_seqs) * num_q_heads;
   plan->ml_bytes = (heads * plan->max_parts * 2 * sizeof(float) + 255) / 256 * 256;
-  plan->workspace = num_seqs == 0 || max_len == 0 ? 0 : plan->ml_bytes + heads * max_len * sizeof(float);
+  plan->ld = (static_cast<int64_t>(max_len) + 31) / 32 * 32;
+  plan->workspace = num_seqs == 0 || max_len == 0 ? 0 : plan->ml_bytes + heads * plan->ld * sizeof(float);
   return PKV_OK;
 }
 
@@ -267,6 +269,7 @@ pkv_status paged_attention_weights(const void* q, int32_t q_dtype, const void* k
   p.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.ml_bytes);
   p.err = flag;
   p.width = weights_width;
+  p.scores_ld = plan.ld;
   p.q_dtype = q_dtype;
   p.num_seqs = num_seqs;
   p.num_q_heads = num_q_heads;

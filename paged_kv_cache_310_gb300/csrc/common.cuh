@@ -136,10 +136,10 @@ cudaError_t ensure_smem_limit(Kernel kernel, int bytes, std::atomic<unsigned lon
 }
 
 template <typename Kernel, typename Args>
-cudaError_t launch_dependent(Kernel kernel, int grid, int threads, int smem_bytes, cudaStream_t stream,
+cudaError_t launch_dependent(Kernel kernel, dim3 grid, int threads, int smem_bytes, cudaStream_t stream,
                              const Args& args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem_bytes;
   cfg.stream = stream;

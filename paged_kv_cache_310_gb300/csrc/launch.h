@@ -163,10 +163,10 @@ struct WeightsParams {
   const int32_t* tracked_lens;  // NULL: every row has an accumulator
   const float* weights;         // [S][Hkv][width]
   float* weights_out;           // may be weights
-  float* scores;                // workspace [S][Hkv][max_len][G]: log2-domain scores
+  float* scores;                // workspace [S][Hq][scores_ld]: log2-domain scores
   float* ws_ml;                 // workspace [S][Hq][max_parts][2]
   int* err;
-  int64_t width;
+  int64_t width, scores_ld;
   int32_t q_dtype, num_seqs, num_q_heads, num_kv_heads, group, max_blocks_per_seq;
   int32_t block_size, num_blocks, head_dim, max_len, part_tokens, max_parts;
   float scale_log2;

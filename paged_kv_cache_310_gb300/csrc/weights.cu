@@ -4,15 +4,18 @@
 //   out[s][g][j] = (j < tracked[s] ? w[s][g][j] : 0) + sum_h softmax_j(scale * q_h . K_j),
 // h over g's query heads.  The softmax needs its sum before any weight is known, so the
 // scores are looked at twice:
-//  * scores_kernel reads K once, a CTA per (partition, KV head, sequence): 16 tokens per
-//    warp and step, as in the decode kernels; scores (fp32, log2 domain) go to the
-//    workspace as [s][g][j][h] and each partition's (maximum, sum) beside them;
+//  * scores_kernel reads K once, a CTA per (partition, KV head, sequence): 32 tokens (16 of
+//    an f32 pool) per warp and step from a ring of cp.async stages; scores (fp32, log2
+//    domain) go to the workspace, a row of tokens per query head, and each partition's
+//    (maximum, sum) beside them;
 //  * weights_kernel joins the partitions' (maximum, sum) and adds up each token's weights.
 // Bound: HBM: K's row (2 D bytes in 16 bits, 5 D / 8 in four), 8 bytes of accumulator and
 // the scores' 8 G bytes, which mostly stay in L2 between the kernels.
 //
 // 16-bit pools go to m16n8k16 MMAs as they are, 4-bit ones are widened in registers
 // (kv4.cuh), f32 ones are multiplied on CUDA cores in fp32.
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "launch.h"
 #include "mma.cuh"
@@ -22,7 +25,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 16;
 constexpr int kFinishThreads = 256;
 constexpr int kFinishTokens = 1024;  // tokens per CTA of weights_kernel
 
@@ -33,25 +35,29 @@ constexpr int kKv4Split = 4;
 template <int KIND, int D>
 struct KPool {
   static constexpr bool kIsKv4 = KIND >= PKV_KV4;
+  static constexpr int kSub = KIND == PKV_F32 ? 1 : 2;  // MMA tiles of 16 tokens per step
+  static constexpr int kTile = 16 * kSub;
+  static constexpr int kEighths = 2 * kSub;  // groups of eight rows: never more than one block each
   static constexpr int kRow = kIsKv4 ? D * 5 / 8 : D * (KIND == PKV_F32 ? 4 : 2);
   static constexpr int kHalf = 8 * kRow;
-  static constexpr int kStage = 2 * kHalf;
-  static constexpr int kChunks = kStage / 16;
-  static constexpr int kPerLane = (kChunks + 31) / 32;
-  static constexpr int kRowChunks = kRow / 16;  // wide kinds
-  static constexpr int kStages = kStage >= 8192 ? 3 : kStage >= 4096 ? 4 : 8;
+  static constexpr int kPieces = kHalf / 16;
+  static constexpr int kLanes = 32 / kEighths;  // lanes that bring eight rows
+  static constexpr int kCopies = (kPieces + kLanes - 1) / kLanes;
+  static constexpr int kStage = kEighths * kHalf;
+  static constexpr int kStages = kStage >= 8192 ? 2 : kStage >= 4096 ? 3 : 4;
   static constexpr int kRingBytes = kWarps * kStages * kStage;
-  // shared offset of 16-byte piece c of a stage: wide rows are a multiple of 128 bytes, so
-  // odd rows swap the halves of each 128 bytes and eight lanes of two rows never share banks
-  __device__ static int place(int c) {
-    return (kIsKv4 ? c : c ^ (((c / (kIsKv4 ? 1 : kRowChunks)) & 1) << 2)) * 16;
-  }
+  static constexpr int kRowPieces = kIsKv4 ? kPieces : kRow / 16;
+  // Wide rows are a multiple of 128 bytes: odd rows swap the halves of each 128 bytes, so the
+  // eight lanes of two rows that load together never share banks.
+  static constexpr int swap(int row) { return kIsKv4 ? 0 : (row & 1) << 2; }
 };
 
 template <int KIND, int D, int NB>
 __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant__ WeightsParams p) {
   using C = KPool<KIND, D>;
   extern __shared__ __align__(128) unsigned char smem[];
+  __shared__ volatile uint32_t bit_patterns[3];
+  grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
   grid_dependents_launch();  // weights_kernel, which waits for this grid
 
   const int part = blockIdx.x, kvh = blockIdx.y, s = blockIdx.z;
@@ -65,55 +71,57 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   const int t0 = part * p.part_tokens;
   if (t0 >= L) return;
   const int ntok = min(p.part_tokens, L - t0);
-  const int ntiles = (ntok + kTile - 1) / kTile;
   const size_t q_row = static_cast<size_t>(s) * p.num_q_heads + static_cast<size_t>(kvh) * G;
 
   float* q_smem = reinterpret_cast<float*>(smem + C::kRingBytes);  // f32 pools: [G][D]
-  int* ids = reinterpret_cast<int*>(smem + C::kRingBytes + (KIND == PKV_F32 ? NB * 8 * D * 4 : 0));
-  const int bs_log2 = 31 - __clz(p.block_size);
+  // where each eight tokens' rows of this KV head start in the pool, in bytes
+  int64_t* offs = reinterpret_cast<int64_t*>(smem + C::kRingBytes + (KIND == PKV_F32 ? NB * 8 * D * 4 : 0));
   {
-    const int first = t0 >> bs_log2, nblk = (ntok + p.block_size - 1) >> bs_log2;
+    const int bs_log2 = 31 - __clz(p.block_size);
     const int32_t* row = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
-    for (int i = threadIdx.x; i < nblk; i += kThreads) {
-      int b = first + i < p.max_blocks_per_seq ? row[first + i] : -1;
+    for (int i = threadIdx.x; i < (ntok + 7) / 8; i += kThreads) {
+      const int tok = t0 + 8 * i, col = tok >> bs_log2;
+      int b = col < p.max_blocks_per_seq ? row[col] : -1;
       if (b < 0 || b >= p.num_blocks) {
         set_error(p.err, kErrIndex);
         b = 0;  // keep the copy in bounds; the flag reports the bad table
       }
-      ids[i] = b;
+      offs[i] = ((static_cast<int64_t>(b) * p.num_kv_heads + kvh) * p.block_size + (tok & (p.block_size - 1))) * C::kRow;
     }
     if (KIND == PKV_F32)
       for (int i = threadIdx.x; i < NB * 8 * D; i += kThreads)
         q_smem[i] = i < G * D ? static_cast<const float*>(p.q)[q_row * D + i] : 0.f;
+    if (threadIdx.x == 0) {  // in registers from here on: constant memory's port is slower
+      bit_patterns[0] = p.bits.low;
+      bit_patterns[1] = p.bits.high;
+      bit_patterns[2] = p.bits.one;
+    }
   }
   __syncthreads();
+  Kv4Bits bits;
+  bits.low = bit_patterns[0];
+  bits.high = bit_patterns[1];
+  bits.one = bit_patterns[2];
 
   unsigned char* ring = smem + warp * (C::kStages * C::kStage);
-  const uint32_t ring_addr = smem_addr(ring);
-  const int64_t tile_bytes = static_cast<int64_t>(p.block_size) * C::kRow;
-  const int64_t block_bytes = tile_bytes * p.num_kv_heads;
-  const unsigned char* pool = static_cast<const unsigned char*>(p.k_cache) + tile_bytes * kvh;
-  auto issue = [&](int tile, int stage) {
-    if (tile < ntiles) {
-      const int tok0 = tile * kTile, tok1 = tok0 + 8;
-      const bool have1 = tok1 < ntok;
-      const int at1 = have1 ? tok1 : tok0;
-      const unsigned char* src0 = pool + ids[tok0 >> bs_log2] * block_bytes + (tok0 & (p.block_size - 1)) * C::kRow;
-      const unsigned char* src1 = pool + ids[at1 >> bs_log2] * block_bytes + (at1 & (p.block_size - 1)) * C::kRow;
+  const int eighth = lane / C::kLanes, piece = lane % C::kLanes;
+  const uint32_t ring_addr = smem_addr(ring) + eighth * C::kHalf;
+  const unsigned char* pool = static_cast<const unsigned char*>(p.k_cache) + piece * 16;
+  auto issue = [&](int tile, uint32_t stage) {
+    const int tok = tile * C::kTile + 8 * eighth;
+    if (tile * C::kTile < ntok) {
+      const uint32_t bytes = tok < ntok ? 16u : 0u;  // eight rows past the end: zeros
+      const unsigned char* src = pool + offs[(tok < ntok ? tok : tile * C::kTile) / 8];
 #pragma unroll
-      for (int i = 0; i < C::kPerLane; ++i) {
-        const int c = lane + 32 * i;
-        if (C::kChunks % 32 == 0 || c < C::kChunks) {
-          const bool second = c >= C::kChunks / 2;
-          const unsigned char* src = (second ? src1 : src0) + (c - (second ? C::kChunks / 2 : 0)) * 16;
-          cp_async16(ring_addr + stage * C::kStage + C::place(c), src, second && !have1 ? 0u : 16u);
-        }
-      }
+      for (int i = 0; i < C::kCopies; ++i)
+        if (C::kLanes * (i + 1) <= C::kPieces || C::kLanes * i + piece < C::kPieces)
+          cp_async16(ring_addr + stage + ((piece ^ C::swap(C::kLanes * i / C::kRowPieces)) + C::kLanes * i) * 16,
+                     src + i * C::kLanes * 16, bytes);
     }
-    cp_async_commit();
+    cp_async_commit();  // one group per call, empty past the end: the waits below count them
   };
 #pragma unroll
-  for (int i = 0; i < C::kStages - 1; ++i) issue(warp + i * kWarps, i);
+  for (int i = 0; i < C::kStages - 1; ++i) issue(warp + i * kWarps, i * C::kStage);
 
   // ---- queries
   constexpr bool kMma = KIND != PKV_F32;
@@ -148,111 +156,151 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
     m[nb][0] = m[nb][1] = -INFINITY;
     l[nb][0] = l[nb][1] = 0.f;
   }
-  float* scores = p.scores + ((static_cast<size_t>(s) * p.num_kv_heads + kvh) * p.max_len + t0) * G;
+  float* scores = p.scores + q_row * p.scores_ld + t0;  // [head][token]
 
-  int stage = 0;
-  for (int tile = warp; tile < ntiles; tile += kWarps) {
+  uint32_t at = 0, refill = (C::kStages - 1) * C::kStage;  // stages, as offsets into the ring
+  auto step = [&](int tile, auto last) {
+    constexpr bool kLast = decltype(last)::value;  // the tile may end past the context
     cp_async_wait<C::kStages - 2>();
-    __syncwarp();
-    issue(tile + (C::kStages - 1) * kWarps, stage == 0 ? C::kStages - 1 : stage - 1);
-    const unsigned char* ks = ring + stage * C::kStage;
-    stage = stage + 1 == C::kStages ? 0 : stage + 1;
-    const int left = ntok - tile * kTile;
+    __syncwarp();  // the other lanes' copies too; and everybody has left the stage refilled next
+    issue(tile + (C::kStages - 1) * kWarps, refill);
+    refill = at;
+    const unsigned char* ks = ring + at;
+    at = at == (C::kStages - 1) * C::kStage ? 0 : at + C::kStage;
+    const int left = kLast ? ntok - tile * C::kTile : C::kTile;
 
-    float x[NB][4];  // rows g, g + 8; columns 2t, 2t + 1
-    if constexpr (kMma) {
-      float c[NB][2][4];
+    float x[NB][C::kSub][4];  // rows g, g + 8 of each tile of 16; columns 2t, 2t + 1
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+    for (int u = 0; u < C::kSub; ++u) {
+      const unsigned char* r0 = ks + 2 * u * C::kHalf + g * C::kRow;  // row g; row g + 8 is kHalf on
+      if constexpr (kMma) {
+        float c[NB][2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[nb][0][i] = c[nb][1][i] = 0.f;
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t a[4], b[4];  // rows g and g + 8: step 2i (0, 1), step 2i + 1 (2, 3)
+          for (int i = 0; i < 4; ++i) c[nb][0][i] = c[nb][1][i] = 0.f;
+        [[maybe_unused]] uint32_t w0[D / 32], w1[D / 32];
+        [[maybe_unused]] __half2 p0, p1;
         if constexpr (C::kIsKv4) {
-          const unsigned char* r0 = ks + g * C::kRow;
-          const int pair = D / 2 + 4 * (t * D / 128), word = t * (D / 8) + 4 * i;
-          const __half2 p0 = *reinterpret_cast<const __half2*>(r0 + pair);
-          const __half2 p1 = *reinterpret_cast<const __half2*>(r0 + C::kHalf + pair);
-          kv4_word(*reinterpret_cast<const uint32_t*>(r0 + word), __low2half2(p0), __high2half2(p0), p.bits, a);
-          kv4_word(*reinterpret_cast<const uint32_t*>(r0 + C::kHalf + word), __low2half2(p1), __high2half2(p1), p.bits, b);
-        } else {
-          const uint4 v0 = *reinterpret_cast<const uint4*>(ks + C::place(g * C::kRowChunks + t + 4 * i));
-          const uint4 v1 = *reinterpret_cast<const uint4*>(ks + C::place((g + 8) * C::kRowChunks + t + 4 * i));
-          a[0] = v0.x; a[1] = v0.y; a[2] = v0.z; a[3] = v0.w;
-          b[0] = v1.x; b[1] = v1.y; b[2] = v1.z; b[3] = v1.w;
+#pragma unroll
+          for (int i = 0; i < D / 32; i += D / 32 > 2 ? 4 : 2) {
+            if constexpr (D == 128) {
+              const uint4 a = *reinterpret_cast<const uint4*>(r0 + t * 16);
+              const uint4 b = *reinterpret_cast<const uint4*>(r0 + C::kHalf + t * 16);
+              w0[0] = a.x; w0[1] = a.y; w0[D / 32 - 2] = a.z; w0[D / 32 - 1] = a.w;
+              w1[0] = b.x; w1[1] = b.y; w1[D / 32 - 2] = b.z; w1[D / 32 - 1] = b.w;
+            } else {
+              const uint2 a = *reinterpret_cast<const uint2*>(r0 + t * 8);
+              const uint2 b = *reinterpret_cast<const uint2*>(r0 + C::kHalf + t * 8);
+              w0[0] = a.x; w0[1] = a.y;
+              w1[0] = b.x; w1[1] = b.y;
+            }
+          }
+          const int pair = D / 2 + 4 * (t * D / 128);
+          p0 = *reinterpret_cast<const __half2*>(r0 + pair);
+          p1 = *reinterpret_cast<const __half2*>(r0 + C::kHalf + pair);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t a[4], b[4];  // rows g and g + 8: step 2i (0, 1), step 2i + 1 (2, 3)
+          if constexpr (C::kIsKv4) {
+            kv4_word(w0[i], __low2half2(p0), __high2half2(p0), bits, a);
+            kv4_word(w1[i], __low2half2(p1), __high2half2(p1), bits, b);
+          } else {
+            const int off = ((t + 4 * i) ^ C::swap(g)) * 16;
+            const uint4 v0 = *reinterpret_cast<const uint4*>(r0 + off);
+            const uint4 v1 = *reinterpret_cast<const uint4*>(r0 + C::kHalf + off);
+            a[0] = v0.x; a[1] = v0.y; a[2] = v0.z; a[3] = v0.w;
+            b[0] = v1.x; b[1] = v1.y; b[2] = v1.z; b[3] = v1.w;
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            if constexpr (KIND == PKV_BF16) {
+              mma_bf16(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][2 * i][0], qh[nb][2 * i][1]);
+              mma_bf16(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][2 * i + 1][0], qh[nb][2 * i + 1][1]);
+            } else {
+              mma_f16(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][2 * i][0], qh[nb][2 * i][1]);
+              mma_f16(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][2 * i + 1][0], qh[nb][2 * i + 1][1]);
+            }
+            if constexpr (kSplit) {
+              mma_f16(c[nb][0], a[0], b[0], a[1], b[1], ql[nb][2 * i][0], ql[nb][2 * i][1]);
+              mma_f16(c[nb][1], a[2], b[2], a[3], b[3], ql[nb][2 * i + 1][0], ql[nb][2 * i + 1][1]);
+            }
+          }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[nb][u][i] = (c[nb][0][i] + c[nb][1][i]) * sc[nb][i & 1];
+      } else {
+        // fp32: lane t multiplies its quarter of rows g and g + 8 with every head's, then the
+        // four lanes add up and each keeps its two columns
+        float4 v0[D / 16], v1[D / 16];
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const int off = ((t + 4 * i) ^ C::swap(g)) * 16;
+          v0[i] = *reinterpret_cast<const float4*>(r0 + off);
+          v1[i] = *reinterpret_cast<const float4*>(r0 + C::kHalf + off);
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
-          if constexpr (KIND == PKV_BF16) {
-            mma_bf16(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][2 * i][0], qh[nb][2 * i][1]);
-            mma_bf16(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][2 * i + 1][0], qh[nb][2 * i + 1][1]);
-          } else {
-            mma_f16(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][2 * i][0], qh[nb][2 * i][1]);
-            mma_f16(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][2 * i + 1][0], qh[nb][2 * i + 1][1]);
-          }
-          if constexpr (kSplit) {
-            mma_f16(c[nb][0], a[0], b[0], a[1], b[1], ql[nb][2 * i][0], ql[nb][2 * i][1]);
-            mma_f16(c[nb][1], a[2], b[2], a[3], b[3], ql[nb][2 * i + 1][0], ql[nb][2 * i + 1][1]);
-          }
-        }
-      }
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb)
+          for (int h = 0; h < 8; ++h) {
+            if (nb * 8 + h >= G) break;  // warp-uniform
+            float2 a = make_float2(0.f, 0.f), b = a;  // even and odd elements
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[nb][i] = c[nb][0][i] + c[nb][1][i];
-    } else {
-      // fp32: lane t multiplies its quarter of rows g and g + 8 with every head's, then the
-      // four lanes add up and each keeps its two columns
-      float4 v0[D / 16], v1[D / 16];
-#pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        v0[i] = *reinterpret_cast<const float4*>(ks + C::place(g * C::kRowChunks + t + 4 * i));
-        v1[i] = *reinterpret_cast<const float4*>(ks + C::place((g + 8) * C::kRowChunks + t + 4 * i));
-      }
-#pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-        for (int h = 0; h < 8; ++h) {
-          if (nb * 8 + h >= G) break;  // warp-uniform
-          float a = 0.f, b = 0.f;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const float4 qv = *reinterpret_cast<const float4*>(q_smem + (nb * 8 + h) * D + (t + 4 * i) * 4);
-            a = fmaf(v0[i].x, qv.x, a); b = fmaf(v1[i].x, qv.x, b);
-            a = fmaf(v0[i].y, qv.y, a); b = fmaf(v1[i].y, qv.y, b);
-            a = fmaf(v0[i].z, qv.z, a); b = fmaf(v1[i].z, qv.z, b);
-            a = fmaf(v0[i].w, qv.w, a); b = fmaf(v1[i].w, qv.w, b);
-          }
-          a = group_sum<4>(a);
-          b = group_sum<4>(b);
-          if (t == h / 2) {
-            x[nb][h & 1] = a;
-            x[nb][2 + (h & 1)] = b;
+            for (int i = 0; i < D / 16; ++i) {
+              const float4 qv = *reinterpret_cast<const float4*>(q_smem + (nb * 8 + h) * D + (t + 4 * i) * 4);
+              const float2 q0 = make_float2(qv.x, qv.y), q1 = make_float2(qv.z, qv.w);
+              a = __ffma2_rn(make_float2(v0[i].x, v0[i].y), q0, a);
+              b = __ffma2_rn(make_float2(v1[i].x, v1[i].y), q0, b);
+              a = __ffma2_rn(make_float2(v0[i].z, v0[i].w), q1, a);
+              b = __ffma2_rn(make_float2(v1[i].z, v1[i].w), q1, b);
+            }
+            const float sa = group_sum<4>(a.x + a.y), sb = group_sum<4>(b.x + b.y);
+            if (t == h / 2) {
+              x[nb][u][h & 1] = sa * p.scale_log2;
+              x[nb][u][2 + (h & 1)] = sb * p.scale_log2;
+            }
           }
         }
       }
     }
 
+    // ---- store the scores, and the lane's running (maximum, sum) of its columns
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-      const int col = nb * 8 + 2 * t;
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = g + (i & 2) * 4, h = col + (i & 1), e = i & 1;
-        if (r < left && h < G) {
-          const float y = x[nb][i] * sc[nb][e];
-          scores[static_cast<size_t>(tile * kTile + r) * G + h] = y;
-          if (y > m[nb][e]) {
-            l[nb][e] *= exp2f(m[nb][e] - y);
-            m[nb][e] = y;
-          }
+      for (int e = 0; e < 2; ++e) {
+        const int h = nb * 8 + 2 * t + e;
+        if (h < G) {
+          float* to = scores + h * p.scores_ld + tile * C::kTile + g;
+          float top = m[nb][e];
+#pragma unroll
+          for (int u = 0; u < C::kSub; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float& y = x[nb][u][2 * i + e];
+              if (kLast && 16 * u + 8 * i + g >= left)
+                y = -INFINITY;
+              else
+                to[16 * u + 8 * i] = y;
+              top = fmaxf(top, y);
+            }
           // nothing seen yet but -inf: no weight (a NaN stays)
-          l[nb][e] += y == -INFINITY && m[nb][e] == -INFINITY ? 0.f : exp2f(y - m[nb][e]);
+          const float base = top == -INFINITY ? 0.f : top;
+          l[nb][e] *= exp2_approx(m[nb][e] - base);
+#pragma unroll
+          for (int u = 0; u < C::kSub; ++u)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) l[nb][e] += exp2_approx(x[nb][u][2 * i + e] - base);
+          m[nb][e] = top;
         }
       }
-    }
-  }
+  };
+  int tile = warp;
+  for (; (tile + 1) * C::kTile <= ntok; tile += kWarps) step(tile, std::false_type{});
+  if (tile * C::kTile < ntok) step(tile, std::true_type{});
   cp_async_wait<0>();
   __syncthreads();
 
@@ -265,7 +313,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
       float M = m[nb][e];
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      float sum = l[nb][e] == 0.f ? 0.f : l[nb][e] * exp2f(m[nb][e] - M);
+      float sum = l[nb][e] == 0.f ? 0.f : l[nb][e] * exp2_approx(m[nb][e] - M);
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       if (g == 0) {
@@ -282,7 +330,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float* r = red + (w * NB * 8 + threadIdx.x) * 2;
-      if (r[1] != 0.f) sum += r[1] * exp2f(r[0] - M);
+      if (r[1] != 0.f) sum += r[1] * exp2_approx(r[0] - M);
     }
     float* ml = p.ws_ml + ((q_row + threadIdx.x) * p.max_parts + part) * 2;
     ml[0] = M;
@@ -308,7 +356,7 @@ __global__ void __launch_bounds__(kFinishThreads) weights_kernel(const __grid_co
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     for (int i = lane; i < np; i += 32)
-      if (ml[i].y != 0.f) sum += ml[i].y * exp2f(ml[i].x - M);
+      if (ml[i].y != 0.f) sum += ml[i].y * exp2_approx(ml[i].x - M);
     sum = group_sum<32>(sum);
     if (lane == 0) {
       top[h] = M;
@@ -317,14 +365,31 @@ __global__ void __launch_bounds__(kFinishThreads) weights_kernel(const __grid_co
   }
   __syncthreads();
   const size_t row = static_cast<size_t>(s) * p.num_kv_heads + kvh;
-  const float* scores = p.scores + row * p.max_len * G;
-  const int end = min(L, j0 + kFinishTokens);
+  const float* scores = p.scores + row * G * p.scores_ld;
   const int tracked = p.tracked_lens ? p.tracked_lens[s] : L;
-  for (int j = j0 + threadIdx.x; j < end; j += kFinishThreads) {
-    float w = 0.f;
-    for (int h = 0; h < G; ++h) w = fmaf(exp2f(scores[static_cast<size_t>(j) * G + h] - top[h]), inverse[h], w);
-    const size_t at = row * p.width + j;
-    p.weights_out[at] = (j < tracked ? p.weights[at] : 0.f) + w;
+  constexpr int kEach = kFinishTokens / kFinishThreads;
+  float w[kEach], before[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int j = j0 + threadIdx.x + i * kFinishThreads;
+    w[i] = 0.f;
+    before[i] = j < L && j < tracked ? p.weights[row * p.width + j] : 0.f;
+  }
+#pragma unroll 4
+  for (int h = 0; h < G; ++h) {
+    float x[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int j = j0 + threadIdx.x + i * kFinishThreads;
+      x[i] = j < L ? scores[h * p.scores_ld + j] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) w[i] = fmaf(exp2_approx(x[i] - top[h]), inverse[h], w[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int j = j0 + threadIdx.x + i * kFinishThreads;
+    if (j < L) p.weights_out[row * p.width + j] = before[i] + w[i];
   }
 }
 
@@ -332,12 +397,12 @@ template <int KIND, int D, int NB>
 cudaError_t launch_t(const WeightsParams& p, cudaStream_t stream) {
   using C = KPool<KIND, D>;
   const size_t smem = C::kRingBytes + (KIND == PKV_F32 ? NB * 8 * D * 4 : 0) +
-                      static_cast<size_t>(p.part_tokens / p.block_size) * 4;
+                      static_cast<size_t>(p.part_tokens);  // 8 bytes per eight tokens
   static std::atomic<unsigned long long> configured{0};
   cudaError_t e = ensure_smem_limit(scores_kernel<KIND, D, NB>, 160 * 1024, configured);
   if (e != cudaSuccess) return e;
-  scores_kernel<KIND, D, NB><<<dim3(p.max_parts, p.num_kv_heads, p.num_seqs), kThreads, smem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(scores_kernel<KIND, D, NB>, dim3(p.max_parts, p.num_kv_heads, p.num_seqs), kThreads,
+                          static_cast<int>(smem), stream, p);
 }
 
 template <int KIND>
@@ -358,16 +423,9 @@ cudaError_t launch_weights(const WeightsParams& p, int dtype, cudaStream_t strea
     default: e = p.q_dtype == PKV_F32 ? launch_k<kKv4Split>(p, stream) : launch_k<PKV_KV4>(p, stream); break;
   }
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((p.max_len + kFinishTokens - 1) / kFinishTokens, p.num_kv_heads, p.num_seqs);
-  cfg.blockDim = dim3(kFinishThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weights_kernel, p);
+  return launch_dependent(weights_kernel,
+                          dim3((p.max_len + kFinishTokens - 1) / kFinishTokens, p.num_kv_heads, p.num_seqs),
+                          kFinishThreads, 0, stream, p);
 }
 
 }  // namespace pkv
