@@ -165,7 +165,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
   __shared__ int start_seq;
   __shared__ volatile uint32_t bit_patterns[3];
   grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
-  grid_dependents_launch();  // the join, which waits for this grid
+  if (p.desc) grid_dependents_launch();  // the join, which waits for this grid
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   const int G = p.group;

@@ -52,34 +52,72 @@ __device__ __forceinline__ void kv4_word(uint32_t w, __half2 step, __half2 lo, c
   out[3] = as_u32(__hfma2(high_codes(w, k), step, lo));
 }
 
-// Eight values of one group, held by four neighbouring lanes with eight each: returns the
-// lane's word of codes and the group's (step, lo) pair.
+// ---- rounding to 4 bits
+// Eight values of one group, held by four neighbouring lanes with eight each, become the
+// lane's word of codes and the group's (step, lo) pair:
 //   lo = fp16(min), step = fp16(fp32(max(0, max - lo) / 15)), each operation rounded once;
 //   code = the integer nearest to fp32(x - lo) / step (exact quotient, ties to even),
 //   held within 0..15; step 0 gives code 0.  A NaN or infinity makes step = lo = NaN.
-// The quotient's integer comes from a product with 1/step, off by at most one near a tie,
-// and is settled by the remainder d - c step, which one fma gives exactly (c step has at
-// most 15 bits, and the remainder no more than d or step): no division, no fp64.
-__device__ __forceinline__ uint32_t kv4_quantise8(float (&x)[8], __half2* pair) {
-  float mn = INFINITY, mx = -INFINITY;
-  bool bad = false;
+
+// Minimum, maximum and a NaN-or-infinity mark (not 0) of a lane's eight values.
+template <typename T>
+__device__ __forceinline__ void kv4_stats(const uint4* raw, const float (&x)[8], float* mn, float* mx, float* mark) {
+  *mn = *mx = x[0];
+  *mark = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    bad |= !(fabsf(x[i]) < INFINITY);
-    x[i] = fminf(fmaxf(x[i], -kKv4Largest), kKv4Largest);
-    mn = fminf(mn, x[i]);
-    mx = fmaxf(mx, x[i]);
+    *mn = fminf(*mn, x[i]);
+    *mx = fmaxf(*mx, x[i]);
+    *mark = fmaf(x[i], 0.f, *mark);
   }
-  uint32_t any_bad = bad;
+}
+// 16-bit values two at a time: their minimum and maximum are exact.
+template <typename H2, typename ToFloat2>
+__device__ __forceinline__ void kv4_stats_pairs(const uint4& raw, float* mn, float* mx, float* mark, H2 zero, ToFloat2 widen) {
+  const H2* h = reinterpret_cast<const H2*>(&raw);
+  H2 lo = h[0], hi = h[0], nan = __hfma2(h[0], zero, zero);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    lo = __hmin2(lo, h[i]);
+    hi = __hmax2(hi, h[i]);
+    nan = __hfma2(h[i], zero, nan);
+  }
+  const float2 a = widen(lo), b = widen(hi), c = widen(nan);
+  *mn = fminf(a.x, a.y);
+  *mx = fmaxf(b.x, b.y);
+  *mark = c.x + c.y;
+}
+template <>
+__device__ __forceinline__ void kv4_stats<__half>(const uint4* raw, const float (&)[8], float* mn, float* mx, float* mark) {
+  kv4_stats_pairs<__half2>(*raw, mn, mx, mark, __half2half2(__ushort_as_half(0)), [](__half2 v) { return __half22float2(v); });
+}
+template <>
+__device__ __forceinline__ void kv4_stats<__nv_bfloat16>(const uint4* raw, const float (&)[8], float* mn, float* mx,
+                                                         float* mark) {
+  kv4_stats_pairs<__nv_bfloat162>(*raw, mn, mx, mark, __bfloat162bfloat162(__ushort_as_bfloat16(0)),
+                                  [](__nv_bfloat162 v) { return __bfloat1622float2(v); });
+}
+
+// raw: the eight values in T (one uint4, or two for f32); x: the same as floats.
+template <typename T>
+__device__ __forceinline__ uint32_t kv4_quantise8(const uint4* raw, float (&x)[8], __half2* pair) {
+  float mn, mx, mark;
+  kv4_stats<T>(raw, x, &mn, &mx, &mark);
 #pragma unroll
   for (int off = 1; off < 4; off <<= 1) {
     mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    any_bad |= __shfl_xor_sync(0xffffffffu, any_bad, off);
+    mark += __shfl_xor_sync(0xffffffffu, mark, off);
   }
-  if (any_bad) {
+  if (!(mark == 0.f)) {  // 0 * infinity and 0 * NaN are NaN
     *pair = as_half2(0x7e007e00u);
     return 0u;
+  }
+  if (mx > kKv4Largest || mn < -kKv4Largest) {  // all four lanes of the group
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fminf(fmaxf(x[i], -kKv4Largest), kKv4Largest);
+    mn = fminf(fmaxf(mn, -kKv4Largest), kKv4Largest);
+    mx = fminf(fmaxf(mx, -kKv4Largest), kKv4Largest);
   }
   const __half lo16 = __float2half_rn(mn + 0.f);  // -0 becomes +0
   const float lo = __half2float(lo16);
@@ -87,12 +125,36 @@ __device__ __forceinline__ uint32_t kv4_quantise8(float (&x)[8], __half2* pair) 
   const float step = __half2float(step16);
   *pair = __halves2half2(step16, lo16);
   if (step == 0.f) return 0u;
-  const float inverse = __frcp_rn(step);
+
+  // The quotient over 15, held within 0..1, then its integer by adding 2^23, which rounds to
+  // nearest even at units; c = integer + 2^23.  Off by less than 2^-19 before the rounding
+  // (15 times a few 2^-24), so right unless the quotient is that near a tie.
+  const float inverse = __fdiv_rn(1.f, 15.f * step);  // 15 step has 15 bits: exact
+  constexpr float kUnits = 8388608.f;
   uint32_t word = 0;
+  float off_tie = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float d = x[i] - lo;
-    float c = fminf(fmaxf(rintf(d * inverse), 0.f), 15.f);
+    const float y = __saturatef((x[i] - lo) * inverse);
+    const float c = fmaf(y, 15.f, kUnits);
+    off_tie = fmaxf(off_tie, fabsf(fmaf(y, 15.f, kUnits - c)));
+    word += __float_as_uint(c) << (4 * i);
+  }
+  word -= 0x4b000000u;  // the bits of 2^23: those of the other seven left the word with the shifts
+  word -= 0x4b000000u << 4;
+  if (off_tie < 0.49999f) return word;
+
+  // Near a tie the remainder d - c step settles it, which one fma gives exactly (c step has at
+  // most 15 bits, and the remainder no more than d or step).
+  word = 0;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    float xi = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e == i) xi = x[e];
+    const float d = xi - lo;
+    float c = rintf(15.f * __saturatef(d * inverse));
     const float r2 = 2.f * fmaf(-c, step, d);
     const bool odd = static_cast<int>(c) & 1;
     if (r2 > step || (r2 == step && odd)) c += 1.f;

@@ -12,58 +12,70 @@ namespace {
 constexpr int kThreads = 256;
 
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+struct Raw8 {
+  static constexpr int kVecs = static_cast<int>(8 * sizeof(T) / 16);
+  uint4 v[kVecs];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 8; i += Elem<T>::kVec) Elem<T>::load16(p + i, x + i);
-}
+    for (int i = 0; i < kVecs; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void widen(float (&x)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; i += Elem<T>::kVec) Elem<T>::load16(&v[i / Elem<T>::kVec], x + i);
+  }
+};
 
 // One thread per eight values of one (token, KV head) row, of K and of V; four
-// neighbouring lanes share a group's minimum and maximum.  The thread count is a
-// multiple of 32 and whole warps take whole groups, so the shuffles see full warps: a
-// thread past the end or with a padding slot computes on zeros and stores nothing.
+// neighbouring lanes share a group's minimum and maximum.  blockIdx.x takes
+// tokens_per_cta tokens (several when a token has few values), blockIdx.y a part of a
+// token's (when it has many).  Threads past the end or with a padding slot work on what
+// they have and store nothing, so the shuffles always see whole warps.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_constant__ Kv4AppendParams p) {
-  grid_dependents_launch();  // a following decode's work may start; it waits for this grid before reading
-  const int per_row = p.head_dim / 8;
-  const int64_t per_token = static_cast<int64_t>(p.num_kv_heads) * per_row;
-  const int64_t total = per_token * p.num_tokens;
-  const int row_bytes = p.head_dim * 5 / 8;
-  const int64_t first = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
-  for (int64_t i = first; i - (threadIdx.x & 31) < total; i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    float k[8], v[8];
-    unsigned char* dst_k = nullptr;
-    unsigned char* dst_v = nullptr;
-    int c = 0;
-    if (i < total) {
-      const int64_t t = i / per_token;
-      const int rem = static_cast<int>(i - t * per_token);
-      const int h = rem / per_row;
-      c = rem - h * per_row;
-      load8(static_cast<const T*>(p.k) + i * 8, k);
-      load8(static_cast<const T*>(p.v) + i * 8, v);
-      const int64_t slot = p.slots[t];
-      if (slot >= p.num_slots) {
-        set_error(p.err, kErrIndex);
-      } else if (slot >= 0) {
-        const int64_t b = slot / p.block_size;
-        const int64_t row = (b * p.num_kv_heads + h) * p.block_size + (slot - b * p.block_size);
-        dst_k = static_cast<unsigned char*>(p.k_cache) + row * row_bytes;
-        dst_v = static_cast<unsigned char*>(p.v_cache) + row * row_bytes;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) k[e] = v[e] = 0.f;
-    }
-    __half2 pk, pv;
-    const uint32_t wk = kv4_quantise8(k, &pk), wv = kv4_quantise8(v, &pv);
-    if (dst_k) {
-      reinterpret_cast<uint32_t*>(dst_k)[c] = wk;
-      reinterpret_cast<uint32_t*>(dst_v)[c] = wv;
-      if ((c & 3) == 0) {
-        const int at = p.head_dim / 8 + c / 4;  // in words: the pairs follow the codes
-        reinterpret_cast<uint32_t*>(dst_k)[at] = as_u32(pk);
-        reinterpret_cast<uint32_t*>(dst_v)[at] = as_u32(pv);
-      }
+  grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
+  grid_dependents_launch();  // a following kernel's launch may overlap this one; it waits before reading
+  const int row_log2 = p.head_dim == 128 ? 4 : 3;  // threads per row
+  const int per_token = p.num_kv_heads << row_log2;
+  const int x = blockIdx.y * kThreads + threadIdx.x;
+  const int in_cta = x / per_token, rem = x - in_cta * per_token;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * p.tokens_per_cta + in_cta;
+  const int h = rem >> row_log2, c = rem & ((1 << row_log2) - 1);
+  const bool have = in_cta < p.tokens_per_cta && t < p.num_tokens;
+  Raw8<T> rk, rv;
+  int64_t slot = -1;
+  if (have) {
+    const int64_t at = (t * per_token + rem) * 8;
+    rk.load(static_cast<const T*>(p.k) + at);
+    rv.load(static_cast<const T*>(p.v) + at);
+    slot = p.slots[t];
+  } else {
+    rk.zero();
+    rv.zero();
+  }
+  float xs[8];
+  __half2 pk, pv;
+  rk.widen(xs);
+  const uint32_t wk = kv4_quantise8<T>(rk.v, xs, &pk);
+  rv.widen(xs);
+  const uint32_t wv = kv4_quantise8<T>(rv.v, xs, &pv);
+  if (slot >= p.num_slots) {
+    set_error(p.err, kErrIndex);
+  } else if (slot >= 0) {
+    const int bs_log2 = 31 - __clz(p.block_size);
+    const int64_t row = ((slot >> bs_log2) * p.num_kv_heads + h) * p.block_size + (slot & (p.block_size - 1));
+    const int words = p.head_dim * 5 / 32;  // 32-bit words of a row
+    uint32_t* dst_k = static_cast<uint32_t*>(p.k_cache) + row * words;
+    uint32_t* dst_v = static_cast<uint32_t*>(p.v_cache) + row * words;
+    dst_k[c] = wk;
+    dst_v[c] = wv;
+    if ((c & 3) == 0) {
+      const int at = p.head_dim / 8 + c / 4;  // the pairs follow the codes
+      dst_k[at] = as_u32(pk);
+      dst_v[at] = as_u32(pv);
     }
   }
 }
@@ -102,18 +114,20 @@ __device__ __forceinline__ void store8(__nv_bfloat16* out, const uint32_t (&v)[4
 // pairs_per_cta pairs (several when blocks are small), the CTAs along y share a block.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_expand_kernel(const __grid_constant__ Kv4ExpandParams p) {
-  const int words = p.head_dim / 8, row_words = words * 5 / 4;
+  grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
+  grid_dependents_launch();  // the next kernel's launch may overlap this one
+  const int words_log2 = p.head_dim == 128 ? 4 : 3, words = 1 << words_log2, row_words = words * 5 / 4;
   const int rows = p.num_kv_heads * p.block_size, total = rows * words;  // of one block
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.pairs_per_cta;
   const int items = static_cast<int>(min(static_cast<int64_t>(p.pairs_per_cta), p.num_pairs - first)) * total;
   for (int i = blockIdx.y * kThreads + threadIdx.x; i < items; i += gridDim.y * kThreads) {
-    const int which = i / total, rem = i - which * total;
+    const int which = p.pairs_per_cta == 1 ? 0 : i / total, rem = i - which * total;
     const int64_t src = p.pairs[2 * (first + which)], dst = p.pairs[2 * (first + which) + 1];
     if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_out_blocks) {
       set_error(p.err, kErrIndex);
       continue;
     }
-    const int row = rem / words, c = rem - row * words;
+    const int row = rem >> words_log2, c = rem & (words - 1);
     const int64_t base = src * rows * row_words;
     const int64_t at = base + row * row_words + c, pair = base + row * row_words + words + c / 4;
     const uint32_t wk = static_cast<const uint32_t*>(p.k_cache)[at], wv = static_cast<const uint32_t*>(p.v_cache)[at];
@@ -128,23 +142,19 @@ __global__ void __launch_bounds__(kThreads) kv4_expand_kernel(const __grid_const
   }
 }
 
-int grid_for(int64_t work, int cap) {
-  const int64_t g = (work + kThreads - 1) / kThreads;
-  return static_cast<int>(g < 1 ? 1 : (g > cap ? cap : g));
-}
-
 }  // namespace
 
-cudaError_t launch_kv4_append(const Kv4AppendParams& p, int dtype, cudaStream_t stream) {
+cudaError_t launch_kv4_append(Kv4AppendParams p, int dtype, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
-  const int64_t work = static_cast<int64_t>(p.num_tokens) * p.num_kv_heads * (p.head_dim / 8);
-  const int grid = grid_for(work, 152 * 16);
+  const int per_token = p.num_kv_heads * (p.head_dim / 8);
+  p.tokens_per_cta = per_token >= kThreads ? 1 : kThreads / per_token;
+  const dim3 grid((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta,
+                  per_token > kThreads ? (per_token + kThreads - 1) / kThreads : 1);
   switch (dtype) {
-    case PKV_F32: kv4_append_kernel<float><<<grid, kThreads, 0, stream>>>(p); break;
-    case PKV_F16: kv4_append_kernel<__half><<<grid, kThreads, 0, stream>>>(p); break;
-    default: kv4_append_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(p); break;
+    case PKV_F32: return launch_dependent(kv4_append_kernel<float>, grid, kThreads, 0, stream, p);
+    case PKV_F16: return launch_dependent(kv4_append_kernel<__half>, grid, kThreads, 0, stream, p);
+    default: return launch_dependent(kv4_append_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, p);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_kv4_expand(Kv4ExpandParams p, int dtype, cudaStream_t stream) {
@@ -154,11 +164,10 @@ cudaError_t launch_kv4_expand(Kv4ExpandParams p, int dtype, cudaStream_t stream)
   p.pairs_per_cta = total >= kPerCta ? 1 : kPerCta / total;
   const dim3 grid((p.num_pairs + p.pairs_per_cta - 1) / p.pairs_per_cta, total > kPerCta ? (total + kPerCta - 1) / kPerCta : 1);
   switch (dtype) {
-    case PKV_F32: kv4_expand_kernel<float><<<grid, kThreads, 0, stream>>>(p); break;
-    case PKV_F16: kv4_expand_kernel<__half><<<grid, kThreads, 0, stream>>>(p); break;
-    default: kv4_expand_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(p); break;
+    case PKV_F32: return launch_dependent(kv4_expand_kernel<float>, grid, kThreads, 0, stream, p);
+    case PKV_F16: return launch_dependent(kv4_expand_kernel<__half>, grid, kThreads, 0, stream, p);
+    default: return launch_dependent(kv4_expand_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, p);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace pkv

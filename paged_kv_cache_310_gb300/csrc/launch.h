@@ -115,8 +115,9 @@ struct Kv4AppendParams {
   int* err;
   int64_t num_slots;
   int32_t num_tokens, num_kv_heads, block_size, head_dim;
+  int32_t tokens_per_cta;  // set by the launcher
 };
-cudaError_t launch_kv4_append(const Kv4AppendParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_kv4_append(Kv4AppendParams p, int dtype, cudaStream_t stream);
 
 struct Kv4ExpandParams {
   const int64_t* pairs;

@@ -4,8 +4,8 @@
 //   out[s][g][j] = (j < tracked[s] ? w[s][g][j] : 0) + sum_h softmax_j(scale * q_h . K_j),
 // h over g's query heads.  The softmax needs its sum before any weight is known, so the
 // scores are looked at twice:
-//  * scores_kernel reads K once, a CTA per (partition, KV head, sequence): 32 tokens (16 of
-//    an f32 pool) per warp and step from a ring of cp.async stages; scores (fp32, log2
+//  * scores_kernel reads K once, a CTA per (partition, KV head, sequence): 16 tokens (32 of
+//    a 4-bit pool) per warp and step from a ring of cp.async stages; scores (fp32, log2
 //    domain) go to the workspace, a row of tokens per query head, and each partition's
 //    (maximum, sum) beside them;
 //  * weights_kernel joins the partitions' (maximum, sum) and adds up each token's weights.
@@ -25,8 +25,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kFinishThreads = 256;
-constexpr int kFinishTokens = 1024;  // tokens per CTA of weights_kernel
+constexpr int kFinishThreads = 128;
+constexpr int kFinishTokens = 512;  // tokens per CTA of weights_kernel
 
 // Kinds of pool: PKV_F32, PKV_F16, PKV_BF16, PKV_KV4 (f16 and bf16 queries), kKv4Split
 // (4-bit pool, f32 queries in two fp16 parts).
@@ -35,7 +35,7 @@ constexpr int kKv4Split = 4;
 template <int KIND, int D>
 struct KPool {
   static constexpr bool kIsKv4 = KIND >= PKV_KV4;
-  static constexpr int kSub = KIND == PKV_F32 ? 1 : 2;  // MMA tiles of 16 tokens per step
+  static constexpr int kSub = KIND >= PKV_KV4 ? 2 : 1;  // MMA tiles of 16 tokens per step
   static constexpr int kTile = 16 * kSub;
   static constexpr int kEighths = 2 * kSub;  // groups of eight rows: never more than one block each
   static constexpr int kRow = kIsKv4 ? D * 5 / 8 : D * (KIND == PKV_F32 ? 4 : 2);
@@ -44,12 +44,13 @@ struct KPool {
   static constexpr int kLanes = 32 / kEighths;  // lanes that bring eight rows
   static constexpr int kCopies = (kPieces + kLanes - 1) / kLanes;
   static constexpr int kStage = kEighths * kHalf;
-  static constexpr int kStages = kStage >= 8192 ? 2 : kStage >= 4096 ? 3 : 4;
+  static constexpr int kStages = kStage >= 8192 ? 2 : 3;
   static constexpr int kRingBytes = kWarps * kStages * kStage;
   static constexpr int kRowPieces = kIsKv4 ? kPieces : kRow / 16;
   // Wide rows are a multiple of 128 bytes: odd rows swap the halves of each 128 bytes, so the
   // eight lanes of two rows that load together never share banks.
-  static constexpr int swap(int row) { return kIsKv4 ? 0 : (row & 1) << 2; }
+  static_assert(kIsKv4 || kLanes % kRowPieces == 0 || kRowPieces % kLanes == 0, "a copy's rows");
+  __host__ __device__ static constexpr int swap(int row) { return kIsKv4 ? 0 : (row & 1) << 2; }
 };
 
 template <int KIND, int D, int NB>
@@ -114,9 +115,11 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
       const unsigned char* src = pool + offs[(tok < ntok ? tok : tile * C::kTile) / 8];
 #pragma unroll
       for (int i = 0; i < C::kCopies; ++i)
-        if (C::kLanes * (i + 1) <= C::kPieces || C::kLanes * i + piece < C::kPieces)
-          cp_async16(ring_addr + stage + ((piece ^ C::swap(C::kLanes * i / C::kRowPieces)) + C::kLanes * i) * 16,
-                     src + i * C::kLanes * 16, bytes);
+        if (C::kLanes * (i + 1) <= C::kPieces || C::kLanes * i + piece < C::kPieces) {
+          // the piece's row: one for all lanes, or two where a row has fewer pieces than there are lanes
+          const int row = C::kLanes * i / C::kRowPieces + (C::kLanes > C::kRowPieces ? piece / C::kRowPieces : 0);
+          cp_async16(ring_addr + stage + ((piece ^ C::swap(row)) + C::kLanes * i) * 16, src + i * C::kLanes * 16, bytes);
+        }
     }
     cp_async_commit();  // one group per call, empty past the end: the waits below count them
   };
@@ -338,7 +341,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   }
 }
 
-// One CTA per (1,024 tokens, KV head, sequence).
+// One CTA per (512 tokens, KV head, sequence).
 __global__ void __launch_bounds__(kFinishThreads) weights_kernel(const __grid_constant__ WeightsParams p) {
   __shared__ float top[16], inverse[16];
   grid_dependency_wait();
@@ -348,6 +351,28 @@ __global__ void __launch_bounds__(kFinishThreads) weights_kernel(const __grid_co
   if (L < 0 || L > p.max_len || j0 >= L) return;
   const int np = (L + p.part_tokens - 1) / p.part_tokens;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const size_t row = static_cast<size_t>(s) * p.num_kv_heads + kvh;
+  const float* scores = p.scores + row * G * p.scores_ld;
+  const int tracked = p.tracked_lens ? p.tracked_lens[s] : L;
+  constexpr int kEach = kFinishTokens / kFinishThreads, kHeads = 4;
+  // the first heads' scores and the accumulators are asked for before the partitions are joined
+  float w[kEach], before[kEach], x[kHeads][kEach];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int j = j0 + threadIdx.x + i * kFinishThreads;
+        x[h][i] = j < L && h0 + h < G ? scores[(h0 + h) * p.scores_ld + j] : 0.f;
+      }
+  };
+  load(0);
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int j = j0 + threadIdx.x + i * kFinishThreads;
+    w[i] = 0.f;
+    before[i] = j < L && j < tracked ? p.weights[row * p.width + j] : 0.f;
+  }
   for (int h = warp; h < G; h += kFinishThreads / 32) {
     const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) +
                        (static_cast<size_t>(s) * p.num_q_heads + static_cast<size_t>(kvh) * G + h) * p.max_parts;
@@ -364,27 +389,14 @@ __global__ void __launch_bounds__(kFinishThreads) weights_kernel(const __grid_co
     }
   }
   __syncthreads();
-  const size_t row = static_cast<size_t>(s) * p.num_kv_heads + kvh;
-  const float* scores = p.scores + row * G * p.scores_ld;
-  const int tracked = p.tracked_lens ? p.tracked_lens[s] : L;
-  constexpr int kEach = kFinishTokens / kFinishThreads;
-  float w[kEach], before[kEach];
+  for (int h0 = 0; h0 < G; h0 += kHeads) {
+    if (h0 > 0) load(h0);
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int j = j0 + threadIdx.x + i * kFinishThreads;
-    w[i] = 0.f;
-    before[i] = j < L && j < tracked ? p.weights[row * p.width + j] : 0.f;
-  }
-#pragma unroll 4
-  for (int h = 0; h < G; ++h) {
-    float x[kEach];
+    for (int h = 0; h < kHeads; ++h)
+      if (h0 + h < G) {
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int j = j0 + threadIdx.x + i * kFinishThreads;
-      x[i] = j < L ? scores[h * p.scores_ld + j] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) w[i] = fmaf(exp2_approx(x[i] - top[h]), inverse[h], w[i]);
+        for (int i = 0; i < kEach; ++i) w[i] = fmaf(exp2_approx(x[h][i] - top[h0 + h]), inverse[h0 + h], w[i]);
+      }
   }
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
