@@ -4,10 +4,11 @@
 // and, of the others, the k - r with the largest accumulated weight (NaN counts as
 // -infinity; equal weights: the lowest row first).  Kept rows keep their order.
 //  * select_kernel, one CTA per (KV head, sequence): the (k - r)-th largest weight by radix
-//    selection (four passes of eight bits over order-preserving integer keys), then one
-//    ordered pass that writes the kept rows' indices and weights.  A row's place is the
-//    number of heavier rows before it plus the number of equal ones, the latter held at
-//    how many of them are kept: one prefix sum of two packed counts.
+//    selection (up to four passes of eight bits over order-preserving integer keys, held in
+//    shared memory up to 48 Ki rows), then one ordered pass that writes the kept rows'
+//    indices and weights.  A row's place is the number of heavier rows before it plus the
+//    number of equal ones, the latter held at how many of them are kept: one prefix sum of
+//    two packed counts.  Bound: the latency of its passes, not bytes.
 //  * move_kernel copies the kept rows of K and V into the sequence's new blocks, 16 bytes
 //    (8 where rows are 40) per thread.  Bound: HBM; each kept row is read and written once.
 #include "common.cuh"
@@ -18,6 +19,7 @@ namespace {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kPerThread = 4;  // rows per thread and step of the ordered pass
+constexpr int kMaxKeys = 48 * 1024;  // rows whose keys fit in shared memory
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 64;  // kept rows per CTA
 
@@ -30,8 +32,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ EvictParams p) {
   __shared__ uint32_t hist[256];
   __shared__ uint32_t warp_sum[32];
-  __shared__ uint32_t found[2];  // digit, rows still to take among it
-  grid_dependents_launch();      // move_kernel, which waits for this grid
+  __shared__ uint32_t found[3];  // digit, rows still to take among it, rows that have it
+  extern __shared__ uint32_t keys[];
+  grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
+  grid_dependents_launch();  // move_kernel, which waits for this grid
   const int kvh = blockIdx.x, s = blockIdx.y;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int n = p.context_lens[s], keep = p.keep_lens[s];
@@ -49,12 +53,25 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   if (k - r == 0) {
     threshold = 0xffffffffu;  // no key is above it
   } else if (k - r < candidates) {
+    const bool held = candidates <= p.key_room;
+    if (held) {
+      constexpr int kBatch = 8;  // loads in flight per thread
+      for (int j0 = tid; j0 < candidates; j0 += kSelectThreads * kBatch) {
+        float x[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) x[i] = j0 + i * kSelectThreads < candidates ? w[j0 + i * kSelectThreads] : 0.f;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          if (j0 + i * kSelectThreads < candidates) keys[j0 + i * kSelectThreads] = weight_key(x[i]);
+      }  // each thread reads back only what it wrote
+    }
     uint32_t need = k - r;
     for (int shift = 24; shift >= 0; shift -= 8) {
       if (tid < 256) hist[tid] = 0;
       __syncthreads();
+#pragma unroll 4
       for (int j = tid; j < candidates; j += kSelectThreads) {
-        const uint32_t key = weight_key(w[j]);
+        const uint32_t key = held ? keys[j] : weight_key(w[j]);
         if (shift == 24 || (key >> (shift + 8)) == (threshold >> (shift + 8))) atomicAdd(&hist[(key >> shift) & 255], 1u);
       }
       __syncthreads();
@@ -78,6 +95,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
           if (above < need && above + c[i] >= need) {
             found[0] = 255 - (lane * 8 + i);
             found[1] = need - above;
+            found[2] = c[i];
           }
           above += c[i];
         }
@@ -85,7 +103,13 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
       __syncthreads();
       threshold |= found[0] << shift;
       need = found[1];
+      const bool all = found[2] == need;  // every row with these digits is kept: no need to look further
       __syncthreads();
+      if (all) {
+        threshold -= 1;  // >= 0x007fffff here, the key of -infinity
+        need = 0;
+        break;
+      }
     }
     ties = need;
   }
@@ -94,13 +118,23 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   int32_t* kept = p.kept + row * p.max_keep;
   float* out = p.weights_out + row * p.width;
   uint32_t above_before = 0, ties_before = 0;  // in the steps done
+  float x[kPerThread], ahead[kPerThread];
+  auto load = [&](int j0, float (&to)[kPerThread]) {
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      const int j = j0 + tid * kPerThread + i;
+      to[i] = j < n ? w[j] : 0.f;
+    }
+  };
+  load(0, ahead);
   for (int j0 = 0; j0 < n; j0 += kSelectThreads * kPerThread) {
     const int j = j0 + tid * kPerThread;
-    float x[kPerThread];
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) x[i] = ahead[i];
+    load(j0 + kSelectThreads * kPerThread, ahead);
     uint32_t count = 0, flag[kPerThread];  // rows above the threshold, and ties << 16
 #pragma unroll
     for (int i = 0; i < kPerThread; ++i) {
-      x[i] = j + i < n ? w[j + i] : 0.f;
       const uint32_t key = weight_key(x[i]);
       flag[i] = j + i >= n ? 0u : j + i >= candidates || key > threshold ? 1u : key == threshold && ties ? 0x10000u : 0u;
       count += flag[i];
@@ -175,23 +209,18 @@ template <typename V>
 cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
   const int most = p.max_keep < p.max_len ? p.max_keep : p.max_len;  // rows a sequence may keep
   if (most == 0) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((most + kMoveRows - 1) / kMoveRows, p.num_kv_heads, p.num_seqs);
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, move_kernel<V>, p);
+  return launch_dependent(move_kernel<V>, dim3((most + kMoveRows - 1) / kMoveRows, p.num_kv_heads, p.num_seqs),
+                          kMoveThreads, 0, stream, p);
 }
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
-  select_kernel<<<dim3(p.num_kv_heads, p.num_seqs), kSelectThreads, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
+  p.key_room = p.max_len < kMaxKeys ? p.max_len : kMaxKeys;
+  static std::atomic<unsigned long long> configured{0};
+  cudaError_t e = ensure_smem_limit(select_kernel, kMaxKeys * 4, configured);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(select_kernel, dim3(p.num_kv_heads, p.num_seqs), kSelectThreads, p.key_room * 4, stream, p);
   if (e != cudaSuccess) return e;
   return p.row_bytes % 16 == 0 ? launch_move<uint4>(p, stream) : launch_move<uint2>(p, stream);
 }

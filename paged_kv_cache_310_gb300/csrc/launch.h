@@ -190,7 +190,8 @@ struct EvictParams {
   int64_t width;
   int32_t num_seqs, num_kv_heads, max_blocks_per_seq, max_new_blocks;
   int32_t block_size, num_blocks, row_bytes, max_len, max_keep, recent;
+  int32_t key_room;  // rows whose keys a CTA holds in shared memory; set by the launcher
 };
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+cudaError_t launch_evict(EvictParams p, cudaStream_t stream);
 
 }  // namespace pkv

@@ -199,7 +199,8 @@ def test_evict_parity(pool, d, bs, recent):
     Evict(311_100 + bs + d, lens, keep, recent, 3, d, bs, pool, shared=True).check()
 
 
-@pytest.mark.parametrize("n,keep,recent", [(4097, 4096, 1), (9000, 17, 16), (20000, 10000, 100), (4096, 1, 0), (8192, 8000, 0)])
+@pytest.mark.parametrize("n,keep,recent", [(4097, 4096, 1), (9000, 17, 16), (20000, 10000, 100), (4096, 1, 0), (8192, 8000, 0),
+                                           (49152, 700, 5), (49153, 20001, 0), (70000, 33333, 1)])
 def test_evict_long(n, keep, recent):
     Evict(311_120, [n, 50], [keep, 20], recent, 1, 64, 16, "bf16").check()
 
@@ -209,6 +210,18 @@ def test_evict_equal_weights_keep_the_lowest_rows(value):
     c = Evict(311_130, [5000], [1234], 34, 2, 64, 8, "f16")
     c.w.fill_(value)
     c.check()
+
+
+def test_evict_weights_that_share_leading_bits():
+    # the threshold is found after one, two, three or four passes of eight bits
+    for bits in (0x3F800000, 0x3F000000, 0x00000000, 0xBF800000):
+        for spread in (0x01000000, 0x00010000, 0x00000100, 0x00000002):
+            c = Evict(311_135, [700], [300], 10, 2, 64, 8, "f16")
+            gen = torch.Generator().manual_seed(311_136)
+            k = torch.randint(0, spread, c.w.shape, generator=gen) + bits
+            k = torch.where(k >= 1 << 31, k - (1 << 32), k)
+            c.w = k.to(torch.int32).view(torch.float32).contiguous()
+            c.check()
 
 
 def test_evict_flags_bad_lengths_and_blocks():
