@@ -200,16 +200,18 @@ def test_evict_parity(pool, d, bs, recent):
 
 
 @pytest.mark.parametrize("n,keep,recent", [(4097, 4096, 1), (9000, 17, 16), (20000, 10000, 100), (4096, 1, 0), (8192, 8000, 0),
-                                           (49152, 700, 5), (49153, 20001, 0), (70000, 33333, 1)])
+                                           (49152, 700, 5), (49153, 20001, 0), (70000, 33333, 1), (8191, 8190, 8190),
+                                           (32768, 16384, 16384), (400001, 5, 2), (32767, 32767, 9)])
 def test_evict_long(n, keep, recent):
     Evict(311_120, [n, 50], [keep, 20], recent, 1, 64, 16, "bf16").check()
 
 
 @pytest.mark.parametrize("value", [0.0, 1.0, float("nan"), float("-inf"), float("inf")])
 def test_evict_equal_weights_keep_the_lowest_rows(value):
-    c = Evict(311_130, [5000], [1234], 34, 2, 64, 8, "f16")
-    c.w.fill_(value)
-    c.check()
+    for n, keep, heads in ((5000, 1234, 2), (20000, 12345, 1)):   # one CTA or a cluster a head
+        c = Evict(311_130, [n], [keep], 34, heads, 64, 8, "f16")
+        c.w.fill_(value)
+        c.check()
 
 
 def test_evict_weights_that_share_leading_bits():
