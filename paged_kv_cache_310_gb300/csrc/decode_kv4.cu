@@ -58,7 +58,11 @@ constexpr float kSlack = 8.f;      // a score may exceed the running maximum by 
 constexpr float kLift = 6.f;       // p = 2^(x - m + 6): small weights stay normal fp16 numbers
 
 // NB blocks of eight columns; kDup: at most four heads, in columns 0..3 and again in 4..7;
-// kSplit: f32 queries, in two fp16 parts.
+// kSplit: f32 queries, in two fp16 parts.  kRound (f32 outputs): a step's products are
+// summed by MMAs that start from zero and added to O by additions that round to nearest.
+// The MMA truncates its sums; O kept in its accumulator shrank by 0.5 of a unit in the last
+// place per MMA, 2.7e-6 of itself over 128 Ki tokens (1.2e-7 with kRound), which a 16-bit
+// output does not show; with it 128 sequences of 64/8 heads take 96 us in place of 90.
 template <int D, int NB, bool kDup, bool kSplit>
 struct Kv4 {
   static constexpr int kRow = Kv4Row<D>::kBytes;
@@ -155,7 +159,7 @@ __device__ __forceinline__ void store_pair(void* out, size_t i, float x, float y
   }
 }
 
-template <int D, int NB, bool kDup, bool kSplit>
+template <int D, int NB, bool kDup, bool kSplit, bool kRound>
 __global__ void __launch_bounds__(kThreads, Kv4<D, NB, kDup, kSplit>::kCtasPerSm)
 decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
   using C = Kv4<D, NB, kDup, kSplit>;
@@ -487,27 +491,66 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
     // ---- output
 #pragma unroll
     for (int u = 1; u < kSub; ++u) load_v(u);
+    auto pairs_of = [&](int u, __half2 (&step)[2], __half2 (&lo)[2]) {  // tokens (2t, 2t + 1), (2t + 8, 2t + 9)
 #pragma unroll
-    for (int u = 0; u < kSub; ++u) {
-      const __half2 step0 = as_half2(__byte_perm(pr[u][0], pr[u][1], 0x5410));
-      const __half2 lo0 = as_half2(__byte_perm(pr[u][0], pr[u][1], 0x7632));
-      const __half2 step1 = as_half2(__byte_perm(pr[u][2], pr[u][3], 0x5410));
-      const __half2 lo1 = as_half2(__byte_perm(pr[u][2], pr[u][3], 0x7632));
+      for (int e = 0; e < 2; ++e) {
+        step[e] = as_half2(__byte_perm(pr[u][2 * e], pr[u][2 * e + 1], 0x5410));
+        lo[e] = as_half2(__byte_perm(pr[u][2 * e], pr[u][2 * e + 1], 0x7632));
+      }
+    };
+    auto widen_v = [&](int u, int i, int j, const __half2 (&step)[2], const __half2 (&lo)[2], uint32_t (&a)[4]) {
+      const uint32_t sel = 0x4400u + 0x1111u * j;  // byte j of both words, twice each
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t x = __byte_perm(vw[u][2 * e][i], vw[u][2 * e + 1][i], sel);
+        a[2 * e] = as_u32(__hfma2(low_codes(x, bits), step[e], lo[e]));
+        a[2 * e + 1] = as_u32(__hfma2(high_codes(x, bits), step[e], lo[e]));
+      }
+    };
+    if constexpr (kRound) {
+      __half2 step[kSub][2], lo[kSub][2];
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) pairs_of(u, step[u], lo[u]);
 #pragma unroll
       for (int i = 0; i < kVWords; ++i) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint32_t sel = 0x4400u + 0x1111u * j;  // byte j of both words, twice each
-          const uint32_t x0 = __byte_perm(vw[u][0][i], vw[u][1][i], sel);
-          const uint32_t x1 = __byte_perm(vw[u][2][i], vw[u][3][i], sel);
-          const uint32_t a0 = as_u32(__hfma2(low_codes(x0, bits), step0, lo0));
-          const uint32_t a1 = as_u32(__hfma2(high_codes(x0, bits), step0, lo0));
-          const uint32_t a2 = as_u32(__hfma2(low_codes(x1, bits), step1, lo1));
-          const uint32_t a3 = as_u32(__hfma2(high_codes(x1, bits), step1, lo1));
+          float sum[NB][4];
 #pragma unroll
-          for (int nb = 0; nb < NB; ++nb) {
-            mma_f16(o[nb][4 * i + j], a0, a1, a2, a3, ph[nb][u][0], ph[nb][u][1]);
-            if (!kDup) mma_f16(o[nb][4 * i + j], a0, a1, a2, a3, pl[nb][u][0], pl[nb][u][1]);
+          for (int u = 0; u < kSub; ++u) {
+            uint32_t a[4];
+            widen_v(u, i, j, step[u], lo[u], a);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              if (u == 0)
+                mma_f16_first(sum[nb], a[0], a[1], a[2], a[3], ph[nb][u][0], ph[nb][u][1]);
+              else
+                mma_f16(sum[nb], a[0], a[1], a[2], a[3], ph[nb][u][0], ph[nb][u][1]);
+              if (!kDup) mma_f16(sum[nb], a[0], a[1], a[2], a[3], pl[nb][u][0], pl[nb][u][1]);
+            }
+          }
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nb][4 * i + j][e] += sum[nb][e];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < kSub; ++u) {
+        __half2 step[2], lo[2];
+        pairs_of(u, step, lo);
+#pragma unroll
+        for (int i = 0; i < kVWords; ++i) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a[4];
+            widen_v(u, i, j, step, lo, a);
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+              mma_f16(o[nb][4 * i + j], a[0], a[1], a[2], a[3], ph[nb][u][0], ph[nb][u][1]);
+              if (!kDup) mma_f16(o[nb][4 * i + j], a[0], a[1], a[2], a[3], pl[nb][u][0], pl[nb][u][1]);
+            }
           }
         }
       }
@@ -657,20 +700,27 @@ __global__ void __launch_bounds__(kJoinThreads) join_kv4_kernel(const __grid_con
   }
 }
 
-template <int D, int NB, bool kDup, bool kSplit>
+template <int D, int NB, bool kDup, bool kSplit, bool kRound>
 cudaError_t launch_t(const Kv4DecodeParams& p, cudaStream_t stream) {
   using C = Kv4<D, NB, kDup, kSplit>;
   static std::atomic<unsigned long long> configured{0};
-  cudaError_t e = ensure_smem_limit(decode_kv4_kernel<D, NB, kDup, kSplit>, C::kSmemBytes, configured);
+  cudaError_t e = ensure_smem_limit(decode_kv4_kernel<D, NB, kDup, kSplit, kRound>, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
-  return launch_dependent(decode_kv4_kernel<D, NB, kDup, kSplit>, p.ctas, kThreads, C::kSmemBytes, stream, p);
+  return launch_dependent(decode_kv4_kernel<D, NB, kDup, kSplit, kRound>, p.ctas, kThreads, C::kSmemBytes, stream, p);
 }
 
-template <int D, bool kSplit>
+template <int D, bool kSplit, bool kRound>
 cudaError_t launch_g(const Kv4DecodeParams& p, cudaStream_t stream) {
-  if (p.group <= 4) return launch_t<D, 1, true, kSplit>(p, stream);
-  if (p.group <= 8) return launch_t<D, 1, false, kSplit>(p, stream);
-  return launch_t<D, 2, false, kSplit>(p, stream);
+  if (p.group <= 4) return launch_t<D, 1, true, kSplit, kRound>(p, stream);
+  if (p.group <= 8) return launch_t<D, 1, false, kSplit, kRound>(p, stream);
+  return launch_t<D, 2, false, kSplit, kRound>(p, stream);
+}
+
+template <int D>
+cudaError_t launch_d(const Kv4DecodeParams& p, cudaStream_t stream) {
+  if (p.q_dtype == PKV_F32) return launch_g<D, true, true>(p, stream);  // f32 out as well
+  if (p.out_dtype == PKV_F32) return launch_g<D, false, true>(p, stream);
+  return launch_g<D, false, false>(p, stream);
 }
 
 }  // namespace
@@ -687,11 +737,7 @@ int kv4_decode_ctas(int head_dim, int group, int q_dtype, int64_t max_units, int
 }
 
 cudaError_t launch_decode_kv4(const Kv4DecodeParams& p, cudaStream_t stream) {
-  cudaError_t e;
-  if (p.q_dtype == PKV_F32)
-    e = p.head_dim == 64 ? launch_g<64, true>(p, stream) : launch_g<128, true>(p, stream);
-  else
-    e = p.head_dim == 64 ? launch_g<64, false>(p, stream) : launch_g<128, false>(p, stream);
+  const cudaError_t e = p.head_dim == 64 ? launch_d<64>(p, stream) : launch_d<128>(p, stream);
   if (e != cudaSuccess || !p.desc) return e;
   return launch_dependent(join_kv4_kernel, p.ctas, kJoinThreads, 0, stream, p);
 }
