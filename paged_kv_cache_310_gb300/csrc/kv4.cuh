@@ -121,24 +121,32 @@ __device__ __forceinline__ uint32_t kv4_quantise8(const uint4* raw, float (&x)[8
   }
   const __half lo16 = __float2half_rn(mn + 0.f);  // -0 becomes +0
   const float lo = __half2float(lo16);
-  const __half step16 = __float2half_rn(__fdiv_rn(fmaxf(0.f, mx - lo), 15.f));
+  // spread / 15, rounded once, by Markstein's method: a first quotient, its exact remainder by
+  // fma, and the correction (compared with a division for every mantissa: always equal)
+  const float spread = fmaxf(0.f, mx - lo);
+  constexpr float kFifteenth = 1.f / 15.f;
+  const float q0 = spread * kFifteenth;
+  const __half step16 = __float2half_rn(fmaf(fmaf(-15.f, q0, spread), kFifteenth, q0));
   const float step = __half2float(step16);
   *pair = __halves2half2(step16, lo16);
   if (step == 0.f) return 0u;
 
   // The quotient over 15, held within 0..1, then its integer by adding 2^23, which rounds to
-  // nearest even at units; c = integer + 2^23.  Off by less than 2^-19 before the rounding
-  // (15 times a few 2^-24), so right unless the quotient is that near a tie.
-  const float inverse = __fdiv_rn(1.f, 15.f * step);  // 15 step has 15 bits: exact
+  // nearest even at units; c = integer + 2^23.  Off by less than 2^-17 before the rounding
+  // (15 times a few 2^-23), so right unless the quotient is that near a tie.
+  const float inverse = __fdividef(1.f, 15.f * step);
   constexpr float kUnits = 8388608.f;
+  const float2 minus_lo = make_float2(-lo, -lo), fifteen = make_float2(15.f, 15.f), units = make_float2(kUnits, kUnits);
   uint32_t word = 0;
   float off_tie = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = __saturatef((x[i] - lo) * inverse);
-    const float c = fmaf(y, 15.f, kUnits);
-    off_tie = fmaxf(off_tie, fabsf(fmaf(y, 15.f, kUnits - c)));
-    word += __float_as_uint(c) << (4 * i);
+  for (int i = 0; i < 8; i += 2) {
+    const float2 d = __fadd2_rn(make_float2(x[i], x[i + 1]), minus_lo);
+    const float2 y = make_float2(__saturatef(d.x * inverse), __saturatef(d.y * inverse));
+    const float2 c = __ffma2_rn(y, fifteen, units);
+    const float2 off = __ffma2_rn(y, fifteen, __fadd2_rn(units, make_float2(-c.x, -c.y)));
+    off_tie = fmaxf(off_tie, fmaxf(fabsf(off.x), fabsf(off.y)));
+    word += (__float_as_uint(c.x) << (4 * i)) + (__float_as_uint(c.y) << (4 * i + 4));
   }
   word -= 0x4b000000u;  // the bits of 2^23: those of the other seven left the word with the shifts
   word -= 0x4b000000u << 4;
