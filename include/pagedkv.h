@@ -62,7 +62,8 @@
  *    for f16/bf16 and up to 8 for f32 (tf32 MMAs on split operands: scores to about
  *    2^-21 relative, within the f32 tolerance for logits of a few units; for logits
  *    of tens of units choose PKV_PATH_CUDA_CORE, fp32 throughout); prefill on tensor
- *    cores for f16/bf16, groups up to 16.
+ *    cores for f16/bf16, groups up to 16.  4-bit pools (PKV_KV4) and eviction have their
+ *    own calls below; block copies and swaps take 4-bit pools too.
  */
 #ifndef PAGEDKV_H
 #define PAGEDKV_H
@@ -301,7 +302,8 @@ pkv_status paged_kv_gather(const void* k_cache, const void* v_cache, const int32
  * values as D / 2 bytes of codes -- byte i: value 2i in the low half, 2i + 1 in the high
  * half -- and then D / 32 pairs (step, lo) of fp16, one for each group of 32 values.
  * Code c of a group stands for fp16(lo + c * step), rounded once (to nearest even).
- * paged_block_copy and paged_block_swap_out / _in take these pools like any other.
+ * paged_block_copy and paged_block_swap_out / _in take these pools like any other (a swap
+ * buffer's rows are then head_dim * 5 / 8 bytes).
  * ---------------------------------------------------------------------------------- */
 
 /*

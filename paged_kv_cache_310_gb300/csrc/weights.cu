@@ -25,8 +25,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kFinishThreads = 128;
-constexpr int kFinishTokens = 512;  // tokens per CTA of weights_kernel
+constexpr int kFinishThreads = 256;
+constexpr int kFinishTokens = 1024;  // tokens per CTA of weights_kernel
 
 // Kinds of pool: PKV_F32, PKV_F16, PKV_BF16, PKV_KV4 (f16 and bf16 queries), kKv4Split
 // (4-bit pool, f32 queries in two fp16 parts).
@@ -108,6 +108,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   const int eighth = lane / C::kLanes, piece = lane % C::kLanes;
   const uint32_t ring_addr = smem_addr(ring) + eighth * C::kHalf;
   const unsigned char* pool = static_cast<const unsigned char*>(p.k_cache) + piece * 16;
+  const uint64_t policy = policy_evict_first();  // K is read once; the scores should stay in L2
   auto issue = [&](int tile, uint32_t stage) {
     const int tok = tile * C::kTile + 8 * eighth;
     if (tile * C::kTile < ntok) {
@@ -118,7 +119,8 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
         if (C::kLanes * (i + 1) <= C::kPieces || C::kLanes * i + piece < C::kPieces) {
           // the piece's row: one for all lanes, or two where a row has fewer pieces than there are lanes
           const int row = C::kLanes * i / C::kRowPieces + (C::kLanes > C::kRowPieces ? piece / C::kRowPieces : 0);
-          cp_async16(ring_addr + stage + ((piece ^ C::swap(row)) + C::kLanes * i) * 16, src + i * C::kLanes * 16, bytes);
+          cp_async16_hint(ring_addr + stage + ((piece ^ C::swap(row)) + C::kLanes * i) * 16, src + i * C::kLanes * 16,
+                          bytes, policy);
         }
     }
     cp_async_commit();  // one group per call, empty past the end: the waits below count them
@@ -153,7 +155,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
     }
   }
 
-  float m[NB][2], l[NB][2];  // this lane's rows of its columns only
+  float m[NB][2], l[NB][2];  // the warp's maximum, this lane's rows' sum
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
     m[nb][0] = m[nb][1] = -INFINITY;
@@ -178,10 +180,6 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
       const unsigned char* r0 = ks + 2 * u * C::kHalf + g * C::kRow;  // row g; row g + 8 is kHalf on
       if constexpr (kMma) {
         float c[NB][2][4];
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) c[nb][0][i] = c[nb][1][i] = 0.f;
         [[maybe_unused]] uint32_t w0[D / 32], w1[D / 32];
         [[maybe_unused]] __half2 p0, p1;
         if constexpr (C::kIsKv4) {
@@ -218,9 +216,16 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
+            if (i == 0) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) c[nb][0][e] = c[nb][1][e] = 0.f;
+            }
             if constexpr (KIND == PKV_BF16) {
               mma_bf16(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][2 * i][0], qh[nb][2 * i][1]);
               mma_bf16(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][2 * i + 1][0], qh[nb][2 * i + 1][1]);
+            } else if (i == 0) {
+              mma_f16_first(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][0][0], qh[nb][0][1]);
+              mma_f16_first(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][1][0], qh[nb][1][1]);
             } else {
               mma_f16(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][2 * i][0], qh[nb][2 * i][1]);
               mma_f16(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][2 * i + 1][0], qh[nb][2 * i + 1][1]);
@@ -270,36 +275,47 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
       }
     }
 
-    // ---- store the scores, and the lane's running (maximum, sum) of its columns
+    // ---- store the scores; the warp's (maximum, sum) of its columns: the maximum is raised only
+    // when a score exceeds it by 8 (log2 domain), so sums hold powers up to 2^8
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb) {
+      float top = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int h = nb * 8 + 2 * t + e;
-        if (h < G) {
-          float* to = scores + h * p.scores_ld + tile * C::kTile + g;
-          float top = m[nb][e];
+        float* to = scores + h * p.scores_ld + tile * C::kTile + g;
 #pragma unroll
-          for (int u = 0; u < C::kSub; ++u)
+        for (int u = 0; u < C::kSub; ++u)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              float& y = x[nb][u][2 * i + e];
-              if (kLast && 16 * u + 8 * i + g >= left)
-                y = -INFINITY;
-              else
-                to[16 * u + 8 * i] = y;
-              top = fmaxf(top, y);
-            }
-          // nothing seen yet but -inf: no weight (a NaN stays)
-          const float base = top == -INFINITY ? 0.f : top;
-          l[nb][e] *= exp2_approx(m[nb][e] - base);
+          for (int i = 0; i < 2; ++i) {
+            float& y = x[nb][u][2 * i + e];
+            if (h >= G || (kLast && 16 * u + 8 * i + g >= left))
+              y = -INFINITY;
+            else
+              to[16 * u + 8 * i] = y;
+            top = fmaxf(top, y - m[nb][e]);
+          }
+      }
+      if (__any_sync(0xffffffffu, top > 8.f)) {  // m = -inf: any finite score
 #pragma unroll
-          for (int u = 0; u < C::kSub; ++u)
+        for (int e = 0; e < 2; ++e) {
+          float M = m[nb][e];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) l[nb][e] += exp2_approx(x[nb][u][2 * i + e] - base);
-          m[nb][e] = top;
+          for (int u = 0; u < C::kSub; ++u) M = fmaxf(M, fmaxf(x[nb][u][e], x[nb][u][2 + e]));
+#pragma unroll
+          for (int off = 4; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+          if (M != m[nb][e]) l[nb][e] *= exp2_approx(m[nb][e] - M);
+          m[nb][e] = M;
         }
       }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // nothing seen yet but -inf: no weight (a NaN stays)
+        const float base = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
+#pragma unroll
+        for (int u = 0; u < C::kSub; ++u) l[nb][e] += exp2_approx(x[nb][u][e] - base) + exp2_approx(x[nb][u][2 + e] - base);
+      }
+    }
   };
   int tile = warp;
   for (; (tile + 1) * C::kTile <= ntok; tile += kWarps) step(tile, std::false_type{});
@@ -313,10 +329,8 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float M = m[nb][e];
-#pragma unroll
-      for (int off = 4; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-      float sum = l[nb][e] == 0.f ? 0.f : l[nb][e] * exp2_approx(m[nb][e] - M);
+      const float M = m[nb][e];
+      float sum = l[nb][e];
 #pragma unroll
       for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       if (g == 0) {
@@ -341,41 +355,40 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   }
 }
 
-// One CTA per (512 tokens, KV head, sequence).
-__global__ void __launch_bounds__(kFinishThreads) weights_kernel(const __grid_constant__ WeightsParams p) {
-  __shared__ float top[16], inverse[16];
-  grid_dependency_wait();
-  const int kvh = blockIdx.y, s = blockIdx.z, G = p.group;
-  const int L = p.context_lens[s];
-  const int j0 = blockIdx.x * kFinishTokens;
-  if (L < 0 || L > p.max_len || j0 >= L) return;
-  const int np = (L + p.part_tokens - 1) / p.part_tokens;
+// One CTA per (1,024 tokens, KV head, sequence); a thread adds up four tokens, 256 apart, so
+// that every load and store is a whole line per warp whatever the rows' alignment.
+// kWhole: all of the CTA's tokens are within the context (no test per load).
+template <bool kWhole>
+__device__ __forceinline__ void sum_weights(const WeightsParams& p, int s, int kvh, int L, float2* join) {
+  const int G = p.group, j0 = blockIdx.x * kFinishTokens + threadIdx.x;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const size_t row = static_cast<size_t>(s) * p.num_kv_heads + kvh;
-  const float* scores = p.scores + row * G * p.scores_ld;
   const int tracked = p.tracked_lens ? p.tracked_lens[s] : L;
   constexpr int kEach = kFinishTokens / kFinishThreads, kHeads = 4;
   // the first heads' scores and the accumulators are asked for before the partitions are joined
   float w[kEach], before[kEach], x[kHeads][kEach];
-  auto load = [&](int h0) {
+  const float* from = p.scores + row * G * p.scores_ld + j0;
+  auto load = [&](int heads) {
 #pragma unroll
     for (int h = 0; h < kHeads; ++h)
+      if (h < heads) {
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) {
-        const int j = j0 + threadIdx.x + i * kFinishThreads;
-        x[h][i] = j < L && h0 + h < G ? scores[(h0 + h) * p.scores_ld + j] : 0.f;
+        for (int i = 0; i < kEach; ++i)
+          x[h][i] = kWhole || j0 + i * kFinishThreads < L ? from[i * kFinishThreads] : 0.f;
+        from += p.scores_ld;
       }
   };
-  load(0);
+  load(G);
+  const float* acc = p.weights + row * p.width + j0;
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
-    const int j = j0 + threadIdx.x + i * kFinishThreads;
+    const int j = j0 + i * kFinishThreads;
     w[i] = 0.f;
-    before[i] = j < L && j < tracked ? p.weights[row * p.width + j] : 0.f;
+    before[i] = (kWhole || j < L) && j < tracked ? acc[i * kFinishThreads] : 0.f;
   }
+  const int np = (L + p.part_tokens - 1) / p.part_tokens;
   for (int h = warp; h < G; h += kFinishThreads / 32) {
-    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) +
-                       (static_cast<size_t>(s) * p.num_q_heads + static_cast<size_t>(kvh) * G + h) * p.max_parts;
+    const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) + (row * G + h) * p.max_parts;
     float M = -INFINITY, sum = 0.f;
     for (int i = lane; i < np; i += 32) M = fmaxf(M, ml[i].x);
 #pragma unroll
@@ -383,26 +396,36 @@ __global__ void __launch_bounds__(kFinishThreads) weights_kernel(const __grid_co
     for (int i = lane; i < np; i += 32)
       if (ml[i].y != 0.f) sum += ml[i].y * exp2_approx(ml[i].x - M);
     sum = group_sum<32>(sum);
-    if (lane == 0) {
-      top[h] = M;
-      inverse[h] = 1.f / sum;
-    }
+    if (lane == 0) join[h] = make_float2(M, 1.f / sum);
   }
   __syncthreads();
   for (int h0 = 0; h0 < G; h0 += kHeads) {
-    if (h0 > 0) load(h0);
+    if (h0 > 0) load(G - h0);
 #pragma unroll
     for (int h = 0; h < kHeads; ++h)
       if (h0 + h < G) {
+        const float2 ml = join[h0 + h];
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) w[i] = fmaf(exp2_approx(x[h][i] - top[h0 + h]), inverse[h0 + h], w[i]);
+        for (int i = 0; i < kEach; ++i) w[i] = fmaf(exp2_approx(x[h][i] - ml.x), ml.y, w[i]);
       }
   }
+  float* out = p.weights_out + row * p.width + j0;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int j = j0 + threadIdx.x + i * kFinishThreads;
-    if (j < L) p.weights_out[row * p.width + j] = before[i] + w[i];
-  }
+  for (int i = 0; i < kEach; ++i)
+    if (kWhole || j0 + i * kFinishThreads < L) out[i * kFinishThreads] = before[i] + w[i];
+}
+
+__global__ void __launch_bounds__(kFinishThreads) weights_kernel(const __grid_constant__ WeightsParams p) {
+  __shared__ float2 join[kWeightsMaxGroup];  // (maximum, 1 / sum) of a query head
+  grid_dependency_wait();
+  const int kvh = blockIdx.y, s = blockIdx.z;
+  const int L = p.context_lens[s];
+  const int j0 = blockIdx.x * kFinishTokens;
+  if (L < 0 || L > p.max_len || j0 >= L) return;
+  if (j0 + kFinishTokens <= L)
+    sum_weights<true>(p, s, kvh, L, join);
+  else
+    sum_weights<false>(p, s, kvh, L, join);
 }
 
 template <int KIND, int D, int NB>
