@@ -351,7 +351,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
     const int left = kLast ? L - first - i_tile * kUnit : kTile;  // tokens of this tile
 
     // ---- scores
-    float c[NB][kSub][2][4];
+    float c[NB][kSub][4];
 #pragma unroll
     for (int u = 0; u < kSub; ++u) {
       constexpr int kWords = D / 32;
@@ -381,16 +381,16 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
         for (int nb = 0; nb < NB; ++nb) {
           const uint4 q = q_lane[(nb * (kSplit ? 2 : 1) * (D / 32) + i) * 32];
           if (i == 0) {
-            mma_f16_first(c[nb][u][0], a[0], b[0], a[1], b[1], q.x, q.y);
-            mma_f16_first(c[nb][u][1], a[2], b[2], a[3], b[3], q.z, q.w);
+            mma_f16_first(c[nb][u], a[0], b[0], a[1], b[1], q.x, q.y);
+            mma_f16(c[nb][u], a[2], b[2], a[3], b[3], q.z, q.w);
           } else {
-            mma_f16(c[nb][u][0], a[0], b[0], a[1], b[1], q.x, q.y);
-            mma_f16(c[nb][u][1], a[2], b[2], a[3], b[3], q.z, q.w);
+            mma_f16(c[nb][u], a[0], b[0], a[1], b[1], q.x, q.y);
+            mma_f16(c[nb][u], a[2], b[2], a[3], b[3], q.z, q.w);
           }
           if (kSplit) {
             const uint4 r = q_lane[((nb * 2 + 1) * (D / 32) + i) * 32];
-            mma_f16(c[nb][u][0], a[0], b[0], a[1], b[1], r.x, r.y);
-            mma_f16(c[nb][u][1], a[2], b[2], a[3], b[3], r.z, r.w);
+            mma_f16(c[nb][u], a[0], b[0], a[1], b[1], r.x, r.y);
+            mma_f16(c[nb][u], a[2], b[2], a[3], b[3], r.z, r.w);
           }
         }
       }
@@ -430,7 +430,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
       for (int u = 0; u < kSub; ++u)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[u][i] = fmaf(c[nb][u][0][i] + c[nb][u][1][i], sc[nb][i & 1], i & 1 ? mb : ma);
+          x[u][i] = fmaf(c[nb][u][i], sc[nb][i & 1], i & 1 ? mb : ma);
           if (kLast && u * 16 + g + (i & 2) * 4 >= left) x[u][i] = -INFINITY;
           top = fmaxf(top, x[u][i]);
         }
@@ -441,7 +441,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
         for (int u = 0; u < kSub; ++u)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x[u][i] = (c[nb][u][0][i] + c[nb][u][1][i]) * sc[nb][i & 1];
+            x[u][i] = c[nb][u][i] * sc[nb][i & 1];
             if (kLast && u * 16 + g + (i & 2) * 4 >= left) x[u][i] = -INFINITY;
             top2[i & 1] = fmaxf(top2[i & 1], x[u][i]);
           }
