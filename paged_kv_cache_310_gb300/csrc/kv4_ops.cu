@@ -162,7 +162,8 @@ cudaError_t launch_kv4_expand(Kv4ExpandParams p, int dtype, cudaStream_t stream)
   constexpr int kPerCta = 4 * kThreads;  // words a CTA takes: four rounds of its threads
   const int total = p.num_kv_heads * p.block_size * (p.head_dim / 8);
   p.pairs_per_cta = total >= kPerCta ? 1 : kPerCta / total;
-  const dim3 grid((p.num_pairs + p.pairs_per_cta - 1) / p.pairs_per_cta, total > kPerCta ? (total + kPerCta - 1) / kPerCta : 1);
+  const int parts = total > kPerCta ? (total + kPerCta - 1) / kPerCta : 1;  // CTAs that share a block
+  const dim3 grid((p.num_pairs + p.pairs_per_cta - 1) / p.pairs_per_cta, parts < 1024 ? parts : 1024);
   switch (dtype) {
     case PKV_F32: return launch_dependent(kv4_expand_kernel<float>, grid, kThreads, 0, stream, p);
     case PKV_F16: return launch_dependent(kv4_expand_kernel<__half>, grid, kThreads, 0, stream, p);
