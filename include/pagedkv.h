@@ -345,7 +345,8 @@ pkv_status paged_kv4_expand(const int64_t* src_dst_pairs, int32_t num_pairs, con
  * q: device [num_seqs][num_q_heads][head_dim] of q_dtype (f32, f16 or bf16); out: q's
  * dtype or f32; query-head groups up to 16.  Softmax, sums and products in fp32: q in fp16
  * (f32 q in two fp16 parts) after a power-of-two scaling of each head's row, weights in
- * two fp16 parts, so the result is good to a few 2^-22 before the output's rounding.
+ * two fp16 parts, so the result is good to a few 2^-22 before the output's rounding (bf16
+ * outputs: one fp16 part, each weight within 2^-12 of itself).
  * n == 0 gives zeros.  A NaN or infinity in a query row, or a NaN in a row attended to,
  * gives NaN as the formula does.  A sequence longer than max_context_len sets the device
  * index flag and is skipped.  The batch's tokens are shared out evenly among the CTAs,
@@ -353,7 +354,8 @@ pkv_status paged_kv4_expand(const int64_t* src_dst_pairs, int32_t num_pairs, con
  * workspace: at least paged_attention_decode_kv4_workspace_bytes(...) bytes (0 when
  * max_context_len <= 128), 256-byte aligned, one per call in flight; its size does not grow
  * with the batch or the lengths past a limit of some 20 MB.  The result does not depend on
- * which physical blocks hold a sequence.  out must not alias any input.
+ * which physical blocks hold a sequence; where a sequence is cut depends on the lengths of
+ * the whole batch, which can change its last bits.  out must not alias any input.
  */
 size_t paged_attention_decode_kv4_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
                                                   int32_t q_dtype, const pkv_cache_desc* cache);
@@ -378,7 +380,7 @@ pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void
  * Rows j >= n are not written.  tracked_lens (device int32 [num_seqs], or NULL = every
  * row): how many of a sequence's rows have an accumulator yet; the newer ones start at 0.
  * weights, weights_out: device f32 [num_seqs][num_kv_heads][weights_width],
- * weights_width >= max_context_len; they may be the same buffer.
+ * weights_width >= max_context_len; they may be the same buffer, but not overlap otherwise.
  * q: device [num_seqs][num_q_heads][head_dim] of q_dtype, which is the cache's dtype; a
  * PKV_KV4 pool takes f32, f16 or bf16.  Query-head groups up to 16.  fp32 throughout
  * (products of 16-bit operands are exact).  A sequence longer than max_context_len sets
@@ -486,16 +488,19 @@ pkv_status pkv_bm_swap_in(pkv_block_manager* manager, int64_t seq_id, int32_t* b
                           int32_t* num_out);
 
 /*
- * Eviction: the sequence gets ceil(new_len / block_size) fresh private blocks, listed in
- * logical order in blocks_out (capacity entries, *num_out set), none of them one it held,
- * and drops its references to the old ones (blocks nobody else holds become free).  Take
- * its old table first; paged_kv_evict then moves the kept rows from there.  new_len at most
- * its length.  The old blocks may be handed out again at once: issue the eviction before
+ * Eviction: each of n distinct sequences gets ceil(new_lens[i] / block_size) fresh private
+ * blocks, in order of sequence and position in blocks_out (capacity entries, *num_out set),
+ * and drops its references to the old ones (blocks nobody else holds become free).  No fresh
+ * block is an old one of any of the n: sequences that one paged_kv_evict shortens are
+ * compacted in one call (one by one, a sequence's fresh blocks may be those that the one
+ * before has just left, which the eviction still reads).  Take the old tables first;
+ * paged_kv_evict then moves the kept rows from there.  new_lens[i] at most the sequence's
+ * length.  The old blocks may be handed out again at once: issue the eviction before
  * anything that writes to them on the same stream.  PKV_ERR_OUT_OF_BLOCKS if the pool
  * cannot hold the fresh blocks beside the old ones (nothing changes).
  */
-pkv_status pkv_bm_compact(pkv_block_manager* manager, int64_t seq_id, int64_t new_len, int32_t* blocks_out,
-                          int32_t capacity, int32_t* num_out);
+pkv_status pkv_bm_compact(pkv_block_manager* manager, const int64_t* seq_ids, const int64_t* new_lens, int32_t n,
+                          int32_t* blocks_out, int32_t capacity, int32_t* num_out);
 
 /* Rows of block_tables ([n][max_blocks], -1 padded) and context_lens for n sequences. */
 pkv_status pkv_bm_block_tables(const pkv_block_manager* manager, const int64_t* seq_ids, int32_t n,

@@ -123,19 +123,21 @@ class BlockManagerModel:
         self.add_sequence(seq, n)
         return list(self.tables[seq])
 
-    def compact(self, seq: int, new_len: int) -> list[int]:
-        """Evicted down to new_len tokens: fresh private blocks, then the old ones released."""
-        need = -(-new_len // self.block_size)
-        if need > len(self.free):
+    def compact(self, seqs, new_lens) -> list[list[int]]:
+        """Evicted down to new_lens tokens: fresh private blocks for all, then the old ones released."""
+        if sum(-(-n // self.block_size) for n in new_lens) > len(self.free):
             raise OutOfBlocks
         fresh = []
-        for i in range(need):
-            b = self._take()
-            self.filled[b] = min(self.block_size, new_len - i * self.block_size)
-            fresh.append(b)
-        self.free_sequence(seq)
-        self.tables[seq], self.lens[seq] = fresh, new_len
-        return list(fresh)
+        for n in new_lens:
+            fresh.append([])
+            for i in range(-(-n // self.block_size)):
+                b = self._take()
+                self.filled[b] = min(self.block_size, n - i * self.block_size)
+                fresh[-1].append(b)
+        for seq, n, blocks in zip(seqs, new_lens, fresh):
+            self.free_sequence(seq)
+            self.tables[seq], self.lens[seq] = list(blocks), n
+        return fresh
 
     def stats(self) -> dict:
         used = [b for b in range(self.num_blocks) if self.refs[b] > 0]

@@ -38,7 +38,7 @@ def _lib():
         lib.pkv_bm_stats.argtypes = [vp, ctypes.POINTER(BlockStats)]
         lib.pkv_bm_swap_out.argtypes = [vp, i64, vp, i32, ctypes.POINTER(i32)]
         lib.pkv_bm_swap_in.argtypes = [vp, i64, vp, i32, ctypes.POINTER(i32)]
-        lib.pkv_bm_compact.argtypes = [vp, i64, i64, vp, i32, ctypes.POINTER(i32)]
+        lib.pkv_bm_compact.argtypes = [vp, vp, vp, i32, vp, i32, ctypes.POINTER(i32)]
         for n in ("pkv_bm_create", "pkv_bm_add_sequence", "pkv_bm_fork", "pkv_bm_append",
                   "pkv_bm_free_sequence", "pkv_bm_block_tables", "pkv_bm_stats", "pkv_bm_swap_out",
                   "pkv_bm_swap_in", "pkv_bm_compact"):
@@ -103,14 +103,21 @@ class BlockManager:
         """Restore into fresh blocks (copy the data back with paged_block_swap_in)."""
         return self._blocks_call(self._lib.pkv_bm_swap_in, seq_id)
 
-    def compact(self, seq_id: int, new_len: int) -> list:
-        """Evict down to new_len tokens: the sequence's fresh blocks (take its old table first,
-        then move the kept rows with paged_kv_evict); the old blocks are released."""
+    def compact(self, seq_ids, new_lens) -> list:
+        """Evict sequences down to new_lens tokens: each one's list of fresh blocks.  Take the
+        old tables first, then move the kept rows with paged_kv_evict; the old blocks are
+        released.  Sequences shortened by one paged_kv_evict are compacted in one call, so
+        that no fresh block is one that the eviction still reads."""
+        ids, lens = (torch.tensor(list(x), dtype=torch.int64) for x in (seq_ids, new_lens))
+        if ids.numel() != lens.numel():
+            raise PagedKVError(1, "as many new_lens as seq_ids wanted")
         cap = self.num_blocks
         out = torch.empty(cap, dtype=torch.int32)
         n = ctypes.c_int32(0)
-        _check(self._lib.pkv_bm_compact(self._h, seq_id, new_len, out.data_ptr(), cap, ctypes.byref(n)))
-        return out[:n.value].tolist()
+        _check(self._lib.pkv_bm_compact(self._h, ids.data_ptr(), lens.data_ptr(), ids.numel(), out.data_ptr(), cap,
+                                        ctypes.byref(n)))
+        blocks = iter(out[:n.value].tolist())
+        return [[next(blocks) for _ in range(-(-x // self.block_size))] for x in lens.tolist()]
 
     def block_tables(self, seq_ids, max_blocks: int | None = None):
         """(block_tables int32 [n, max_blocks] padded with -1, context_lens int32 [n])."""

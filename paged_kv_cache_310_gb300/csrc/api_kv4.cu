@@ -62,6 +62,11 @@ pkv_status check_workspace(const void* workspace, size_t given, size_t need) {
   return PKV_OK;
 }
 
+bool overlap(const float* x, const float* y, size_t floats) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y), bytes = floats * sizeof(float);
+  return a < b + bytes && b < a + bytes;
+}
+
 pkv_status check_table_width(int32_t max_blocks, int32_t tokens, int32_t block_size, const char* what) {
   const int64_t need = (static_cast<int64_t>(tokens) + block_size - 1) / block_size;
   if (max_blocks < need)
@@ -252,6 +257,9 @@ pkv_status paged_attention_weights(const void* q, int32_t q_dtype, const void* k
   if (weights_width < max_context_len)
     return fail(PKV_ERR_INVALID_ARG, "weights_width %lld < max_context_len %d", static_cast<long long>(weights_width),
                 max_context_len);
+  if (weights != weights_out &&
+      overlap(weights, weights_out, static_cast<size_t>(num_seqs) * cache->num_kv_heads * weights_width))
+    return fail(PKV_ERR_INVALID_ARG, "weights_out overlaps weights without being it");
   if (pkv_status st = check_table_width(max_blocks_per_seq, max_context_len, cache->block_size, "max_blocks_per_seq"))
     return st;
   if (pkv_status st = check_workspace(workspace, workspace_bytes, plan.workspace)) return st;
@@ -306,10 +314,10 @@ pkv_status paged_kv_evict(const float* weights, float* weights_out, int64_t weig
   if (weights_width < max_context_len)
     return fail(PKV_ERR_INVALID_ARG, "weights_width %lld < max_context_len %d", static_cast<long long>(weights_width),
                 max_context_len);
-  const uintptr_t a = reinterpret_cast<uintptr_t>(weights), b = reinterpret_cast<uintptr_t>(weights_out);
-  const size_t bytes = static_cast<size_t>(num_seqs) * cache->num_kv_heads * weights_width * sizeof(float);
-  if ((a | b) & 3u) return fail(PKV_ERR_INVALID_ARG, "weights must be 4-byte aligned");
-  if (a < b + bytes && b < a + bytes) return fail(PKV_ERR_INVALID_ARG, "weights_out overlaps weights");
+  if ((reinterpret_cast<uintptr_t>(weights) | reinterpret_cast<uintptr_t>(weights_out)) & 3u)
+    return fail(PKV_ERR_INVALID_ARG, "weights must be 4-byte aligned");
+  if (overlap(weights, weights_out, static_cast<size_t>(num_seqs) * cache->num_kv_heads * weights_width))
+    return fail(PKV_ERR_INVALID_ARG, "weights_out overlaps weights");
   if (pkv_status st = check_table_width(max_blocks_per_seq, max_context_len, cache->block_size, "max_blocks_per_seq"))
     return st;
   const int32_t most = max_keep < max_context_len ? max_keep : max_context_len;  // rows a sequence may keep

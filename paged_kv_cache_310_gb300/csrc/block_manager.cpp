@@ -217,28 +217,53 @@ pkv_status pkv_bm_swap_in(pkv_block_manager* m, int64_t seq_id, int32_t* blocks_
   return PKV_OK;
 }
 
-pkv_status pkv_bm_compact(pkv_block_manager* m, int64_t seq_id, int64_t new_len, int32_t* blocks_out, int32_t capacity,
-                          int32_t* num_out) {
-  if (!m || !num_out) return err(PKV_ERR_INVALID_ARG, "NULL argument");
-  auto it = m->seqs.find(seq_id);
-  if (it == m->seqs.end()) return err(PKV_ERR_INVALID_ARG, "unknown (or swapped) sequence id");
-  auto& s = it->second;
-  if (new_len < 0 || new_len > s.len) return err(PKV_ERR_INVALID_ARG, "new_len outside 0 .. the sequence's length");
-  const int64_t need = blocks_for(new_len, m->block_size);
-  if (need > capacity || (need > 0 && !blocks_out)) return err(PKV_ERR_INVALID_ARG, "blocks_out too small");
-  if (need > static_cast<int64_t>(m->free_stack.size()))
-    return err(PKV_ERR_OUT_OF_BLOCKS, "not enough free blocks for the shortened sequence");
-  // the fresh blocks first, so that none of them is an old one; need <= the number of old
-  // blocks, so their list takes the fresh ones without growing, and the pushes onto the free
-  // stack stay within the capacity it was created with: nothing here allocates or throws
-  for (int64_t i = 0; i < need; ++i) blocks_out[i] = take_block(m);
-  for (auto b = s.blocks.rbegin(); b != s.blocks.rend(); ++b) release_block(m, *b);
-  s.blocks.resize(static_cast<size_t>(need));
-  for (int64_t i = 0; i < need; ++i) {
-    s.blocks[i] = blocks_out[i];
-    m->filled[blocks_out[i]] = static_cast<int32_t>(std::min<int64_t>(m->block_size, new_len - i * m->block_size));
+pkv_status pkv_bm_compact(pkv_block_manager* m, const int64_t* seq_ids, const int64_t* new_lens, int32_t n,
+                          int32_t* blocks_out, int32_t capacity, int32_t* num_out) {
+  if (!m || !num_out || (n > 0 && (!seq_ids || !new_lens))) return err(PKV_ERR_INVALID_ARG, "NULL argument");
+  if (n < 0) return err(PKV_ERR_INVALID_ARG, "n < 0");
+  // first pass: validate and count, so failure changes nothing; a sequence met already is
+  // marked by its length's complement, taken back below
+  int64_t need = 0;
+  int32_t met = 0;
+  const char* wrong = nullptr;
+  for (; met < n; ++met) {
+    auto it = m->seqs.find(seq_ids[met]);
+    if (it == m->seqs.end()) {
+      wrong = "unknown (or swapped) sequence id";
+    } else if (it->second.len < 0) {
+      wrong = "a sequence appears twice in one compaction";
+    } else if (new_lens[met] < 0 || new_lens[met] > it->second.len) {
+      wrong = "new length outside 0 .. the sequence's length";
+    }
+    if (wrong) break;
+    need += blocks_for(new_lens[met], m->block_size);
+    it->second.len = ~it->second.len;
   }
-  s.len = new_len;
+  for (int32_t i = 0; i < met; ++i) {
+    auto& s = m->seqs.find(seq_ids[i])->second;
+    s.len = ~s.len;
+  }
+  if (wrong) return err(PKV_ERR_INVALID_ARG, wrong);
+  if (need > static_cast<int64_t>(m->free_stack.size()))
+    return err(PKV_ERR_OUT_OF_BLOCKS, "not enough free blocks for the shortened sequences");
+  if (need > capacity || (need > 0 && !blocks_out)) return err(PKV_ERR_INVALID_ARG, "blocks_out too small");
+  // every fresh block before any old one is released, so that no sequence's fresh block is one
+  // that another of them is read from.  A sequence needs at most as many as it held, so its list
+  // takes them without growing, and the pushes onto the free stack stay within the capacity it
+  // was created with: nothing here allocates or throws
+  for (int64_t i = 0; i < need; ++i) blocks_out[i] = take_block(m);
+  const int32_t* fresh = blocks_out;
+  for (int32_t i = 0; i < n; ++i) {
+    auto& s = m->seqs.find(seq_ids[i])->second;
+    const int64_t count = blocks_for(new_lens[i], m->block_size);
+    for (auto b = s.blocks.rbegin(); b != s.blocks.rend(); ++b) release_block(m, *b);
+    s.blocks.resize(static_cast<size_t>(count));
+    for (int64_t j = 0; j < count; ++j) {
+      s.blocks[j] = *fresh++;
+      m->filled[s.blocks[j]] = static_cast<int32_t>(std::min<int64_t>(m->block_size, new_lens[i] - j * m->block_size));
+    }
+    s.len = new_lens[i];
+  }
   *num_out = static_cast<int32_t>(need);
   return PKV_OK;
 }

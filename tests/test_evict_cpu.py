@@ -75,18 +75,20 @@ def test_compact_matches_the_model(seed):
             ref.free_sequence(s)
             bm.free_sequence(s)
         else:
-            s = rng.choice(live)
-            old, n = list(ref.tables[s]), rng.randint(0, ref.lens[s])
+            ids = rng.sample(live, min(len(live), rng.randint(1, 3)))
+            old = {b for s in ids for b in ref.tables[s]}
+            lens = [rng.randint(0, ref.lens[s]) for s in ids]
             try:
-                want = ref.compact(s, n)
+                want = ref.compact(ids, lens)
             except OutOfBlocks:
                 before = bm.stats()
                 with pytest.raises(PagedKVError) as e:
-                    bm.compact(s, n)
+                    bm.compact(ids, lens)
                 assert e.value.status == 7 and bm.stats() == before
             else:
-                got = bm.compact(s, n)
-                assert got == want and not set(got) & set(old)
+                got = bm.compact(ids, lens)
+                # no fresh block is one that an eviction of these sequences reads
+                assert got == want and not {b for x in got for b in x} & old
                 compacted += 1
         same_state(bm, ref)
     assert compacted > 20
@@ -95,19 +97,33 @@ def test_compact_matches_the_model(seed):
 def test_compact_refusals():
     bm = BlockManager(8, 4)
     bm.add_sequence(1, 10)
-    before = bm.stats()
-    for args in ((2, 1), (1, 11), (1, -1)):
+    bm.add_sequence(2, 5)
+
+    def state():
+        return bm.stats(), [x.tolist() for x in bm.block_tables([1, 2])]
+
+    before = state()
+    for args in (([3], [1]), ([1], [11]), ([1], [-1]), ([1, 2], [4, 6]), ([2, 1, 2], [1, 1, 1]), ([1, 3], [1, 1]), ([1], [1, 1])):
         with pytest.raises(PagedKVError) as e:
             bm.compact(*args)
-        assert e.value.status == 1 and bm.stats() == before
+        assert e.value.status == 1 and state() == before
+    with pytest.raises(PagedKVError) as e:
+        bm.compact([1, 2], [9, 5])                            # five fresh blocks, three free
+    assert e.value.status == 7 and state() == before
     lib, n = pkv.library(), ctypes.c_int32(0)
     out = (ctypes.c_int32 * 8)()
-    assert lib.pkv_bm_compact(None, 1, 1, out, 8, ctypes.byref(n)) == 1
-    assert lib.pkv_bm_compact(bm._h, 1, 5, out, 1, ctypes.byref(n)) == 1      # two blocks wanted
-    assert lib.pkv_bm_compact(bm._h, 1, 5, None, 8, ctypes.byref(n)) == 1
-    assert lib.pkv_bm_compact(bm._h, 1, 5, out, 8, None) == 1
-    assert bm.stats() == before
-    assert lib.pkv_bm_compact(bm._h, 1, 0, None, 0, ctypes.byref(n)) == 0 and n.value == 0
+    ids, lens = (ctypes.c_int64 * 2)(1, 2), (ctypes.c_int64 * 2)(5, 4)
+    assert lib.pkv_bm_compact(None, ids, lens, 2, out, 8, ctypes.byref(n)) == 1
+    assert lib.pkv_bm_compact(bm._h, None, lens, 2, out, 8, ctypes.byref(n)) == 1
+    assert lib.pkv_bm_compact(bm._h, ids, None, 2, out, 8, ctypes.byref(n)) == 1
+    assert lib.pkv_bm_compact(bm._h, ids, lens, -1, out, 8, ctypes.byref(n)) == 1
+    assert lib.pkv_bm_compact(bm._h, ids, lens, 2, out, 2, ctypes.byref(n)) == 1     # three blocks wanted
+    assert lib.pkv_bm_compact(bm._h, ids, lens, 2, None, 8, ctypes.byref(n)) == 1
+    assert lib.pkv_bm_compact(bm._h, ids, lens, 2, out, 8, None) == 1
+    assert state() == before
+    assert bm.compact([], []) == [] and state() == before
+    none = (ctypes.c_int64 * 2)(0, 0)
+    assert lib.pkv_bm_compact(bm._h, ids, none, 2, None, 0, ctypes.byref(n)) == 0 and n.value == 0
     assert bm.stats()["free_blocks"] == 8
 
 
@@ -128,6 +144,11 @@ def test_weights_checks():
     assert run(q_dtype=pkv.F16) == 1                          # not the cache's
     assert run(q_dtype=9) == 2 and run(d=desc(dtype=pkv.KV4), q_dtype=pkv.KV4) == 2
     assert run(width=255) == 1 and run(wwidth=4095) == 1 and run(scale=float("inf")) == 1
+    size = 4 * 8 * 4096 * 4                                   # in place or apart, not in between
+    for off in (4, size - 4):
+        assert run(out=ctypes.c_void_p(0x10000 + off)) == 1 and b"overlap" in lib.paged_kv_last_error()
+        assert run(w=ctypes.c_void_p(0x10000 + off)) == 1
+    assert run(out=ctypes.c_void_p(0x10000 + size), ws=None) == 3
     need = lib.paged_attention_weights_workspace_bytes(4, 32, 4096, ctypes.byref(d))
     assert need >= 4 * 32 * 4096 * 4
     assert run(ws=None) == 3 and run(nbytes=need - 1) == 3 and run(ws=ctypes.c_void_p(0x10080)) == 1

@@ -292,7 +292,7 @@ def test_serving_loop_under_memory_pressure(pool):
 
     for s in range(4):
         start(s, rng.randint(20, 110))
-    evicted = shared_evictions = 0
+    evicted = shared_evictions = together = 0
     for step in range(60):
         if step == 10:
             bm.fork(0, 9)
@@ -329,23 +329,26 @@ def test_serving_loop_under_memory_pressure(pool):
             assert np.abs(out[i].cpu().double().numpy() - ref).max() <= 2e-3
         # ---- shorten what has outgrown its budget
         over = [s for s, n in zip(ids, lens.tolist()) if n > budget]
-        for s in over:
-            old, n = bm.block_tables([s])
+        if over:
+            old, n = bm.block_tables(over)
             shared_evictions += bm.stats()["shared_blocks"] > 0
-            bm.compact(s, keep)
-            new, left = bm.block_tables([s])
-            w = weights[slots_of[s]][None].clone()
+            together = max(together, len(over))
+            bm.compact(over, [keep] * len(over))
+            new, left = bm.block_tables(over, max_blocks=-(-keep // BS))
+            at = [slots_of[s] for s in over]
+            w = weights[at]
             w_out = torch.zeros_like(w)
-            kept = torch.full((1, HKV, keep), -1, dtype=torch.int32, device="cuda")
-            pkv.paged_kv_evict(w, old.cuda(), n.cuda(), torch.tensor([keep], dtype=torch.int32).cuda(), new.cuda(), kc, vc,
-                               w_out, kept, recent=recent, max_context_len=int(n[0]))
-            weights[slots_of[s]] = w_out[0]
-            tracked[slots_of[s]] = int(left[0])
-            for h in range(HKV):
-                rows = model.kept_rows(w[0, h].cpu().numpy(), int(n[0]), keep, recent)
-                assert kept[0, h].tolist() == rows
-            idx = kept[0].cpu().numpy()
-            hist[s] = [np.take_along_axis(x, idx[:, :, None].astype(np.int64), 1) for x in hist[s]]
-            evicted += 1
+            kept = torch.full((len(over), HKV, keep), -1, dtype=torch.int32, device="cuda")
+            pkv.paged_kv_evict(w, old.cuda(), n.cuda(), torch.full((len(over),), keep, dtype=torch.int32).cuda(), new.cuda(),
+                               kc, vc, w_out, kept, recent=recent, max_context_len=int(n.max()))
+            weights[at] = w_out
+            tracked[at] = left
+            for i, s in enumerate(over):
+                for h in range(HKV):
+                    rows = model.kept_rows(w[i, h].cpu().numpy(), int(n[i]), keep, recent)
+                    assert kept[i, h].tolist() == rows
+                idx = kept[i].cpu().numpy()
+                hist[s] = [np.take_along_axis(x, idx[:, :, None].astype(np.int64), 1) for x in hist[s]]
+            evicted += len(over)
     assert pkv.device_error() == 0
-    assert evicted >= 4 and shared_evictions >= 1
+    assert evicted >= 4 and shared_evictions >= 1 and together >= 2
