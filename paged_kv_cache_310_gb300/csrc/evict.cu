@@ -4,34 +4,56 @@
 // and, of the others, the k - r with the largest accumulated weight (NaN counts as
 // -infinity; equal weights: the lowest row first).  Kept rows keep their order.
 //  * select_kernel, one CTA or a cluster of them per (KV head, sequence): the (k - r)-th
-//    largest weight by radix selection (up to four passes of eight bits over
-//    order-preserving integer keys, held in shared memory up to 48 Ki rows a CTA; a cluster
-//    shares its rows out and adds up its CTAs' counts), then one ordered pass that writes the kept rows'
-//    indices and weights.  A row's place is the number of heavier rows before it plus the
-//    number of equal ones, the latter held at how many of them are kept: one prefix sum of
-//    two packed counts.  Bound: the latency of its passes, not bytes.
+//    largest weight by radix selection (up to three passes of eleven bits over
+//    order-preserving integer keys; weights are held in shared memory up to 48 Ki rows a CTA;
+//    a cluster shares its rows out and adds up its CTAs' counts), then one ordered pass that
+//    writes the kept rows' indices and weights.  A row's place is the number of heavier rows
+//    before it plus the number of equal ones, the latter held at how many of them are kept:
+//    ballots within a warp's 32 rows, one sum of two packed counts over the warps.  Bound: the
+//    latency of its passes, not bytes: of 13 us for 32,767 rows in a cluster, 1.4 are the
+//    load, 2 each pass, 1 the counts for the other CTAs, 4 the ordered pass.  Digits of eleven
+//    bits (four passes of eight before) spread accumulators of similar size over more
+//    counters; 512 threads leave room for two CTAs per SM, so that a batch of 256 runs at once
+//    (32 sequences of 512 to 4,096 rows, 8 heads: 81 us a call, 85 with 1,024 threads).
 //  * move_kernel copies the kept rows of K and V into the sequence's new blocks, 16 bytes
-//    (8 where rows are 40) per thread.  Bound: HBM; each kept row is read and written once.
+//    (8 where rows are 40) per thread.  Bound: HBM; each kept row is read and written once:
+//    69 us of that call, 413 MB, 6.0 TB/s.
 #include "common.cuh"
 #include "launch.h"
 
 namespace pkv {
 namespace {
 
-constexpr int kSelectThreads = 1024;
-constexpr int kPerThread = 4;  // rows per thread and step of the ordered pass
-constexpr int kMaxKeys = 48 * 1024;  // rows whose keys fit in shared memory
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kPerLane = 8;  // rows per lane and step of the ordered pass: a warp takes 32 at a time
+constexpr int kDigits = 2048;  // eleven bits a pass
+constexpr int kBins = kDigits / kSelectThreads;
+static_assert(kBins == 4 && kSelectWarps <= 32, "a thread reads its bins as one vector; one warp scans the warps' sums");
+constexpr int kMaxKeys = 48 * 1024;  // rows whose weights fit in shared memory
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 32;  // kept rows per CTA
+constexpr int kMoveRows = 32;  // kept rows per CTA (that batch: 81 us; with 16, 86; with 64, 82)
 
-// Cluster-wide barrier, and a word of another CTA's shared memory.
+// Cluster-wide barrier, and words of another CTA's shared memory.
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-__device__ __forceinline__ uint32_t cluster_load(const uint32_t* mine, uint32_t rank) {
-  uint32_t at, v;
+__device__ __forceinline__ uint32_t cluster_address(const void* mine, uint32_t rank) {
+  uint32_t at;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_addr(mine)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return at;
+}
+__device__ __forceinline__ uint32_t cluster_load(const uint32_t* mine, uint32_t rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_address(mine, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 cluster_load(const uint4* mine, uint32_t rank) {
+  uint4 v;
+  asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(cluster_address(mine, rank))
+               : "memory");
   return v;
 }
 
@@ -41,17 +63,18 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ EvictParams p) {
-  __shared__ uint32_t hist[2][256];  // this CTA's counts, of even and odd passes
-  __shared__ uint32_t counts[256];   // the cluster's
-  __shared__ uint32_t totals[2];     // this CTA's rows above the threshold, and ties
-  __shared__ uint32_t warp_sum[32];
+// kSize CTAs per (KV head, sequence): a cluster along x.
+template <int kSize>
+__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_constant__ EvictParams p) {
+  __shared__ __align__(16) uint32_t hist[2][kDigits];  // this CTA's counts, of even and odd passes
+  __shared__ uint32_t totals[2];                       // this CTA's rows above the threshold, and ties
+  __shared__ uint32_t warp_sum[kSelectWarps];
   __shared__ uint32_t found[3];  // digit, rows still to take among it, rows that have it
-  extern __shared__ uint32_t keys[];
+  extern __shared__ float held_weights[];
   grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
   grid_dependents_launch();  // move_kernel, which waits for this grid
   const int kvh = blockIdx.y, s = blockIdx.z;
-  const uint32_t size = gridDim.x, rank = blockIdx.x;  // the cluster spans x
+  const uint32_t rank = kSize > 1 ? blockIdx.x : 0;
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int n = p.context_lens[s], keep = p.keep_lens[s];
   if (n < 0 || n > p.max_len || keep < 0 || min(keep, n) > p.max_keep) {
@@ -63,81 +86,85 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   const size_t row = static_cast<size_t>(s) * p.num_kv_heads + kvh;
   const float* w = p.weights + row * p.width;
   // this CTA's rows
-  const int each = (n + static_cast<int>(size) - 1) / static_cast<int>(size);
+  const int each = (n + kSize - 1) / kSize;
   const int first = min(n, static_cast<int>(rank) * each), last = min(n, first + each);
   const int own = max(0, min(last, candidates) - first);  // of them, those chosen by weight
 
   // ---- the threshold: keys above it are kept, and the first `ties` of those equal to it
-  uint32_t threshold = 0, ties = 0;
-  if (k - r == 0) {
-    threshold = 0xffffffffu;  // no key is above it
-  } else if (k - r < candidates) {
-    const bool held = own <= p.key_room;
-    if (held) {
-      constexpr int kBatch = 8;  // loads in flight per thread
-      for (int j0 = tid; j0 < own; j0 += kSelectThreads * kBatch) {
-        float x[kBatch];
+  uint32_t threshold = k - r == 0 ? 0xffffffffu : 0, ties = 0;  // no key is above it, or every key
+  bool held = false;
+  if (k - r > 0 && k - r < candidates) {
+    held = own <= p.key_room;
+    reinterpret_cast<uint4*>(hist[0])[tid] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    constexpr int kBatch = 8;  // loads in flight per thread
+    for (int j0 = tid; j0 < own; j0 += kSelectThreads * kBatch) {
+      float x[kBatch];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) x[i] = j0 + i * kSelectThreads < own ? w[first + j0 + i * kSelectThreads] : 0.f;
+      for (int i = 0; i < kBatch; ++i) x[i] = j0 + i * kSelectThreads < own ? w[first + j0 + i * kSelectThreads] : 0.f;
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          if (j0 + i * kSelectThreads < own) keys[j0 + i * kSelectThreads] = weight_key(x[i]);
-      }  // each thread reads back only what it wrote
+      for (int i = 0; i < kBatch; ++i)
+        if (j0 + i * kSelectThreads < own) {
+          if (held) held_weights[j0 + i * kSelectThreads] = x[i];
+          atomicAdd(&hist[0][weight_key(x[i]) >> 21], 1u);
+        }
     }
     uint32_t need = k - r;
-    if (tid < 256) hist[0][tid] = 0;
-    for (int shift = 24, pass = 0; shift >= 0; shift -= 8, ++pass) {
+    for (int pass = 0; pass < 3; ++pass) {  // bits 31..21, 20..10, 9..0
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       uint32_t* mine = hist[pass & 1];
-      __syncthreads();
+      if (pass > 0) {
+        const int above_bits = pass == 1 ? 21 : 10;
+        const uint32_t mask = pass == 1 ? 2047u : 1023u;
 #pragma unroll 4
-      for (int j = tid; j < own; j += kSelectThreads) {
-        const uint32_t key = held ? keys[j] : weight_key(w[first + j]);
-        if (shift == 24 || (key >> (shift + 8)) == (threshold >> (shift + 8))) atomicAdd(&mine[(key >> shift) & 255], 1u);
+        for (int j = tid; j < own; j += kSelectThreads) {
+          const uint32_t key = weight_key(held ? held_weights[j] : w[first + j]);  // what this thread put there
+          if ((key >> above_bits) == (threshold >> above_bits)) atomicAdd(&mine[(key >> shift) & mask], 1u);
+        }
       }
-      if (size > 1)
+      if (kSize > 1)
         cluster_barrier();
       else
         __syncthreads();
-      if (tid < 256) {
-        // the other buffer is free: everybody read it before arriving at the barrier
-        hist[(pass & 1) ^ 1][tid] = 0;
-        uint32_t c = mine[tid];
-        for (uint32_t i = 1; i < size; ++i) c += cluster_load(mine + tid, (rank + i) % size);
-        counts[tid] = c;
+      // the other buffer is free: everybody read it before arriving at the barrier
+      reinterpret_cast<uint4*>(hist[(pass & 1) ^ 1])[tid] = make_uint4(0, 0, 0, 0);
+      // thread 0 holds the largest digits: the digit whose rows from the top reach `need`
+      const int group = kSelectThreads - 1 - tid;
+      const uint4* bins = reinterpret_cast<const uint4*>(mine) + group;
+      uint4 c = *bins, theirs[kSize];
+#pragma unroll
+      for (int i = 1; i < kSize; ++i) theirs[i] = cluster_load(bins, (rank + i) % kSize);
+#pragma unroll
+      for (int i = 1; i < kSize; ++i) {
+        c.x += theirs[i].x;
+        c.y += theirs[i].y;
+        c.z += theirs[i].z;
+        c.w += theirs[i].w;
       }
+      const uint32_t count[kBins] = {c.w, c.z, c.y, c.x}, sum = c.x + c.y + c.z + c.w;
+      uint32_t above = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, above, off);
+        if (lane >= off) above += x;
+      }
+      if (lane == 31) warp_sum[warp] = above;
       __syncthreads();
-      if (warp == 0) {
-        // lane 0 holds the eight largest digits: the digit whose rows from the top reach `need`
-        uint32_t c[8], sum = 0;
+      above += __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u) - sum;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          c[i] = counts[255 - (lane * 8 + i)];
-          sum += c[i];
+      for (int i = 0; i < kBins; ++i) {
+        if (above < need && above + count[i] >= need) {
+          found[0] = 4 * group + 3 - i;
+          found[1] = need - above;
+          found[2] = count[i];
         }
-        uint32_t above = sum;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const uint32_t x = __shfl_up_sync(0xffffffffu, above, off);
-          if (lane >= off) above += x;
-        }
-        above -= sum;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (above < need && above + c[i] >= need) {
-            found[0] = 255 - (lane * 8 + i);
-            found[1] = need - above;
-            found[2] = c[i];
-          }
-          above += c[i];
-        }
+        above += count[i];
       }
       __syncthreads();
       threshold |= found[0] << shift;
       need = found[1];
-      const bool all = found[2] == need;  // every row with these digits is kept: no need to look further
-      __syncthreads();
-      if (all) {
-        threshold -= 1;  // >= 0x007fffff here, the key of -infinity
+      if (found[2] == need) {  // every row with these digits is kept: no need to look further
+        threshold -= 1;        // >= 0x005fffff here: the key of -infinity is 0x007fffff
         need = 0;
         break;
       }
@@ -146,20 +173,19 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
   }
 
   // ---- the kept rows in order
-  auto flag_of = [&](int j, float x) {  // 1 above the threshold or recent, 1 << 16 a tie
-    const uint32_t key = weight_key(x);
-    return j >= last ? 0u : j >= candidates || key > threshold ? 1u : key == threshold && ties ? 0x10000u : 0u;
-  };
   uint32_t above_before = 0, ties_before = 0;  // in the CTAs and steps before
-  if (size > 1) {
+  if (kSize > 1) {
     // count this CTA's first: their numbers tell the others where to begin
     if (tid < 2) totals[tid] = 0;
     __syncthreads();
     uint32_t above = 0, equal = 0;
-    for (int j = first + tid; j < last; j += kSelectThreads) {
-      const uint32_t f = flag_of(j, w[j]);
-      above += f & 0xffffu;
-      equal += f >> 16;
+    if (k - r > 0) {
+#pragma unroll 4
+      for (int j = tid; j < own; j += kSelectThreads) {
+        const uint32_t key = weight_key(held ? held_weights[j] : w[first + j]);
+        above += key > threshold;
+        equal += key == threshold;
+      }
     }
     above = __reduce_add_sync(0xffffffffu, above);
     equal = __reduce_add_sync(0xffffffffu, equal);
@@ -168,65 +194,55 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
       atomicAdd(&totals[1], equal);
     }
     cluster_barrier();
-    for (uint32_t i = 0; i < rank; ++i) {
-      above_before += cluster_load(&totals[0], i);
-      ties_before += cluster_load(&totals[1], i);
-    }
+    const bool before = lane < static_cast<int>(rank);  // the recent rows come behind every other
+    above = before ? cluster_load(&totals[0], lane) : 0u;
+    equal = before ? cluster_load(&totals[1], lane) : 0u;
+    above_before = __reduce_add_sync(0xffffffffu, above) + max(0, first - candidates);
+    ties_before = ties ? __reduce_add_sync(0xffffffffu, equal) : 0u;
   }
   int32_t* kept = p.kept + row * p.max_keep;
   float* out = p.weights_out + row * p.width;
-  float x[kPerThread], ahead[kPerThread];
-  auto load = [&](int j0, float (&to)[kPerThread]) {
+  constexpr int kStep = kSelectThreads * kPerLane;
+  for (int j0 = first; j0 < last; j0 += kStep) {
+    const int j = j0 + warp * 32 * kPerLane + lane;
+    float x[kPerLane];
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int j = j0 + tid * kPerThread + i;
-      to[i] = j < last ? w[j] : 0.f;
+    for (int i = 0; i < kPerLane; ++i) {
+      const int at = j + 32 * i;
+      x[i] = at >= last ? 0.f : held && at - first < own ? held_weights[at - first] : w[at];
     }
-  };
-  load(first, ahead);
-  for (int j0 = first; j0 < last; j0 += kSelectThreads * kPerThread) {
-    const int j = j0 + tid * kPerThread;
+    uint32_t heavy[kPerLane], equal[kPerLane], count = 0;  // masks of the warp's rows; their numbers, ties << 16
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) x[i] = ahead[i];
-    load(j0 + kSelectThreads * kPerThread, ahead);
-    uint32_t count = 0, flag[kPerThread];  // rows above the threshold, and ties << 16
-#pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      flag[i] = flag_of(j + i, x[i]);
-      count += flag[i];
+    for (int i = 0; i < kPerLane; ++i) {
+      const int at = j + 32 * i;
+      const uint32_t key = weight_key(x[i]);
+      heavy[i] = __ballot_sync(0xffffffffu, at < last && (at >= candidates || key > threshold));
+      equal[i] = __ballot_sync(0xffffffffu, at < last && at < candidates && key == threshold && ties);
+      count += __popc(heavy[i]) + (__popc(equal[i]) << 16);
     }
-    uint32_t scan = count;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, scan, off);
-      if (lane >= off) scan += y;
-    }
-    if (lane == 31) warp_sum[warp] = scan;
+    if (lane == 0) warp_sum[warp] = count;
     __syncthreads();
-    uint32_t total = warp_sum[lane], before = total;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, before, off);
-      if (lane >= off) before += y;
-    }
-    const uint32_t all = __shfl_sync(0xffffffffu, before, 31);
-    before = __shfl_sync(0xffffffffu, before - total, warp) + scan - count;
-    __syncthreads();  // warp_sum is written again
+    const uint32_t theirs = lane < kSelectWarps ? warp_sum[lane] : 0u;
+    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0u);
+    const uint32_t all = __reduce_add_sync(0xffffffffu, theirs);
     uint32_t a = above_before + (before & 0xffffu), e = ties_before + (before >> 16);
+    const uint32_t lower = (1u << lane) - 1u;
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      if (flag[i] == 1u || (flag[i] && e < ties)) {
-        const uint32_t at = a + min(e, ties);
-        kept[at] = j + i;
+    for (int i = 0; i < kPerLane; ++i) {
+      const uint32_t above = a + __popc(heavy[i] & lower), tied = e + __popc(equal[i] & lower);
+      if ((heavy[i] >> lane & 1u) || ((equal[i] >> lane & 1u) && tied < ties)) {
+        const uint32_t at = above + min(tied, ties);
+        kept[at] = j + 32 * i;
         out[at] = x[i];
       }
-      a += flag[i] & 0xffffu;
-      e += flag[i] >> 16;
+      a += __popc(heavy[i]);
+      e += __popc(equal[i]);
     }
     above_before += all & 0xffffu;
     ties_before += all >> 16;
+    __syncthreads();  // warp_sum is written again
   }
-  if (size > 1) cluster_barrier();  // nobody leaves while its counts may be read
+  if (kSize > 1) cluster_barrier();  // nobody leaves while its counts may be read
 }
 
 template <typename V>
@@ -262,6 +278,30 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   }
 }
 
+template <int kSize>
+cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e = ensure_smem_limit(select_kernel<kSize>, kMaxKeys * 4, configured);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(kSize, p.num_kv_heads, p.num_seqs);
+  if (kSize == 1) return launch_dependent(select_kernel<kSize>, grid, kSelectThreads, p.key_room * 4, stream, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kSelectThreads);
+  cfg.dynamicSmemBytes = p.key_room * 4;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kSize;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, select_kernel<kSize>, p);
+}
+
 template <typename V>
 cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
   const int most = p.max_keep < p.max_len ? p.max_keep : p.max_len;  // rows a sequence may keep
@@ -273,37 +313,21 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
-  // A selection's passes are bound by its CTA's instructions (one of 32,767 rows: 20 us), so
-  // few long ones are shared by up to eight CTAs each, as many as leave two CTAs per SM and
-  // 4,096 rows each; a batch that fills the GPU by itself gains nothing (its barriers cost).
+  // A selection's passes are bound by its CTA's instructions, so few long ones are shared by up
+  // to eight CTAs each, as many as leave two CTAs per SM and 4,096 rows each (one sequence of
+  // 32,767 rows, 4 heads: 16.9 us a call with four CTAs, 22.4 with two); a batch that fills the
+  // GPU by itself gains nothing, and with fewer rows the barriers cost more than they save (16
+  // sequences of 4,096 rows, 8 heads: 30.4 us with one CTA each, 33.6 with two).  Clusters of
+  // sixteen lose: 83 us in place of 72 for 131,072 rows.
   const int64_t items = static_cast<int64_t>(p.num_seqs) * p.num_kv_heads;
   int size = 1;
   while (size < 8 && items * size * 2 <= 2 * 152 && p.max_len / (size * 2) >= 4096) size *= 2;
   const int most = (p.max_len + size - 1) / size;
   p.key_room = most < kMaxKeys ? most : kMaxKeys;
-  static std::atomic<unsigned long long> configured{0};
-  cudaError_t e = ensure_smem_limit(select_kernel, kMaxKeys * 4, configured);
-  if (e != cudaSuccess) return e;
-  const dim3 grid(size, p.num_kv_heads, p.num_seqs);
-  if (size == 1) {
-    e = launch_dependent(select_kernel, grid, kSelectThreads, p.key_room * 4, stream, p);
-  } else {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(kSelectThreads);
-    cfg.dynamicSmemBytes = p.key_room * 4;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = size;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    e = cudaLaunchKernelEx(&cfg, select_kernel, p);
-  }
+  const cudaError_t e = size == 1   ? launch_select<1>(p, stream)
+                        : size == 2 ? launch_select<2>(p, stream)
+                        : size == 4 ? launch_select<4>(p, stream)
+                                    : launch_select<8>(p, stream);
   if (e != cudaSuccess) return e;
   return p.row_bytes % 16 == 0 ? launch_move<uint4>(p, stream) : launch_move<uint2>(p, stream);
 }
