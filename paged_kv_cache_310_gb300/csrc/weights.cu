@@ -14,6 +14,7 @@
 //
 // 16-bit pools go to m16n8k16 MMAs as they are, 4-bit ones are widened in registers
 // (kv4.cuh), f32 ones are multiplied on CUDA cores in fp32.
+#include <cfloat>
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -158,10 +159,19 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   float m[NB][2], l[NB][2];  // the warp's maximum, this lane's rows' sum
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
-    m[nb][0] = m[nb][1] = -INFINITY;
+    m[nb][0] = m[nb][1] = -FLT_MAX;  // not -infinity: -infinity less it is no NaN
     l[nb][0] = l[nb][1] = 0.f;
   }
-  float* scores = p.scores + q_row * p.scores_ld + t0;  // [head][token]
+  float* column[NB][2];  // this lane's heads' rows of scores, and whether they are heads
+  bool first_in[NB], second_in[NB];
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb) {
+    const int h = nb * 8 + 2 * t;
+    column[nb][0] = p.scores + (q_row + h) * p.scores_ld + t0 + g;
+    column[nb][1] = column[nb][0] + p.scores_ld;
+    first_in[nb] = h < G;
+    second_in[nb] = h + 1 < G;
+  }
 
   uint32_t at = 0, refill = (C::kStages - 1) * C::kStage;  // stages, as offsets into the ring
   auto step = [&](int tile, auto last) {
@@ -179,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
     for (int u = 0; u < C::kSub; ++u) {
       const unsigned char* r0 = ks + 2 * u * C::kHalf + g * C::kRow;  // row g; row g + 8 is kHalf on
       if constexpr (kMma) {
-        float c[NB][2][4];
+        float c[NB][4];
         [[maybe_unused]] uint32_t w0[D / 32], w1[D / 32];
         [[maybe_unused]] __half2 p0, p1;
         if constexpr (C::kIsKv4) {
@@ -216,30 +226,31 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
           }
 #pragma unroll
           for (int nb = 0; nb < NB; ++nb) {
-            if (i == 0) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) c[nb][0][e] = c[nb][1][e] = 0.f;
-            }
+            const uint32_t *h0 = qh[nb][2 * i], *h1 = qh[nb][2 * i + 1];
             if constexpr (KIND == PKV_BF16) {
-              mma_bf16(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][2 * i][0], qh[nb][2 * i][1]);
-              mma_bf16(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][2 * i + 1][0], qh[nb][2 * i + 1][1]);
-            } else if (i == 0) {
-              mma_f16_first(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][0][0], qh[nb][0][1]);
-              mma_f16_first(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][1][0], qh[nb][1][1]);
+              if (i == 0) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) c[nb][e] = 0.f;
+              }
+              mma_bf16(c[nb], a[0], b[0], a[1], b[1], h0[0], h0[1]);
+              mma_bf16(c[nb], a[2], b[2], a[3], b[3], h1[0], h1[1]);
             } else {
-              mma_f16(c[nb][0], a[0], b[0], a[1], b[1], qh[nb][2 * i][0], qh[nb][2 * i][1]);
-              mma_f16(c[nb][1], a[2], b[2], a[3], b[3], qh[nb][2 * i + 1][0], qh[nb][2 * i + 1][1]);
+              if (i == 0)
+                mma_f16_first(c[nb], a[0], b[0], a[1], b[1], h0[0], h0[1]);
+              else
+                mma_f16(c[nb], a[0], b[0], a[1], b[1], h0[0], h0[1]);
+              mma_f16(c[nb], a[2], b[2], a[3], b[3], h1[0], h1[1]);
             }
             if constexpr (kSplit) {
-              mma_f16(c[nb][0], a[0], b[0], a[1], b[1], ql[nb][2 * i][0], ql[nb][2 * i][1]);
-              mma_f16(c[nb][1], a[2], b[2], a[3], b[3], ql[nb][2 * i + 1][0], ql[nb][2 * i + 1][1]);
+              mma_f16(c[nb], a[0], b[0], a[1], b[1], ql[nb][2 * i][0], ql[nb][2 * i][1]);
+              mma_f16(c[nb], a[2], b[2], a[3], b[3], ql[nb][2 * i + 1][0], ql[nb][2 * i + 1][1]);
             }
           }
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[nb][u][i] = (c[nb][0][i] + c[nb][1][i]) * sc[nb][i & 1];
+          for (int i = 0; i < 4; ++i) x[nb][u][i] = c[nb][i] * sc[nb][i & 1];
       } else {
         // fp32: lane t multiplies its quarter of rows g and g + 8 with every head's, then the
         // four lanes add up and each keeps its two columns
@@ -252,6 +263,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
+          x[nb][u][0] = x[nb][u][1] = x[nb][u][2] = x[nb][u][3] = 0.f;
 #pragma unroll
           for (int h = 0; h < 8; ++h) {
             if (nb * 8 + h >= G) break;  // warp-uniform
@@ -276,27 +288,25 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
     }
 
     // ---- store the scores; the warp's (maximum, sum) of its columns: the maximum is raised only
-    // when a score exceeds it by 8 (log2 domain), so sums hold powers up to 2^8
+    // when a score exceeds it by 8 (log2 domain), so sums hold powers up to 2^8.  Columns past
+    // the group come along (scores 0) and are used by nobody.
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      float top = -INFINITY;
+      float d[2][2 * C::kSub], top = -INFINITY;  // scores less the maximum
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int h = nb * 8 + 2 * t + e;
-        float* to = scores + h * p.scores_ld + tile * C::kTile + g;
+        float* to = column[nb][e] + tile * C::kTile;
 #pragma unroll
-        for (int u = 0; u < C::kSub; ++u)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float& y = x[nb][u][2 * i + e];
-            if (h >= G || (kLast && 16 * u + 8 * i + g >= left))
-              y = -INFINITY;
-            else
-              to[16 * u + 8 * i] = y;
-            top = fmaxf(top, y - m[nb][e]);
-          }
+        for (int i = 0; i < 2 * C::kSub; ++i) {
+          float& y = x[nb][i / 2][2 * (i & 1) + e];
+          const bool in = !kLast || 8 * i + g < left;
+          if (!in) y = -INFINITY;
+          if (in && (e == 0 ? first_in[nb] : second_in[nb])) to[8 * i] = y;
+          d[e][i] = y - m[nb][e];
+          top = fmaxf(top, d[e][i]);
+        }
       }
-      if (__any_sync(0xffffffffu, top > 8.f)) {  // m = -inf: any finite score
+      if (__any_sync(0xffffffffu, top > 8.f)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float M = m[nb][e];
@@ -306,15 +316,14 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
           for (int off = 4; off < 32; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
           if (M != m[nb][e]) l[nb][e] *= exp2_approx(m[nb][e] - M);
           m[nb][e] = M;
+#pragma unroll
+          for (int i = 0; i < 2 * C::kSub; ++i) d[e][i] = x[nb][i / 2][2 * (i & 1) + e] - M;
         }
       }
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // nothing seen yet but -inf: no weight (a NaN stays)
-        const float base = m[nb][e] == -INFINITY ? 0.f : m[nb][e];
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int u = 0; u < C::kSub; ++u) l[nb][e] += exp2_approx(x[nb][u][e] - base) + exp2_approx(x[nb][u][2 + e] - base);
-      }
+        for (int u = 0; u < C::kSub; ++u) l[nb][e] += exp2_approx(d[e][2 * u]) + exp2_approx(d[e][2 * u + 1]);
     }
   };
   int tile = warp;
@@ -341,7 +350,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
     }
   __syncthreads();
   if (threadIdx.x < G) {
-    float M = -INFINITY, sum = 0.f;
+    float M = -FLT_MAX, sum = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, red[(w * NB * 8 + threadIdx.x) * 2]);
 #pragma unroll
