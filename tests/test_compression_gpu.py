@@ -54,6 +54,44 @@ def test_blocks_past_four_gigabytes():
             assert torch.equal(moved, torch.from_numpy(held[rows, h]).bfloat16())
 
 
+def test_the_most_sequences_a_call_takes():
+    n, d, bs = 65_535, 64, 8
+    gen = torch.Generator(device="cuda").manual_seed(311_330)
+    rand = lambda *shape: torch.randn(*shape, generator=gen, device="cuda")
+    kc, vc = (torch.zeros((n, 1, bs, d * 5 // 8), dtype=torch.uint8, device="cuda") for _ in range(2))
+    tables = torch.randperm(n, generator=gen, device="cuda").to(torch.int32)[:, None]
+    lens = torch.randint(0, 3, (n,), generator=gen, device="cuda").to(torch.int32)
+    slots = (tables.long() * bs + torch.arange(2, device="cuda")).flatten()
+    pkv.paged_kv4_append(rand(2 * n, 1, d), rand(2 * n, 1, d), slots, kc, vc)
+    wide = [torch.zeros((n, 1, bs, d), device="cuda") for _ in range(2)]
+    pairs = torch.arange(n, device="cuda")[:, None].expand(n, 2).contiguous()
+    pkv.paged_kv4_expand(pairs, kc, vc, *wide)
+    k, v = (x[tables[:, 0].long(), 0, :2].double() for x in wide)               # [n, 2, d]
+    q, out = rand(n, 2, d), torch.empty(n, 2, d, device="cuda")
+    pkv.paged_attention_decode_kv4(q, kc, vc, tables, lens, 0.125, out, max_context_len=2)
+    seen = torch.arange(2, device="cuda") < lens[:, None]                       # [n, 2]
+    p = torch.softmax(torch.where(seen[:, None], 0.125 * q.double() @ k.mT, -1e300), -1) * seen[:, None]
+    assert pkv.device_error() == 0
+    # scores below 15 are good to 15 * 2^-21, a weight to twice that, times values below 5: 7e-5
+    assert (out - p @ v).abs().max() <= 1e-4
+    w = torch.full((n, 1, 2), 7.0, device="cuda")
+    pkv.paged_attention_weights(q, kc, tables, lens, 0.125, w, tracked_lens=torch.zeros_like(lens), max_context_len=2)
+    assert (torch.where(seen, w[:, 0] - p.sum(1), w[:, 0] - 7.0)).abs().max() <= 1e-4
+    # the heavier row of each sequence becomes the first of a block that nobody reads
+    spare = [torch.zeros((2 * n, 1, bs, d * 5 // 8), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for s, c in zip(spare, (kc, vc)):
+        s[:n] = c
+    new = (2 * n - 1 - torch.arange(n, device="cuda")).to(torch.int32)[:, None]
+    w_out, kept = torch.zeros_like(w), torch.full((n, 1, 1), -1, dtype=torch.int32, device="cuda")
+    pkv.paged_kv_evict(w, tables, lens, torch.ones_like(lens), new, *spare, w_out, kept, max_context_len=2)
+    best = torch.where((lens == 2) & (w[:, 0, 1] > w[:, 0, 0]), 1, 0)
+    assert pkv.device_error() == 0
+    assert torch.equal(kept[:, 0, 0].long(), torch.where(lens > 0, best, -1))
+    some = (lens > 0).nonzero().flatten()
+    for s, c in zip(spare, (kc, vc)):
+        assert torch.equal(s[new[some, 0].long(), 0, 0], c[tables[some, 0].long(), 0, best[some]])
+
+
 class Server:
     """Two sequences in a 4-bit pool, and one step: append, decode, weights, eviction."""
 

@@ -203,7 +203,8 @@ def test_evict_parity(pool, d, bs, recent):
                                            (49152, 700, 5), (49153, 20001, 0), (70000, 33333, 1), (8191, 8190, 8190),
                                            (32768, 16384, 16384), (400001, 5, 2), (32767, 32767, 9)])
 def test_evict_long(n, keep, recent):
-    Evict(311_120, [n, 50], [keep, 20], recent, 1, 64, 16, "bf16").check()
+    # with sequences so short that most of a cluster's CTAs have no row of them
+    Evict(311_120, [n, 50, 3, 0, 1], [keep, 20, 2, 1, 1], recent, 1, 64, 16, "bf16").check()
 
 
 @pytest.mark.parametrize("value", [0.0, 1.0, float("nan"), float("-inf"), float("inf")])
@@ -215,9 +216,9 @@ def test_evict_equal_weights_keep_the_lowest_rows(value):
 
 
 def test_evict_weights_that_share_leading_bits():
-    # the threshold is found after one, two, three or four passes of eight bits
+    # the threshold is found after one, two or three passes of eleven bits
     for bits in (0x3F800000, 0x3F000000, 0x00000000, 0xBF800000):
-        for spread in (0x01000000, 0x00010000, 0x00000100, 0x00000002):
+        for spread in (0x01000000, 0x00400000, 0x00200000, 0x00010000, 0x00000800, 0x00000400, 0x00000100, 0x00000002):
             c = Evict(311_135, [700], [300], 10, 2, 64, 8, "f16")
             gen = torch.Generator().manual_seed(311_136)
             k = torch.randint(0, spread, c.w.shape, generator=gen) + bits
