@@ -46,7 +46,7 @@ pkv_status plan_kv4(int32_t num_seqs, int32_t num_q_heads, int32_t max_len, int3
   plan->ml_at = plan->o_at = plan->workspace = 0;
   if (units > 1 && plan->ctas > 1 && num_seqs > 0) {
     const size_t rows = static_cast<size_t>(2) * plan->ctas * group;
-    plan->ml_at = (plan->ctas * 16 + 255) / 256 * 256;
+    plan->ml_at = (plan->ctas * 32 + 255) / 256 * 256;
     plan->o_at = plan->ml_at + (rows * 8 + 255) / 256 * 256;
     plan->workspace = plan->o_at + rows * c->head_dim * sizeof(float);
   }

@@ -217,7 +217,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
   __syncthreads();
   const int64_t units = total * p.num_kv_heads;  // the batch's cost
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (units + kMinCost - 1) / kMinCost);
-  if (threadIdx.x == 0 && p.desc) p.desc[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x < 2 && p.desc) p.desc[2 * blockIdx.x + threadIdx.x] = make_int4(-1, 0, 0, 0);
   if (static_cast<int64_t>(blockIdx.x) >= ctas) return;
   const int64_t begin = blockIdx.x * units / ctas, end = (blockIdx.x + 1) * units / ctas;
 
@@ -647,10 +647,15 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
       }
     }
   }
-  if (threadIdx.x == 0 && u0 == 0 && count < n_units) {
-    // the item ends in the span of the last CTA c with c * units / ctas <= its last place
-    const int64_t last = cur - at_cost + cost - 1;
-    p.desc[blockIdx.x] = make_int4(s, kvh, static_cast<int>(((last + 1) * ctas + units - 1) / units - 1), 0);
+  if (threadIdx.x == 0 && count < n_units) {
+    // place x of the batch's cost is in the span of the last CTA c with c * units / ctas <= x
+    auto span_of = [&](int64_t x) {
+      const int64_t y = (x + 1) * ctas + units - 1;
+      return y < (int64_t{1} << 32) ? static_cast<int>(static_cast<uint32_t>(y) / static_cast<uint32_t>(units)) - 1
+                                    : static_cast<int>(y / units - 1);
+    };
+    const int64_t at = cur - at_cost;  // the item's first place; its units begin kItemCost later
+    p.desc[2 * blockIdx.x + (u0 == 0)] = make_int4(s, kvh, span_of(at + kItemCost), span_of(at + cost - 1));
   }
   __syncthreads();  // the sums have been read: the ring and the queries take their place
   }
@@ -669,45 +674,107 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
   }
 }
 
-// One CTA per span: joins the item that starts in it and ends in a later one, if there is
-// one.  Its pieces are the span's last item (slot 2c + 1) and the first ones of the spans up
-// to the item's end (slots 2c).  A warp takes 64 dimensions of a head at a time: its lanes
-// take a piece each for the factors 2^(m - M), then two dimensions each for the sum.
+// Joins the items that lie in several spans, a CTA per span.  An item's pieces are the last
+// item of its first span (slot 2 start + 1) and the first ones of the others (slots 2c).  Its
+// tasks are 64 dimensions of a head each: a lane takes a piece at a time for the factors
+// 2^(m - M), then two dimensions for the sum.  Up to kFew pieces are joined by the first span's
+// CTA, a warp per task, whose loads all leave at once.  The CTAs of more share out the tasks in
+// turn, and one with fewer tasks than warps shares a task's pieces out among its warps (one
+// sequence of 128 Ki tokens and one KV head is 342 pieces: joined by its first CTA alone, 16
+// heads took 240 us behind 13 us of attention).
 constexpr int kJoinThreads = 256;
+constexpr int kJoinWarps = kJoinThreads / 32;
+constexpr int kFew = 8;
 __global__ void __launch_bounds__(kJoinThreads) join_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
+  __shared__ float2 partial[kJoinWarps][32];
   grid_dependency_wait();
-  const int4 d = p.desc[blockIdx.x];
-  if (d.x < 0) return;
-  const int c = blockIdx.x, n = d.z - c + 1, G = p.group, D = p.head_dim;
+  const int G = p.group, D = p.head_dim, parts = D / 64, tasks = G * parts;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const size_t out = (static_cast<size_t>(d.x) * p.num_q_heads + static_cast<size_t>(d.y) * G) * D;
-  auto slot = [&](int i) { return static_cast<size_t>(i == 0 ? 2 * c + 1 : 2 * (c + i)) * G; };
-  const int parts = D / 64;  // 64 dimensions of a head per warp and round
-  for (int x = warp; x < G * parts; x += kJoinThreads / 32) {
-    const int h = x / parts, e = x % parts * 64 + 2 * lane;
-    float M = -INFINITY;
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.ws_ml[slot(i) + h].x);
+  const int4 continued = p.desc[2 * blockIdx.x], begun = p.desc[2 * blockIdx.x + 1];
+  auto first_row = [&](const int4& d) {
+    return static_cast<size_t>(d.x) * p.num_q_heads + static_cast<size_t>(d.y) * G;
+  };
+  auto slot = [&](const int4& d, int i) { return static_cast<size_t>(2 * (d.z + i) + (i == 0)) * G; };
+
+  if (begun.x >= 0 && begun.w - begun.z < kFew) {
+    const int n = begun.w - begun.z + 1;
+    for (int x = warp; x < tasks; x += kJoinWarps) {
+      const int h = x / parts, e = x % parts * 64 + 2 * lane;
+      float2 o[kFew];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float lsum = 0.f, a = 0.f, b = 0.f;
-    for (int base = 0; base < n; base += 32) {
-      float f = 0.f;
-      if (base + lane < n) {
-        const float2 ml = p.ws_ml[slot(base + lane) + h];
-        f = exp2_approx(ml.x - M);
-        lsum = fmaf(f, ml.y, lsum);
-      }
-      const int here = min(32, n - base);
-#pragma unroll 8
-      for (int i = 0; i < here; ++i) {
-        const float2 o = *reinterpret_cast<const float2*>(p.ws_o + (slot(base + i) + h) * D + e);
+      for (int i = 0; i < kFew; ++i)
+        o[i] = i < n ? *reinterpret_cast<const float2*>(p.ws_o + (slot(begun, i) + h) * D + e) : make_float2(0.f, 0.f);
+      const int mine = lane % kFew;
+      const float2 ml = mine < n ? p.ws_ml[slot(begun, mine) + h] : make_float2(-INFINITY, 0.f);
+      float M = ml.x;
+#pragma unroll
+      for (int off = 1; off < kFew; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      const float f = mine < n ? exp2_approx(ml.x - M) : 0.f;
+      const float lsum = group_sum<kFew>(f * ml.y);
+      float a = 0.f, b = 0.f;
+#pragma unroll
+      for (int i = 0; i < kFew; ++i) {
         const float w = __shfl_sync(0xffffffffu, f, i);
-        a = fmaf(w, o.x, a);
-        b = fmaf(w, o.y, b);
+        a = fmaf(w, o[i].x, a);
+        b = fmaf(w, o[i].y, b);
       }
+      store_pair(p.out, (first_row(begun) + h) * D + e, a / lsum, b / lsum, p.out_dtype);
     }
-    lsum = group_sum<32>(lsum);
-    store_pair(p.out, out + h * D + e, a / lsum, b / lsum, p.out_dtype);
+  }
+
+#pragma unroll 1
+  for (int role = 0; role < 2; ++role) {
+    const int4 d = role ? begun : continued;
+    if (d.x < 0 || d.w - d.z < kFew) continue;
+    const int n = d.w - d.z + 1, rank = blockIdx.x - d.z;
+    const int mine = rank < tasks ? (tasks - rank + n - 1) / n : 0;
+    const int share = mine >= 8 ? 1 : mine >= 4 ? 2 : mine >= 2 ? 4 : 8;  // warps per task
+    for (int k0 = 0; k0 < mine; k0 += kJoinWarps / share) {
+      const int k = k0 + warp / share, sub = warp % share;
+      const int x = rank + k * n, h = x / parts, e = x % parts * 64 + 2 * lane;
+      float lsum = 0.f, a = 0.f, b = 0.f;
+      if (k < mine) {
+        float M = -INFINITY;
+        for (int i = lane; i < n; i += 32) M = fmaxf(M, p.ws_ml[slot(d, i) + h].x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        for (int i = lane; i < n; i += 32) {
+          const float2 ml = p.ws_ml[slot(d, i) + h];
+          lsum = fmaf(exp2_approx(ml.x - M), ml.y, lsum);
+        }
+        lsum = group_sum<32>(lsum);  // of all pieces, in every warp of the task
+        for (int base = sub; base < n; base += 32 * share) {  // pieces base, base + share, ...
+          const int at = base + lane * share;
+          const float f = at < n ? exp2_approx(p.ws_ml[slot(d, at) + h].x - M) : 0.f;
+          for (int i0 = 0; i0 < 32 && base + i0 * share < n; i0 += 16) {
+            float2 o[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int j = base + (i0 + i) * share;
+              o[i] = j < n ? *reinterpret_cast<const float2*>(p.ws_o + (slot(d, j) + h) * D + e) : make_float2(0.f, 0.f);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float w = __shfl_sync(0xffffffffu, f, i0 + i);
+              a = fmaf(w, o[i].x, a);
+              b = fmaf(w, o[i].y, b);
+            }
+          }
+        }
+      }
+      if (share > 1) {
+        __syncthreads();  // the sums of the tasks before have been read
+        partial[warp][lane] = make_float2(a, b);
+        __syncthreads();
+        if (sub == 0)
+          for (int w = 1; w < share; ++w) {
+            const float2 y = partial[warp + w][lane];
+            a += y.x;
+            b += y.y;
+          }
+      }
+      if (sub == 0 && k < mine) store_pair(p.out, (first_row(d) + h) * D + e, a / lsum, b / lsum, p.out_dtype);
+    }
   }
 }
 

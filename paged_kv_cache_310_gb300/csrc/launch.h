@@ -140,7 +140,8 @@ struct Kv4DecodeParams {
   const int32_t* block_tables;
   const int32_t* context_lens;
   void* out;
-  int4* desc;    // workspace [ctas]: the item a CTA's span leaves unfinished; NULL: none can be
+  int4* desc;    // workspace [ctas][2]: the unfinished items a CTA continues and begins (sequence, KV head,
+                 // first and last CTA; -1: none); NULL: none can be
   float2* ws_ml; // workspace [2 ctas][G]: (maximum, sum) of an unfinished item
   float* ws_o;   // workspace [2 ctas][G][D]: its un-normalised output
   int* err;

@@ -107,6 +107,8 @@ def test_parity(q_dtype, d, bs, group, hkv):
 
 
 @pytest.mark.parametrize("lens,hq,hkv,d,bs", [([4097, 1, 5000], 8, 2, 128, 16), ([9001], 4, 1, 64, 8),
+                                              ([70001], 16, 1, 128, 16), ([30011, 9000, 17], 2, 1, 64, 64),
+                                              ([20000, 5], 5, 1, 128, 32),
                                               ([2049, 2048, 2047, 511], 16, 1, 128, 64)])
 def test_long_contexts(lens, hq, hkv, d, bs):
     c = Case(310_830 + len(lens), lens, hq, hkv, d, bs, "f32")
