@@ -13,23 +13,20 @@
 //    latency of its passes, not bytes: of 13 us for 32,767 rows in a cluster, 1.4 are the
 //    load, 2 each pass, 1 the counts for the other CTAs, 4 the ordered pass.  Digits of eleven
 //    bits (four passes of eight before) spread accumulators of similar size over more
-//    counters; 512 threads leave room for two CTAs per SM, so that a batch of 256 runs at once
-//    (32 sequences of 512 to 4,096 rows, 8 heads: 81 us a call, 85 with 1,024 threads).
+//    counters (32 sequences of 512 to 4,096 rows, 8 heads: 81 us a call).
 //  * move_kernel copies the kept rows of K and V into the sequence's new blocks, 16 bytes
 //    (8 where rows are 40) per thread.  Bound: HBM; each kept row is read and written once:
 //    69 us of that call, 413 MB, 6.0 TB/s.
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 
 namespace pkv {
 namespace {
 
-constexpr int kSelectThreads = 512;
-constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kPerLane = 8;  // rows per lane and step of the ordered pass: a warp takes 32 at a time
 constexpr int kDigits = 2048;  // eleven bits a pass
-constexpr int kBins = kDigits / kSelectThreads;
-static_assert(kBins == 4 && kSelectWarps <= 32, "a thread reads its bins as one vector; one warp scans the warps' sums");
 constexpr int kMaxKeys = 48 * 1024;  // rows whose weights fit in shared memory
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRows = 32;  // kept rows per CTA (that batch: 81 us; with 16, 86; with 64, 82)
@@ -48,6 +45,12 @@ __device__ __forceinline__ uint32_t cluster_load(const uint32_t* mine, uint32_t 
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_address(mine, rank)) : "memory");
   return v;
 }
+__device__ __forceinline__ uint2 cluster_load(const uint2* mine, uint32_t rank) {
+  uint2 v;
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(cluster_address(mine, rank)) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ uint4 cluster_load(const uint4* mine, uint32_t rank) {
   uint4 v;
   asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -56,6 +59,8 @@ __device__ __forceinline__ uint4 cluster_load(const uint4* mine, uint32_t rank) 
                : "memory");
   return v;
 }
+__device__ __forceinline__ void unpack(const uint2& v, uint32_t (&x)[2]) { x[0] = v.x, x[1] = v.y; }
+__device__ __forceinline__ void unpack(const uint4& v, uint32_t (&x)[4]) { x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w; }
 
 // Larger weight, larger key; -0 as +0; NaN as -infinity.
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -64,11 +69,16 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 // kSize CTAs per (KV head, sequence): a cluster along x.
-template <int kSize>
-__global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_constant__ EvictParams p) {
+template <int kSize, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) select_kernel(const __grid_constant__ EvictParams p) {
+  constexpr int kWarps = kThreads / 32;
+  constexpr int kBins = kDigits / kThreads;  // digits of a thread
+  using Bins = std::conditional_t<kBins % 4 == 0, uint4, uint2>;  // read at once
+  constexpr int kAtOnce = sizeof(Bins) / 4;
+  static_assert(kBins % 2 == 0 && kWarps <= 32, "bins are read in pairs; one warp adds up the warps' sums");
   __shared__ __align__(16) uint32_t hist[2][kDigits];  // this CTA's counts, of even and odd passes
   __shared__ uint32_t totals[2];                       // this CTA's rows above the threshold, and ties
-  __shared__ uint32_t warp_sum[kSelectWarps];
+  __shared__ uint32_t warp_sum[kWarps];
   __shared__ uint32_t found[3];  // digit, rows still to take among it, rows that have it
   extern __shared__ float held_weights[];
   grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
@@ -95,17 +105,18 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_
   bool held = false;
   if (k - r > 0 && k - r < candidates) {
     held = own <= p.key_room;
-    reinterpret_cast<uint4*>(hist[0])[tid] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < kBins; ++i) hist[0][tid + i * kThreads] = 0;
     __syncthreads();
     constexpr int kBatch = 8;  // loads in flight per thread
-    for (int j0 = tid; j0 < own; j0 += kSelectThreads * kBatch) {
+    for (int j0 = tid; j0 < own; j0 += kThreads * kBatch) {
       float x[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) x[i] = j0 + i * kSelectThreads < own ? w[first + j0 + i * kSelectThreads] : 0.f;
+      for (int i = 0; i < kBatch; ++i) x[i] = j0 + i * kThreads < own ? w[first + j0 + i * kThreads] : 0.f;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
-        if (j0 + i * kSelectThreads < own) {
-          if (held) held_weights[j0 + i * kSelectThreads] = x[i];
+        if (j0 + i * kThreads < own) {
+          if (held) held_weights[j0 + i * kThreads] = x[i];
           atomicAdd(&hist[0][weight_key(x[i]) >> 21], 1u);
         }
     }
@@ -117,7 +128,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_
         const int above_bits = pass == 1 ? 21 : 10;
         const uint32_t mask = pass == 1 ? 2047u : 1023u;
 #pragma unroll 4
-        for (int j = tid; j < own; j += kSelectThreads) {
+        for (int j = tid; j < own; j += kThreads) {
           const uint32_t key = weight_key(held ? held_weights[j] : w[first + j]);  // what this thread put there
           if ((key >> above_bits) == (threshold >> above_bits)) atomicAdd(&mine[(key >> shift) & mask], 1u);
         }
@@ -127,21 +138,32 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_
       else
         __syncthreads();
       // the other buffer is free: everybody read it before arriving at the barrier
-      reinterpret_cast<uint4*>(hist[(pass & 1) ^ 1])[tid] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < kBins; ++i) hist[(pass & 1) ^ 1][tid + i * kThreads] = 0;
       // thread 0 holds the largest digits: the digit whose rows from the top reach `need`
-      const int group = kSelectThreads - 1 - tid;
-      const uint4* bins = reinterpret_cast<const uint4*>(mine) + group;
-      uint4 c = *bins, theirs[kSize];
+      const int lowest = (kThreads - 1 - tid) * kBins;
+      const Bins* bins = reinterpret_cast<const Bins*>(mine + lowest);
+      uint32_t count[kBins], sum = 0;  // from its largest digit down
 #pragma unroll
-      for (int i = 1; i < kSize; ++i) theirs[i] = cluster_load(bins, (rank + i) % kSize);
+      for (int u = 0; u < kBins / kAtOnce; ++u) {
+        Bins theirs[kSize];
+        theirs[0] = bins[u];
 #pragma unroll
-      for (int i = 1; i < kSize; ++i) {
-        c.x += theirs[i].x;
-        c.y += theirs[i].y;
-        c.z += theirs[i].z;
-        c.w += theirs[i].w;
+        for (int i = 1; i < kSize; ++i) theirs[i] = cluster_load(bins + u, (rank + i) % kSize);
+        uint32_t c[kAtOnce] = {};
+#pragma unroll
+        for (int i = 0; i < kSize; ++i) {
+          uint32_t y[kAtOnce];
+          unpack(theirs[i], y);
+#pragma unroll
+          for (int e = 0; e < kAtOnce; ++e) c[e] += y[e];
+        }
+#pragma unroll
+        for (int e = 0; e < kAtOnce; ++e) {
+          count[kBins - 1 - kAtOnce * u - e] = c[e];
+          sum += c[e];
+        }
       }
-      const uint32_t count[kBins] = {c.w, c.z, c.y, c.x}, sum = c.x + c.y + c.z + c.w;
       uint32_t above = sum;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -154,7 +176,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < kBins; ++i) {
         if (above < need && above + count[i] >= need) {
-          found[0] = 4 * group + 3 - i;
+          found[0] = lowest + kBins - 1 - i;
           found[1] = need - above;
           found[2] = count[i];
         }
@@ -181,7 +203,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_
     uint32_t above = 0, equal = 0;
     if (k - r > 0) {
 #pragma unroll 4
-      for (int j = tid; j < own; j += kSelectThreads) {
+      for (int j = tid; j < own; j += kThreads) {
         const uint32_t key = weight_key(held ? held_weights[j] : w[first + j]);
         above += key > threshold;
         equal += key == threshold;
@@ -202,7 +224,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_
   }
   int32_t* kept = p.kept + row * p.max_keep;
   float* out = p.weights_out + row * p.width;
-  constexpr int kStep = kSelectThreads * kPerLane;
+  constexpr int kStep = kThreads * kPerLane;
   for (int j0 = first; j0 < last; j0 += kStep) {
     const int j = j0 + warp * 32 * kPerLane + lane;
     float x[kPerLane];
@@ -222,7 +244,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const __grid_
     }
     if (lane == 0) warp_sum[warp] = count;
     __syncthreads();
-    const uint32_t theirs = lane < kSelectWarps ? warp_sum[lane] : 0u;
+    const uint32_t theirs = lane < kWarps ? warp_sum[lane] : 0u;
     const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0u);
     const uint32_t all = __reduce_add_sync(0xffffffffu, theirs);
     uint32_t a = above_before + (before & 0xffffu), e = ties_before + (before >> 16);
@@ -278,16 +300,16 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
   }
 }
 
-template <int kSize>
+template <int kSize, int kThreads>
 cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
   static std::atomic<unsigned long long> configured{0};
-  const cudaError_t e = ensure_smem_limit(select_kernel<kSize>, kMaxKeys * 4, configured);
+  const cudaError_t e = ensure_smem_limit(select_kernel<kSize, kThreads>, kMaxKeys * 4, configured);
   if (e != cudaSuccess) return e;
   const dim3 grid(kSize, p.num_kv_heads, p.num_seqs);
-  if (kSize == 1) return launch_dependent(select_kernel<kSize>, grid, kSelectThreads, p.key_room * 4, stream, p);
+  if (kSize == 1) return launch_dependent(select_kernel<kSize, kThreads>, grid, kThreads, p.key_room * 4, stream, p);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kSelectThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = p.key_room * 4;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -299,7 +321,14 @@ cudaError_t launch_select(const EvictParams& p, cudaStream_t stream) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, select_kernel<kSize>, p);
+  return cudaLaunchKernelEx(&cfg, select_kernel<kSize, kThreads>, p);
+}
+
+template <int kThreads>
+cudaError_t launch_cluster(const EvictParams& p, int size, cudaStream_t stream) {
+  return size == 2   ? launch_select<2, kThreads>(p, stream)
+         : size == 4 ? launch_select<4, kThreads>(p, stream)
+                     : launch_select<8, kThreads>(p, stream);
 }
 
 template <typename V>
@@ -315,7 +344,7 @@ cudaError_t launch_move(const EvictParams& p, cudaStream_t stream) {
 cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
   // A selection's passes are bound by its CTA's instructions, so few long ones are shared by up
   // to eight CTAs each, as many as leave two CTAs per SM and 4,096 rows each (one sequence of
-  // 32,767 rows, 4 heads: 16.9 us a call with four CTAs, 22.4 with two); a batch that fills the
+  // 32,767 rows, 4 heads: 16.1 us a call with four CTAs, 22.4 with two); a batch that fills the
   // GPU by itself gains nothing, and with fewer rows the barriers cost more than they save (16
   // sequences of 4,096 rows, 8 heads: 30.4 us with one CTA each, 33.6 with two).  Clusters of
   // sixteen lose: 83 us in place of 72 for 131,072 rows.
@@ -324,10 +353,15 @@ cudaError_t launch_evict(EvictParams p, cudaStream_t stream) {
   while (size < 8 && items * size * 2 <= 2 * 152 && p.max_len / (size * 2) >= 4096) size *= 2;
   const int most = (p.max_len + size - 1) / size;
   p.key_room = most < kMaxKeys ? most : kMaxKeys;
-  const cudaError_t e = size == 1   ? launch_select<1>(p, stream)
-                        : size == 2 ? launch_select<2>(p, stream)
-                        : size == 4 ? launch_select<4>(p, stream)
-                                    : launch_select<8>(p, stream);
+  // Threads: enough CTAs for every SM side by side (256 sequences of 1,024 rows, 8 heads: 100 us
+  // a call with 128, 120 with 512; 32 of 4,096: 52 with 512, 54 with 256, 65 with 128); a
+  // thousand where clusters leave a CTA an SM and many rows (one of 131,072, 8 heads: 69 us
+  // against 72; four of 32,768, which are two CTAs per SM: 81 against 66).
+  const cudaError_t e = size > 1 && items * size <= 152 && most > 4096 ? launch_cluster<1024>(p, size, stream)
+                        : size > 1                                     ? launch_cluster<512>(p, size, stream)
+                        : p.max_len <= 1024                            ? launch_select<1, 128>(p, stream)
+                        : p.max_len <= 2048                            ? launch_select<1, 256>(p, stream)
+                                                                       : launch_select<1, 512>(p, stream);
   if (e != cudaSuccess) return e;
   return p.row_bytes % 16 == 0 ? launch_move<uint4>(p, stream) : launch_move<uint2>(p, stream);
 }

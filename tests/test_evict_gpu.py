@@ -207,6 +207,13 @@ def test_evict_long(n, keep, recent):
     Evict(311_120, [n, 50, 3, 0, 1], [keep, 20, 2, 1, 1], recent, 1, 64, 16, "bf16").check()
 
 
+@pytest.mark.parametrize("seqs,longest,heads", [(20, 1024, 8), (9, 2048, 3), (3, 3000, 2), (1, 9000, 2), (1, 16000, 1),
+                                                (4, 33000, 8), (2, 40000, 3)])
+def test_evict_with_every_number_of_threads(seqs, longest, heads):
+    lens = [longest - 7 * s for s in range(seqs)]
+    Evict(311_125, lens, [n // 3 + 1 for n in lens], 11, heads, 64, 16, "f16").check()
+
+
 @pytest.mark.parametrize("value", [0.0, 1.0, float("nan"), float("-inf"), float("inf")])
 def test_evict_equal_weights_keep_the_lowest_rows(value):
     for n, keep, heads in ((5000, 1234, 2), (20000, 12345, 1)):   # one CTA or a cluster a head
