@@ -101,6 +101,12 @@ pkv_status plan_weights(int32_t num_seqs, int32_t num_q_heads, int32_t max_len, 
   plan->ml_bytes = (heads * plan->max_parts * 2 * sizeof(float) + 255) / 256 * 256;
   plan->ld = (static_cast<int64_t>(max_len) + 31) / 32 * 32;
   plan->workspace = num_seqs == 0 || max_len == 0 ? 0 : plan->ml_bytes + heads * plan->ld * sizeof(float);
+  if (max_len <= kWeightsOne) {
+    plan->part_tokens = max_len < 128 ? 128 : (max_len + 127) / 128 * 128;
+    plan->max_parts = 1;
+    plan->ld += 4;  // rows of scores in shared memory: eight tokens of four heads in different banks
+    plan->workspace = 0;
+  }
   return PKV_OK;
 }
 
@@ -273,8 +279,10 @@ pkv_status paged_attention_weights(const void* q, int32_t q_dtype, const void* k
   p.tracked_lens = tracked_lens;
   p.weights = weights;
   p.weights_out = weights_out;
-  p.ws_ml = static_cast<float*>(workspace);
-  p.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.ml_bytes);
+  if (plan.workspace > 0) {
+    p.ws_ml = static_cast<float*>(workspace);
+    p.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.ml_bytes);
+  }
   p.err = flag;
   p.width = weights_width;
   p.scores_ld = plan.ld;

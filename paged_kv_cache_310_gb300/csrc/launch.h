@@ -165,7 +165,7 @@ struct WeightsParams {
   const int32_t* tracked_lens;  // NULL: every row has an accumulator
   const float* weights;         // [S][Hkv][width]
   float* weights_out;           // may be weights
-  float* scores;                // workspace [S][Hq][scores_ld]: log2-domain scores
+  float* scores;                // workspace [S][Hq][scores_ld]: log2-domain scores; NULL: kept in shared memory
   float* ws_ml;                 // workspace [S][Hq][max_parts][2]
   int* err;
   int64_t width, scores_ld;
@@ -175,6 +175,7 @@ struct WeightsParams {
   Kv4Bits bits;
 };
 constexpr int kWeightsMaxGroup = 16;
+constexpr int kWeightsOne = 512;  // up to here one CTA sees all tokens of a (sequence, KV head)
 cudaError_t launch_weights(const WeightsParams& p, int dtype, cudaStream_t stream);
 
 struct EvictParams {

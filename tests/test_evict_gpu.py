@@ -87,9 +87,24 @@ def test_weights_parity(pool, q_dtype, d, bs, group, hkv):
     c.check(tracked=[n + 5 for n in LENS])
 
 
+@pytest.mark.parametrize("pool,q_dtype", [("f32", None), ("f16", None), ("bf16", None), ("kv4", "f16"), ("kv4", "bf16"),
+                                          ("kv4", "f32")])
+@pytest.mark.parametrize("d,bs,group,hkv", [(64, 16, 1, 3), (128, 16, 8, 2), (128, 8, 5, 1), (64, 64, 16, 1), (128, 32, 16, 1)])
+def test_weights_of_contexts_that_one_cta_sees_whole(pool, q_dtype, d, bs, group, hkv):
+    for lens in ([512, 0, 1, 511, 300], [7, 128, 127], [1], [129, 20], [513, 512]):   # the last: two kernels
+        c = Step(311_010 + d + bs + group + len(lens), lens, group * hkv, hkv, d, bs, pool, q_dtype)
+        c.check()
+        c.check(tracked=[max(0, n - 3) for n in lens], in_place=True)
+
+
 @pytest.mark.parametrize("pool,q_dtype", [("f32", None), ("bf16", None), ("kv4", "f16")])
 def test_weights_over_several_partitions(pool, q_dtype):
     Step(311_020, [5001, 4096, 700], 8, 2, 128, 16, pool, q_dtype, width=8192).check()
+
+
+def test_weights_of_a_batch_whose_partitions_are_whole_contexts():
+    # so many items that a partition holds 4,096 tokens, the whole of each context
+    Step(311_025, [4000] + [40] * 950, 4, 2, 64, 64, "bf16").check()
 
 
 def test_weights_of_a_step_sum_to_the_group():
