@@ -352,8 +352,8 @@ pkv_status paged_kv4_expand(const int64_t* src_dst_pairs, int32_t num_pairs, con
  * index flag and is skipped.  The batch's tokens are shared out evenly among the CTAs,
  * whatever the lengths; sequences that cross a CTA's share are joined by a second kernel.
  * workspace: at least paged_attention_decode_kv4_workspace_bytes(...) bytes (0 when
- * max_context_len <= 128), 256-byte aligned, one per call in flight; its size does not grow
- * with the batch or the lengths past a limit of some 20 MB.  The result does not depend on
+ * max_context_len <= 128, and for small batches up to 512), 256-byte aligned, one per call in
+ * flight; its size does not grow with the batch or the lengths past a limit of some 20 MB.  The result does not depend on
  * which physical blocks hold a sequence; where a sequence is cut depends on the lengths of
  * the whole batch, which can change its last bits.  out must not alias any input.
  */

@@ -22,6 +22,7 @@ pkv_status check_kv4(const pkv_cache_desc* c) {
 
 struct Kv4Plan {
   int ctas;
+  bool whole;
   size_t ml_at, o_at, workspace;  // offsets of the workspace's parts; 0 bytes: no item is ever split
 };
 
@@ -44,6 +45,11 @@ pkv_status plan_kv4(int32_t num_seqs, int32_t num_q_heads, int32_t max_len, int3
   const int64_t items = static_cast<int64_t>(num_seqs) * c->num_kv_heads;
   plan->ctas = kv4_decode_ctas(c->head_dim, group, q_dtype, most, items < 1 ? 1 : items);
   plan->ml_at = plan->o_at = plan->workspace = 0;
+  plan->whole = max_len <= kKv4Whole && items <= kv4_decode_ctas(c->head_dim, group, q_dtype, int64_t{1} << 50, 1);
+  if (plan->whole) {
+    plan->ctas = items < 1 ? 1 : static_cast<int>(items);
+    return PKV_OK;
+  }
   if (units > 1 && plan->ctas > 1 && num_seqs > 0) {
     const size_t rows = static_cast<size_t>(2) * plan->ctas * group;
     plan->ml_at = (plan->ctas * 32 + 255) / 256 * 256;
@@ -230,6 +236,7 @@ pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void
   p.head_dim = cache->head_dim;
   p.max_len = max_context_len;
   p.ctas = plan.ctas;
+  p.whole = plan.whole;
   p.scale_log2 = scale * 1.4426950408889634f;
   cudaError_t e = launch_decode_kv4(p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "4-bit decode launch");

@@ -90,8 +90,9 @@ struct Kv4 {
 
 // What a sequence costs per KV head, in units: its units and what an item costs of its own
 // (none where the length is 0 or out of range).
-__device__ __forceinline__ int cost_of(int len, int max_len) {
-  return len <= 0 || len > max_len ? 0 : (len + kUnit - 1) / kUnit + kItemCost;
+// whole: one, so that each of as many spans is an item (kKv4Whole).
+__device__ __forceinline__ int cost_of(int len, int max_len, bool whole) {
+  return len <= 0 || len > max_len ? 0 : whole ? 1 : (len + kUnit - 1) / kUnit + kItemCost;
 }
 
 // Query fragments of 4-bit K rows in shared memory: piece [w][4 g + t] (16 bytes) is lane
@@ -206,7 +207,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
 
   // ---- this CTA's span of the batch's units
   int64_t total = 0;
-  for (int s = threadIdx.x; s < p.num_seqs; s += kThreads) total += cost_of(p.context_lens[s], p.max_len);
+  for (int s = threadIdx.x; s < p.num_seqs; s += kThreads) total += cost_of(p.context_lens[s], p.max_len, p.whole);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   if (lane == 0) scan[warp] = total;
@@ -216,17 +217,17 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
   for (int w = 0; w < kWarps; ++w) total += scan[w];
   __syncthreads();
   const int64_t units = total * p.num_kv_heads;  // the batch's cost
-  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), (units + kMinCost - 1) / kMinCost);
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), p.whole ? units : (units + kMinCost - 1) / kMinCost);
   if (threadIdx.x < 2 && p.desc) p.desc[2 * blockIdx.x + threadIdx.x] = make_int4(-1, 0, 0, 0);
   if (static_cast<int64_t>(blockIdx.x) >= ctas) return;
-  const int64_t begin = blockIdx.x * units / ctas, end = (blockIdx.x + 1) * units / ctas;
+  int64_t begin = blockIdx.x * units / ctas, end = (blockIdx.x + 1) * units / ctas;
 
   // ---- the sequence it starts in: the last one with (cost before it) * heads <= begin
   {
     int64_t before = 0;
     for (int base = 0; base < p.num_seqs; base += kThreads) {
       const int s = base + threadIdx.x;
-      const int mine = s < p.num_seqs ? cost_of(p.context_lens[s], p.max_len) : 0;
+      const int mine = s < p.num_seqs ? cost_of(p.context_lens[s], p.max_len, p.whole) : 0;
       int64_t incl = mine;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -251,12 +252,19 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
       if (begin < before * p.num_kv_heads) break;  // found: begin < units, so it always is
     }
   }
-  int s = start_seq, L = p.context_lens[s], cost = cost_of(L, p.max_len);
+  int s = start_seq, L = p.context_lens[s], cost = cost_of(L, p.max_len, false);
   int kvh, at_cost;  // KV head of the item, and where in its cost the span begins
   {
     const int64_t r = begin - start_before * p.num_kv_heads;
-    kvh = static_cast<int>(r / cost);
-    at_cost = static_cast<int>(r - static_cast<int64_t>(kvh) * cost);
+    if (p.whole) {  // the span is item r of the sequence
+      kvh = static_cast<int>(r);
+      at_cost = 0;
+      begin = 0;
+      end = cost;
+    } else {
+      kvh = static_cast<int>(r / cost);
+      at_cost = static_cast<int>(r - static_cast<int64_t>(kvh) * cost);
+    }
   }
 
   uint4* q_frag = reinterpret_cast<uint4*>(smem + C::kMainBytes);
@@ -668,7 +676,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
     do {
       if (++s >= p.num_seqs) return;  // not reached: the span has cost left
       L = p.context_lens[s];
-      cost = cost_of(L, p.max_len);
+      cost = cost_of(L, p.max_len, false);
     } while (cost == 0);
   }
   }

@@ -147,11 +147,15 @@ struct Kv4DecodeParams {
   int* err;
   int32_t q_dtype, out_dtype, num_seqs, num_q_heads, num_kv_heads, group, max_blocks_per_seq;
   int32_t block_size, num_blocks, head_dim, max_len, ctas;
+  bool whole;  // a CTA takes whole items
   float scale_log2;
   Kv4Bits bits;
 };
 constexpr int kKv4MaxGroup = 16;
 constexpr int kKv4Unit = 128;  // tokens of one unit of work
+// Up to here items are not split if the GPU holds a CTA for each at once: no workspace and no
+// second kernel, which cost more than splitting so few tokens saves.
+constexpr int kKv4Whole = 512;
 // CTAs of a call over at most max_units units in `items` (sequence, KV head) items.
 int kv4_decode_ctas(int head_dim, int group, int q_dtype, int64_t max_units, int64_t items);
 cudaError_t launch_decode_kv4(const Kv4DecodeParams& p, cudaStream_t stream);

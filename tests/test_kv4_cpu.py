@@ -168,6 +168,9 @@ def test_decode_checks(lib):
     big = lib.paged_attention_decode_kv4_workspace_bytes(512, 32, 1 << 20, pkv.BF16, ctypes.byref(d))
     assert big == lib.paged_attention_decode_kv4_workspace_bytes(64, 32, 1 << 18, pkv.BF16, ctypes.byref(d)) < 32 << 20
     assert lib.paged_attention_decode_kv4_workspace_bytes(4, 32, 64, pkv.BF16, ctypes.byref(d)) == 0    # no split
+    assert lib.paged_attention_decode_kv4_workspace_bytes(4, 32, 512, pkv.BF16, ctypes.byref(d)) == 0
+    assert lib.paged_attention_decode_kv4_workspace_bytes(4, 32, 513, pkv.BF16, ctypes.byref(d)) > 0
+    assert lib.paged_attention_decode_kv4_workspace_bytes(512, 32, 512, pkv.BF16, ctypes.byref(d)) > 0
     assert lib.paged_attention_decode_kv4_workspace_bytes(4, 30, 4096, pkv.BF16, ctypes.byref(d)) == 0  # invalid
     assert run(L=(1 << 30) + 1, width=1 << 30) == 2
     assert run(L=1 << 30, S=65535, d=desc(num_kv_heads=65535, head_dim=64, block_size=8), Hq=65535, width=1 << 30) == 2
