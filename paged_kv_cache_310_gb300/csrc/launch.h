@@ -154,7 +154,8 @@ struct Kv4DecodeParams {
 constexpr int kKv4MaxGroup = 16;
 constexpr int kKv4Unit = 128;  // tokens of one unit of work
 // Up to here items are not split if the GPU holds a CTA for each at once: no workspace and no
-// second kernel, which cost more than splitting so few tokens saves.
+// second kernel, which cost more than splitting so few tokens saves (70 sequences of 512, 32/8
+// heads: 14 us against 20; one: 8 against 9).
 constexpr int kKv4Whole = 512;
 // CTAs of a call over at most max_units units in `items` (sequence, KV head) items.
 int kv4_decode_ctas(int head_dim, int group, int q_dtype, int64_t max_units, int64_t items);
