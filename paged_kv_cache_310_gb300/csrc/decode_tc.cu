@@ -1061,13 +1061,20 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
 // over at most 32 chunk counts; order inside one count does not matter, every item
 // is computed the same way wherever it runs).  Sequences of length 0 get their
 // all-zero output here; lengths outside [0, max_parts * part_tokens] set the flag.
+//
+// Launched as a programmatic dependent: the kernel before on the stream may still run (the
+// library's appends, expansion and attention weights let it start).  Such a kernel has itself
+// waited for all that came before it, and none writes context lengths, so these are read and
+// counted at once.  What is written here may lie in memory that the kernel before still reads
+// or writes -- the caller's workspace and output can be buffers that its call was given, or
+// freed ones -- so the first write comes after the wait, which also makes the decode kernel's
+// wait on this grid cover the kernel before.
 constexpr int kListThreads = 1024;
 constexpr int kMaxChunkCounts = kTcMaxPartition / kChunk;
 
 template <typename T>
 __global__ void __launch_bounds__(kListThreads) work_list_kernel(const __grid_constant__ DecodeParams p) {
   grid_dependents_launch();  // the decode kernel may start its prologue now
-  if (threadIdx.x == 0) *p.work_next = 0;  // claims past the decode grid's first items
   __shared__ int hist[kMaxChunkCounts + 1];
   __shared__ int next[kMaxChunkCounts + 1];
   const int full_chunks = p.part_tokens / kChunk;
@@ -1085,13 +1092,17 @@ __global__ void __launch_bounds__(kListThreads) work_list_kernel(const __grid_co
     if (rem) atomicAdd(&hist[(rem + kChunk - 1) / kChunk], H);
   }
   __syncthreads();
+  int run = 0;
   if (threadIdx.x == 0) {
-    int run = 0;
     for (int c = kMaxChunkCounts; c >= 1; --c) {
       next[c] = run;
       run += hist[c];
     }
+  }
+  grid_dependency_wait();
+  if (threadIdx.x == 0) {
     *p.work_count = run;
+    *p.work_next = 0;  // claims past the decode grid's first items
   }
   __syncthreads();
   for (int s = threadIdx.x; s < p.num_seqs; s += kListThreads) {
@@ -1112,10 +1123,6 @@ __global__ void __launch_bounds__(kListThreads) work_list_kernel(const __grid_co
     if (p.context_lens[s] != 0) continue;
     for (int i = lane; i < row; i += 32) store_out<T>(p.out, static_cast<size_t>(s) * row + i, 0.f, p.out_f32);
   }
-  // Launched as a programmatic dependent of the previous kernel (the append, whose
-  // writes this kernel does not read): finish only after it, so the decode kernel's
-  // wait on this one also covers the append.
-  grid_dependency_wait();
 }
 
 // 2-D map over rows of head_dim 16-bit elements, box 64 x box_rows, 128-byte swizzle.

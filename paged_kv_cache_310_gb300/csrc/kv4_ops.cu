@@ -40,7 +40,7 @@ struct Raw8 {
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const __grid_constant__ Kv4AppendParams p) {
   grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
-  grid_dependents_launch();  // a following kernel's launch may overlap this one; it waits before reading
+  grid_dependents_launch();  // the next kernel's launch may overlap this one; it waits before it writes
   const int row_log2 = p.head_dim == 128 ? 4 : 3;  // threads per row
   const int per_token = p.num_kv_heads << row_log2;
   const int x = blockIdx.y * kThreads + threadIdx.x;
@@ -118,7 +118,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* out, const uint32_t (&v)[4
 template <typename T>
 __global__ void __launch_bounds__(kThreads) kv4_expand_kernel(const __grid_constant__ Kv4ExpandParams p) {
   grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
-  grid_dependents_launch();  // the next kernel's launch may overlap this one
+  grid_dependents_launch();  // the next kernel's launch may overlap this one; it waits before it writes
   const int words_log2 = p.head_dim == 128 ? 4 : 3, words = 1 << words_log2, row_words = words * 5 / 4;
   const int rows = p.num_kv_heads * p.block_size, total = rows * words;  // of one block
   const int64_t first = static_cast<int64_t>(blockIdx.x) * p.pairs_per_cta;

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) scores_kernel(const __grid_constant_
   __shared__ volatile uint32_t bit_patterns[3];
   __shared__ float2 join[kWeightsMaxGroup];  // (maximum, 1 / sum) of a query head
   grid_dependency_wait();    // of the kernel before: only this one's launch overlaps it
-  grid_dependents_launch();  // weights_kernel, or another call: they wait for this grid
+  grid_dependents_launch();  // weights_kernel, or another call's: it waits for this grid before it writes
 
   const int part = blockIdx.x, kvh = blockIdx.y, s = blockIdx.z;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
