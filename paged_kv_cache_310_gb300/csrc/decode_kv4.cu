@@ -19,8 +19,8 @@
 //  * P goes from the score layout to the B layout by 8 x 8 transposes, in two fp16 parts
 //    (p rounded, and the rest), so a weight is good to 2^-22.  Up to four heads per KV
 //    head the second part takes columns 4..7 (q's columns are doubled, so the lanes there
-//    hold the same p); above, a second MMA.  For bf16 outputs one part does: each weight is
-//    then off by up to 2^-12 of itself, either way, where the output's own rounding is 2^-8.
+//    hold the same p); above, a second MMA.  (One part would be 11 bits of a weight, 2^-11 of
+//    it, which a bf16 output shows next to its own 2^-8.)
 //
 // Work: a unit is 128 tokens of one (sequence, KV head), an item all units of one.  The
 // batch's items, in order of sequence and head, each with its units and kItemCost more for
@@ -37,8 +37,8 @@
 // log2 domain), sum and O, combined through shared memory at the item's end in a fixed
 // order.  Waits are cp.async.wait_group only.
 //
-// Measured (128 sequences of 512 to 4,096 tokens, 64/8 heads, bf16): 80 us a call, 0.70 of
-// copy bandwidth.  About 350 instructions per 16 tokens, 216 of them widening; the integer
+// Measured (128 sequences of 512 to 4,096 tokens, 64/8 heads, bf16): 88 us a call, 0.64 of
+// copy bandwidth (80 us with one fp16 part of the weights).  About 350 instructions per 16 tokens, 216 of them widening; the integer
 // and fp16 pipes are each busy 45 % of the time, the tensor pipe 22 %, HBM 70 %.
 #include <type_traits>
 
@@ -63,7 +63,7 @@ constexpr float kSlack = 8.f;      // a score may exceed the running maximum by 
 constexpr float kLift = 6.f;       // p = 2^(x - m + 6): small weights stay normal fp16 numbers
 
 // NB blocks of eight columns; kDup: at most four heads, in columns 0..3 and again in 4..7;
-// kSplit: f32 queries, in two fp16 parts.  (The kernel's kLo: weights in two fp16 parts.)
+// kSplit: f32 queries, in two fp16 parts.
 // The kernel's kRound, for f32 outputs: a step's products are summed by MMAs that start from
 // zero and added to O by additions that round to nearest.  The MMA truncates its sums; O kept
 // in its accumulator shrank by half a unit in the last place per MMA, 2.7e-6 of itself over
@@ -166,7 +166,7 @@ __device__ __forceinline__ void store_pair(void* out, size_t i, float x, float y
   }
 }
 
-template <int D, int NB, bool kDup, bool kSplit, bool kLo, bool kRound>
+template <int D, int NB, bool kDup, bool kSplit, bool kRound>
 __global__ void __launch_bounds__(kThreads, Kv4<D, NB, kDup, kSplit>::kCtasPerSm)
 decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
   using C = Kv4<D, NB, kDup, kSplit>;
@@ -435,7 +435,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
 
     // ---- softmax; tokens past the end get -inf
     uint32_t ph[NB][kSub][2];                   // P^T fragments: tokens 0-7 and 8-15
-    [[maybe_unused]] uint32_t pl[NB][kSub][2];  // their second parts
+    [[maybe_unused]] uint32_t pl[NB][kSub][2];  // their second parts (kDup: in ph's columns 4..7)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
       float x[kSub][4];  // score - m + 6
@@ -490,17 +490,15 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
         l[nb][0] += e[0] + e[2];
         l[nb][1] += e[1] + e[3];
         uint32_t h0 = pack_half2(e[0], e[1]), h1 = pack_half2(e[2], e[3]);
-        if constexpr (kLo) {
-          const uint32_t r0 = pack_half2_rest(e[0], e[1], h0), r1 = pack_half2_rest(e[2], e[3], h1);
-          if constexpr (kDup) {
-            if (t >= 2) {
-              h0 = r0;
-              h1 = r1;
-            }
-          } else {
-            pl[nb][u][0] = movmatrix_trans(r0);
-            pl[nb][u][1] = movmatrix_trans(r1);
+        const uint32_t r0 = pack_half2_rest(e[0], e[1], h0), r1 = pack_half2_rest(e[2], e[3], h1);
+        if constexpr (kDup) {
+          if (t >= 2) {
+            h0 = r0;
+            h1 = r1;
           }
+        } else {
+          pl[nb][u][0] = movmatrix_trans(r0);
+          pl[nb][u][1] = movmatrix_trans(r1);
         }
         ph[nb][u][0] = movmatrix_trans(h0);
         ph[nb][u][1] = movmatrix_trans(h1);
@@ -545,7 +543,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
                 mma_f16_first(sum[nb], a[0], a[1], a[2], a[3], ph[nb][u][0], ph[nb][u][1]);
               else
                 mma_f16(sum[nb], a[0], a[1], a[2], a[3], ph[nb][u][0], ph[nb][u][1]);
-              if constexpr (kLo && !kDup) mma_f16(sum[nb], a[0], a[1], a[2], a[3], pl[nb][u][0], pl[nb][u][1]);
+              if constexpr (!kDup) mma_f16(sum[nb], a[0], a[1], a[2], a[3], pl[nb][u][0], pl[nb][u][1]);
             }
           }
 #pragma unroll
@@ -568,7 +566,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
               mma_f16(o[nb][4 * i + j], a[0], a[1], a[2], a[3], ph[nb][u][0], ph[nb][u][1]);
-              if constexpr (kLo && !kDup) mma_f16(o[nb][4 * i + j], a[0], a[1], a[2], a[3], pl[nb][u][0], pl[nb][u][1]);
+              if constexpr (!kDup) mma_f16(o[nb][4 * i + j], a[0], a[1], a[2], a[3], pl[nb][u][0], pl[nb][u][1]);
             }
           }
         }
@@ -786,29 +784,27 @@ __global__ void __launch_bounds__(kJoinThreads) join_kv4_kernel(const __grid_con
   }
 }
 
-template <int D, int NB, bool kDup, bool kSplit, bool kLo, bool kRound>
+template <int D, int NB, bool kDup, bool kSplit, bool kRound>
 cudaError_t launch_t(const Kv4DecodeParams& p, cudaStream_t stream) {
   using C = Kv4<D, NB, kDup, kSplit>;
   static std::atomic<unsigned long long> configured{0};
-  cudaError_t e = ensure_smem_limit(decode_kv4_kernel<D, NB, kDup, kSplit, kLo, kRound>, C::kSmemBytes, configured);
+  cudaError_t e = ensure_smem_limit(decode_kv4_kernel<D, NB, kDup, kSplit, kRound>, C::kSmemBytes, configured);
   if (e != cudaSuccess) return e;
-  return launch_dependent(decode_kv4_kernel<D, NB, kDup, kSplit, kLo, kRound>, p.ctas, kThreads, C::kSmemBytes, stream, p);
+  return launch_dependent(decode_kv4_kernel<D, NB, kDup, kSplit, kRound>, p.ctas, kThreads, C::kSmemBytes, stream, p);
 }
 
 template <int D, bool kSplit, bool kRound>
 cudaError_t launch_g(const Kv4DecodeParams& p, cudaStream_t stream) {
-  if (p.group <= 4) return launch_t<D, 1, true, kSplit, true, kRound>(p, stream);
-  if (p.group <= 8) return launch_t<D, 1, false, kSplit, true, kRound>(p, stream);
-  return launch_t<D, 2, false, kSplit, true, kRound>(p, stream);
+  if (p.group <= 4) return launch_t<D, 1, true, kSplit, kRound>(p, stream);
+  if (p.group <= 8) return launch_t<D, 1, false, kSplit, kRound>(p, stream);
+  return launch_t<D, 2, false, kSplit, kRound>(p, stream);
 }
 
 template <int D>
 cudaError_t launch_d(const Kv4DecodeParams& p, cudaStream_t stream) {
   if (p.q_dtype == PKV_F32) return launch_g<D, true, true>(p, stream);  // f32 out as well
   if (p.out_dtype == PKV_F32) return launch_g<D, false, true>(p, stream);
-  if (p.out_dtype == PKV_F16) return launch_g<D, false, false>(p, stream);
-  return p.group <= 8 ? launch_t<D, 1, false, false, false, false>(p, stream)
-                      : launch_t<D, 2, false, false, false, false>(p, stream);
+  return launch_g<D, false, false>(p, stream);
 }
 
 }  // namespace
