@@ -345,7 +345,10 @@ pkv_status paged_kv4_expand(const int64_t* src_dst_pairs, int32_t num_pairs, con
  * q: device [num_seqs][num_q_heads][head_dim] of q_dtype (f32, f16 or bf16); out: q's
  * dtype or f32; query-head groups up to 16.  Softmax, sums and products in fp32: q in fp16
  * (f32 q in two fp16 parts) after a power-of-two scaling of each head's row, weights in
- * two fp16 parts, so the result is good to a few 2^-22 before the output's rounding.
+ * two fp16 parts: each within 2^-22 of itself, or 2^-36 of the largest met where that is more
+ * (a weight below 2^-36 of it counts in the softmax's sum, not in the output).  Sums of n
+ * values add up to n / 16 roundings of 2^-23, f32 outputs' to nearest, f16 and bf16 outputs'
+ * towards zero (over 128 Ki tokens 2.7e-6 of the result), before the output's own rounding.
  * n == 0 gives zeros.  A NaN or infinity in a query row, or a NaN in a row attended to,
  * gives NaN as the formula does.  A sequence longer than max_context_len sets the device
  * index flag and is skipped.  The batch's tokens are shared out evenly among the CTAs,

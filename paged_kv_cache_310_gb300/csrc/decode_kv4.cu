@@ -17,7 +17,8 @@
 //  * V: lane (g, t) takes the g-th eighth of rows 2t, 2t+1, 2t+8, 2t+9; a byte permute
 //    pairs two tokens' codes of one dimension, as the contraction over tokens wants them.
 //  * P goes from the score layout to the B layout by 8 x 8 transposes, in two fp16 parts
-//    (p rounded, and the rest), so a weight is good to 2^-22.  Up to four heads per KV
+//    (p rounded, and the rest), so a weight is good to 2^-22 of itself, and to 2^-36 of the
+//    largest that the warp has met where that is more (kLift).  Up to four heads per KV
 //    head the second part takes columns 4..7 (q's columns are doubled, so the lanes there
 //    hold the same p); above, a second MMA.  (One part would be 11 bits of a weight, 2^-11 of
 //    it, which a bf16 output shows next to its own 2^-8.)
@@ -33,13 +34,14 @@
 //
 // Each of a CTA's four warps takes 32 of a unit's 128 tokens and runs alone: it has its own
 // ring of cp.async stages (lanes 0-7 bring K and V of the tile's first eight rows, 8-15 of
-// the next, ...), its own running maximum (raised only when a score exceeds it by 8,
+// the next, ...), its own running maximum (raised only when a score exceeds it by 4,
 // log2 domain), sum and O, combined through shared memory at the item's end in a fixed
 // order.  Waits are cp.async.wait_group only.
 //
 // Measured (128 sequences of 512 to 4,096 tokens, 64/8 heads, bf16): 88 us a call, 0.64 of
-// copy bandwidth (80 us with one fp16 part of the weights).  About 350 instructions per 16 tokens, 216 of them widening; the integer
-// and fp16 pipes are each busy 45 % of the time, the tensor pipe 22 %, HBM 70 %.
+// copy bandwidth (80 us with one fp16 part of the weights).  About 350 instructions per 16
+// tokens, 216 of them widening; the integer and fp16 pipes are each busy 45 % of the time, the
+// tensor pipe 22 %, HBM 70 %.
 #include <type_traits>
 
 #include "kv4.cuh"
@@ -59,8 +61,13 @@ static_assert(kUnit == kKv4Unit, "the host sizes the grid by it");
 constexpr int kItemCost = 2;       // an item's queries, first copies and sums cost about this many units
 constexpr int kMinCost = 3;        // per CTA at least
 constexpr int kOffs = 16;          // tiles whose block offsets a warp holds at a time
-constexpr float kSlack = 8.f;      // a score may exceed the running maximum by this much
-constexpr float kLift = 6.f;       // p = 2^(x - m + 6): small weights stay normal fp16 numbers
+constexpr float kSlack = 4.f;      // a score may exceed the running maximum by this much
+// p = 2^(x - m + 11), at most 2^15: as large as fp16 takes, since its numbers end at 2^-24, so the
+// second part of a small p, or all of it, is off by up to 2^-25.  (With a slack of 8 and a lift
+// of 6 that was 2^-31 of the largest weight: 2^-15 of weights that are 2^-16 of a sink's.  Raising
+// the maximum more often costs nothing that shows: 88 us and 73 us as before for 128 sequences of
+// 512 to 4,096 tokens and two of 128 Ki.)
+constexpr float kLift = 11.f;
 
 // NB blocks of eight columns; kDup: at most four heads, in columns 0..3 and again in 4..7;
 // kSplit: f32 queries, in two fp16 parts.
@@ -438,7 +445,7 @@ decode_kv4_kernel(const __grid_constant__ Kv4DecodeParams p) {
     [[maybe_unused]] uint32_t pl[NB][kSub][2];  // their second parts (kDup: in ph's columns 4..7)
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-      float x[kSub][4];  // score - m + 6
+      float x[kSub][4];  // score - m + kLift
       const float ma = kLift - m[nb][0], mb = kLift - m[nb][1];
       float top = -INFINITY;
 #pragma unroll

@@ -49,3 +49,37 @@ def test_weights_keep_32_bits(d, group, dtype):
     out = c.run(dtype).cpu()
     assert pkv.device_error() == 0
     check(c, dtype, out)
+
+
+@pytest.mark.parametrize("group", [1, 4, 8, 16])
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_weights_beside_a_heavy_token(d, group):
+    """A first token with 2^14 to 2^16 times the weight of each other and values of 0, as heads
+    that have nothing to say attend: what is left is the sum of the small weights, times 1.
+
+    Each is within 2^-22 of itself and 2^-36 of the heavy one (2^-20 of itself at most) by its two
+    fp16 parts, 2^-22 by exp2, and by the scores (the heavy one's, up to 16 in the log2 domain,
+    and their difference: 16 * 5 * 2^-24 ln 2, below 2^-18); the sums of 16 tokens and the division
+    add 2^-20.  Together below 2^-17 of the result.  (A heavy token in another warp, or parts that
+    hold 2^-31 of it, up to 2^-15 of a weight, is what this would tell from it.)"""
+    gen = torch.Generator().manual_seed(311_520)
+    seqs, n = 24, 16                                        # one warp's tokens
+    lens = [n] * seqs
+    size = (14 + 2 * torch.rand(seqs, group, generator=gen)) * np.log(2) / d ** -0.5
+    q = torch.zeros(seqs, group, d)
+    q[:, :, 0] = size
+    k = torch.zeros(1, n, d)
+    k[0, 0, 0] = 1.0                                        # step 1/15 in fp16: the heavy token's score is what the row holds
+    rows = [torch.from_numpy(model.quantise(k.double().numpy())) for _ in range(seqs)]
+    c = Case(311_521, lens, group, 1, d, 16, "f32", k_rows=rows, q=q)
+    one = torch.ones(1, n, d)
+    one[0, 0] = 0
+    for s in range(seqs):
+        c.v[c.tables[s, 0], :, :] = torch.from_numpy(model.quantise(one.double().numpy()))
+    out = c.run("f32").cpu().double()
+    assert pkv.device_error() == 0
+    ref = torch.from_numpy(model.decode(c.q.double().numpy(), model.widen(c.k.numpy()), model.widen(c.v.numpy()),
+                                        c.tables.numpy(), lens, c.scale))
+    assert 15 * 2.0 ** -16.1 < ref.min() and ref.max() < 15 * 2.0 ** -13.9
+    off = (out / ref - 1).abs()
+    assert off.max() <= 2.0 ** -17, float(off.max() * 2 ** 17)
