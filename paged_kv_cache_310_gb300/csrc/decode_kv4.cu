@@ -106,10 +106,8 @@ __device__ __forceinline__ int cost_of(int len, int max_len, bool whole) {
 // (g, t)'s B fragment of steps 2w and 2w + 1 for query head g of a block of eight columns.
 //
 // Lane t of a K row brings the D/4 consecutive values from t D/4 on: word w of its codes
-// gives steps 2w (values 0, 4 | 1, 5 of the word) and 2w + 1 (2, 6 | 3, 7).  q is scaled by
-// a power of two that puts its largest element in [2^14, 2^15): bf16 and f16 queries are
-// then exact in fp16 (elements 2^38 below the largest lose bits, f16's none), f32 ones in
-// two parts (hi, and lo with kSplit) to 2^-22.  undo[h] takes the power of two back.
+// gives steps 2w (values 0, 4 | 1, 5 of the word) and 2w + 1 (2, 6 | 3, 7).  q is scaled
+// (query_power) and held in fp16 parts hi and, with kSplit, lo.  undo[h] takes the scale back.
 // D/8 neighbouring threads work on one head; whole warps take part.
 template <int D, int NB, bool kSplit>
 __device__ __forceinline__ void stage_queries(const void* q, int dtype, size_t row, int heads, uint4* frag, float* undo) {
@@ -133,11 +131,8 @@ __device__ __forceinline__ void stage_queries(const void* q, int dtype, size_t r
     if (bad) amax = INFINITY;
 #pragma unroll
     for (int off = 1; off < kPer; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    // 2^up with up = 14 - exponent(amax), at most 126 (its inverse stays a normal number);
-    // a query with a NaN or an infinity keeps its scale and poisons its scores
-    int up = 141 - static_cast<int>(__float_as_uint(amax) >> 23);
-    up = amax == INFINITY || amax == 0.f ? 0 : (up > 126 ? 126 : up);
-    const float factor = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+    const int up = query_power(amax, amax == INFINITY);
+    const float factor = power_of_two(up);
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -149,7 +144,7 @@ __device__ __forceinline__ void stage_queries(const void* q, int dtype, size_t r
     uint4* to = frag + (((h / 8) * (kSplit ? 2 : 1)) * (D / 32) + w) * 32 + (h % 8) * 4 + t;
     *to = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     if (kSplit) to[(D / 32) * 32] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-    if (word == 0) undo[h] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+    if (word == 0) undo[h] = power_of_two(-up);
   }
 }
 

@@ -91,13 +91,22 @@ __device__ __forceinline__ void load8_any(const void* p, int dtype, size_t at, f
   }
 }
 
+// 4-bit K rows are multiplied with queries in fp16: a row of q is scaled by the power of two
+// that puts its largest element, amax, in [2^14, 2^15).  bf16 and f16 elements are then exact
+// (those 2^31 and 2^28 below the largest may lose bits, worth 2^-39 of it), f32 ones good to
+// 2^-22 in two parts.  The power is at most 126, so that its inverse stays a normal number; a
+// row of zeros, and one with a NaN or an infinity, which poisons its scores, is not scaled.
+__device__ __forceinline__ int query_power(float amax, bool bad) {
+  const int up = 141 - static_cast<int>(__float_as_uint(amax) >> 23);  // 14 less amax's exponent
+  return bad || amax == 0.f ? 0 : (up > 126 ? 126 : up);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // Query fragments against 4-bit K rows, one column (query head) per lane group g.
 //
 // Lane t of a K row brings the D/4 consecutive values from t D/4 on: word w of its codes
 // gives steps 2w (values 0, 4 | 1, 5 of the word) and 2w + 1 (2, 6 | 3, 7).  q is scaled
-// by a power of two that puts its largest element in [2^14, 2^15): bf16 and f16 queries
-// are then exact in fp16 (elements 2^38 below the largest lose bits, f16's none), f32 ones
-// in two parts (hi, and lo with kSplit) to 2^-22.  Returns what undoes the power of two.
+// (query_power) and held in fp16 parts hi and, with kSplit, lo.  Returns what undoes the scale.
 template <int D, bool kSplit>
 __device__ __forceinline__ float load_q_kv4(const void* q, int dtype, size_t row, bool valid, int t,
                                             uint32_t (&hi)[D / 16][2], uint32_t (&lo)[kSplit ? D / 16 : 1][2]) {
@@ -124,11 +133,8 @@ __device__ __forceinline__ float load_q_kv4(const void* q, int dtype, size_t row
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
     any_bad |= __shfl_xor_sync(0xffffffffu, any_bad, off);
   }
-  // 2^up with up = 14 - exponent(amax), at most 126 (its inverse stays a normal number);
-  // a query with a NaN or an infinity keeps its scale and poisons its scores
-  int up = 141 - static_cast<int>(__float_as_uint(amax) >> 23);
-  up = any_bad || amax == 0.f ? 0 : (up > 126 ? 126 : up);
-  const float factor = __uint_as_float(static_cast<uint32_t>(up + 127) << 23);
+  const int up = query_power(amax, any_bad);
+  const float factor = power_of_two(up);
 #pragma unroll
   for (int i = 0; i < D / 4; ++i) f[i] *= factor;
 #pragma unroll
@@ -141,7 +147,7 @@ __device__ __forceinline__ float load_q_kv4(const void* q, int dtype, size_t row
       if (kSplit) lo[2 * w + i / 2][i % 2] = pack_half2_rest(a, b, h);
     }
   }
-  return __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+  return power_of_two(-up);
 }
 
 }  // namespace pkv
