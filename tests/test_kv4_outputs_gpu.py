@@ -39,6 +39,7 @@ def check(c, dtype, out):
     low, high = (ref - tol).float().to(DT[dtype]), (ref + tol).float().to(DT[dtype])
     wrong = ~((low <= out) & (out <= high))
     assert not wrong.any(), (int(wrong.sum()), wrong.numel(), float((out.double() - ref).abs().max()), tol)
+    return tol
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
