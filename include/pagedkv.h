@@ -387,8 +387,10 @@ pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void
  * PKV_KV4 pool takes f32, f16 or bf16.  Query-head groups up to 16.  fp32 throughout
  * (products of 16-bit operands are exact).  A sequence longer than max_context_len sets
  * the device index flag and is skipped.  workspace: at least
- * paged_attention_weights_workspace_bytes(...) bytes (0 when max_context_len <= 512),
- * 256-byte aligned, one per call in flight.
+ * paged_attention_weights_workspace_bytes(...) bytes (0 when max_context_len <= 512; else a
+ * float per sequence, query head and token of max_context_len and a little more, of the whole
+ * batch up to 4 GiB, in turns of fewer sequences beyond), 256-byte aligned, one per call
+ * in flight.
  */
 size_t paged_attention_weights_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
                                                const pkv_cache_desc* cache);

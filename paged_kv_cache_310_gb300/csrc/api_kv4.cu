@@ -80,8 +80,16 @@ pkv_status check_table_width(int32_t max_blocks, int32_t tokens, int32_t block_s
   return PKV_OK;
 }
 
+// Scores that would take more go in turns of as many sequences as fit: of 65,535 sequences with
+// 64 heads, one of 128 Ki tokens, they would be 2.2 TB at once, whatever the others' lengths.
+// A turn costs its two kernels' latency, some 10 us (256 sequences of 200 to 400 tokens and one of
+// them 128 Ki, 64/8 heads, 4-bit pool: 212 us at once in 8.6 GB, 240 us in the three turns that
+// this limit makes, 302 us in nine of 1 GiB; uniform batches of 1.3 and 0.8 GB: no difference).
+constexpr size_t kScoresBytes = size_t{4} << 30;
+
 struct WeightsPlan {
   int part_tokens, max_parts;
+  int seqs;  // a turn's sequences
   int64_t ld;  // of a query head's row of scores: whole 128-byte lines
   size_t ml_bytes, workspace;
 };
@@ -103,11 +111,16 @@ pkv_status plan_weights(int32_t num_seqs, int32_t num_q_heads, int32_t max_len, 
   const int64_t per_cta = work / (6 * 152) + 1;
   plan->part_tokens = static_cast<int>(per_cta < 256 ? 256 : per_cta > 4096 ? 4096 : (per_cta + 127) / 128 * 128);
   plan->max_parts = max_len == 0 ? 1 : (max_len + plan->part_tokens - 1) / plan->part_tokens;
-  const size_t heads = static_cast<size_t>(num_seqs) * num_q_heads;
-  plan->ml_bytes = (heads * plan->max_parts * 2 * sizeof(float) + 255) / 256 * 256;
   plan->ld = (static_cast<int64_t>(max_len) + 31) / 32 * 32;
+  const size_t head_bytes = (plan->max_parts * 2 + plan->ld) * sizeof(float);
+  const size_t fit = kScoresBytes / (head_bytes * num_q_heads);  // sequences a turn has room for
+  const size_t most = fit < 1 ? 1 : fit, turns = (num_seqs + most - 1) / most;
+  plan->seqs = num_seqs == 0 ? 0 : static_cast<int>((num_seqs + turns - 1) / turns);
+  const size_t heads = static_cast<size_t>(plan->seqs) * num_q_heads;
+  plan->ml_bytes = (heads * plan->max_parts * 2 * sizeof(float) + 255) / 256 * 256;
   plan->workspace = num_seqs == 0 || max_len == 0 ? 0 : plan->ml_bytes + heads * plan->ld * sizeof(float);
   if (max_len <= kWeightsOne) {
+    plan->seqs = num_seqs;
     plan->part_tokens = max_len < 128 ? 128 : (max_len + 127) / 128 * 128;
     plan->max_parts = 1;
     plan->ld += 4;  // rows of scores in shared memory: eight tokens of four heads in different banks
@@ -279,13 +292,7 @@ pkv_status paged_attention_weights(const void* q, int32_t q_dtype, const void* k
   int* flag = nullptr;
   if (pkv_status st = device_flag(&flag)) return st;
   WeightsParams p{};
-  p.q = q;
   p.k_cache = k_cache;
-  p.block_tables = block_tables;
-  p.context_lens = context_lens;
-  p.tracked_lens = tracked_lens;
-  p.weights = weights;
-  p.weights_out = weights_out;
   if (plan.workspace > 0) {
     p.ws_ml = static_cast<float*>(workspace);
     p.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan.ml_bytes);
@@ -294,7 +301,6 @@ pkv_status paged_attention_weights(const void* q, int32_t q_dtype, const void* k
   p.width = weights_width;
   p.scores_ld = plan.ld;
   p.q_dtype = q_dtype;
-  p.num_seqs = num_seqs;
   p.num_q_heads = num_q_heads;
   p.num_kv_heads = cache->num_kv_heads;
   p.group = num_q_heads / cache->num_kv_heads;
@@ -306,8 +312,19 @@ pkv_status paged_attention_weights(const void* q, int32_t q_dtype, const void* k
   p.part_tokens = plan.part_tokens;
   p.max_parts = plan.max_parts;
   p.scale_log2 = scale * 1.4426950408889634f;
-  cudaError_t e = launch_weights(p, cache->dtype, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "attention weights launch");
+  for (int32_t s = 0; s < num_seqs; s += plan.seqs) {  // turns follow each other in the workspace
+    p.num_seqs = num_seqs - s < plan.seqs ? num_seqs - s : plan.seqs;
+    p.q = static_cast<const char*>(q) + static_cast<size_t>(s) * num_q_heads * cache->head_dim * elem_bytes(q_dtype);
+    p.block_tables = block_tables + static_cast<size_t>(s) * max_blocks_per_seq;
+    p.context_lens = context_lens + s;
+    p.tracked_lens = tracked_lens ? tracked_lens + s : nullptr;
+    const size_t row = static_cast<size_t>(s) * cache->num_kv_heads * weights_width;
+    p.weights = weights + row;
+    p.weights_out = weights_out + row;
+    const cudaError_t e = launch_weights(p, cache->dtype, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "attention weights launch");
+  }
+  return PKV_OK;
 }
 
 pkv_status paged_kv_evict(const float* weights, float* weights_out, int64_t weights_width, const int32_t* block_tables,

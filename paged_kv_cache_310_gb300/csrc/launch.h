@@ -162,7 +162,7 @@ int kv4_decode_ctas(int head_dim, int group, int q_dtype, int64_t max_units, int
 cudaError_t launch_decode_kv4(const Kv4DecodeParams& p, cudaStream_t stream);
 
 // ---- attention weights and eviction
-struct WeightsParams {
+struct WeightsParams {  // of one turn's sequences (all of the batch, or as many as the workspace has scores for)
   const void* q;
   const void* k_cache;
   const int32_t* block_tables;

@@ -88,3 +88,31 @@ def test_repeats_do_not_change_a_bit():
         outs = [c.run(tracked=[0, 0]) for _ in range(4)]
         torch.cuda.synchronize()
         assert all(torch.equal(outs[0].nan_to_num(5.0), o.nan_to_num(5.0)) for o in outs[1:])
+
+
+class Wide(Step):
+    """A step under a bound on the lengths far above them, with accumulators as wide."""
+
+    def run(self, tracked=None, in_place=False, *, bound):
+        q, k, tables, lens, before = (t.cuda() for t in (self.q, self.k, self.tables,
+                                                         torch.tensor(self.lens, dtype=torch.int32), self.before))
+        w = torch.full((*before.shape[:2], bound), 5.0, device="cuda")
+        w[:, :, :before.shape[2]] = before
+        out = w if in_place else torch.full_like(w, 7.0)
+        t = None if tracked is None else torch.tensor(tracked, dtype=torch.int32).cuda()
+        tables = torch.nn.functional.pad(tables, (0, -(-bound // self.k.shape[2]) - tables.shape[1]), value=-1)
+        pkv.paged_attention_weights(q, k, tables, lens, self.scale, w, weights_out=out, tracked_lens=t, max_context_len=bound)
+        assert (out[:, :, before.shape[2]:] == (5.0 if in_place else 7.0)).all()
+        return out[:, :, :before.shape[2]].contiguous()
+
+
+@pytest.mark.parametrize("pool,q_dtype", [("kv4", "f16"), ("bf16", None)])
+def test_batches_in_turns(pool, q_dtype):
+    # 37 sequences of 64 heads under a bound of 524,289 tokens: 5 GB of scores, so two turns
+    bound = 524_289
+    lens = [(41 * s) % 700 + (5000 if s in (3, 19) else 0) for s in range(37)]
+    c = Wide(311_750, lens, 64, 4, 64, 64, pool, q_dtype)
+    one = pkv.paged_attention_weights_workspace_bytes(1, 64, bound, c.k)
+    assert one < pkv.paged_attention_weights_workspace_bytes(37, 64, bound, c.k) < 30 * one
+    c.check(bound=bound)
+    c.check(tracked=[max(0, n - 1) for n in lens], in_place=True, bound=bound)
