@@ -386,7 +386,7 @@ pkv_status paged_attention_decode_kv4(const void* q, int32_t q_dtype, const void
  * q: device [num_seqs][num_q_heads][head_dim] of q_dtype, which is the cache's dtype; a
  * PKV_KV4 pool takes f32, f16 or bf16.  Query-head groups up to 16.  fp32 throughout
  * (products of 16-bit operands are exact).  A sequence longer than max_context_len sets
- * the device index flag and is skipped.  workspace: at least
+ * the device index flag and is skipped (max_context_len 0: nothing is looked at).  workspace: at least
  * paged_attention_weights_workspace_bytes(...) bytes (0 when max_context_len <= 512; else a
  * float per sequence, query head and token of max_context_len and a little more, of the whole
  * batch up to 4 GiB, in turns of fewer sequences beyond), 256-byte aligned, one per call
@@ -419,7 +419,8 @@ pkv_status paged_attention_weights(const void* q, int32_t q_dtype, const void* k
  * [num_seqs][num_kv_heads][max_keep]; keep_lens: device int32 [num_seqs], k <= max_keep;
  * new_tables: device int32 [num_seqs][max_new_blocks] of blocks that no listed sequence
  * reads or shares (pkv_bm_compact gives them).  A sequence whose lengths break these bounds
- * sets the device index flag and is skipped, as are rows with a block id out of range.
+ * sets the device index flag and is skipped, as are rows with a block id out of range
+ * (max_context_len 0: nothing is looked at).
  */
 pkv_status paged_kv_evict(const float* weights, float* weights_out, int64_t weights_width, const int32_t* block_tables,
                           int32_t max_blocks_per_seq, const int32_t* context_lens, const int32_t* keep_lens,

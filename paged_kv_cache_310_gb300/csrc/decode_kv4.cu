@@ -39,9 +39,10 @@
 // order.  Waits are cp.async.wait_group only.
 //
 // Measured (128 sequences of 512 to 4,096 tokens, 64/8 heads, bf16): 88 us a call, 0.64 of
-// copy bandwidth (80 us with one fp16 part of the weights).  About 350 instructions per 16
-// tokens, 216 of them widening; the integer and fp16 pipes are each busy 45 % of the time, the
-// tensor pipe 22 %, HBM 70 %.
+// copy bandwidth (80 us with one fp16 part of the weights), 9 of them the join.  About 365
+// instructions per 16 tokens, 216 of them widening.  No one unit is full: while the first kernel
+// runs, 60 % of the issue slots are taken, the FMA pipe (fp16 and fp32) is busy 48 % of the time,
+// the integer pipe 41 %, the tensor pipe 31 %, HBM 58 %; a warp mostly waits for a pipe or its turn.
 #include <type_traits>
 
 #include "kv4.cuh"

@@ -13,14 +13,15 @@
 // shared memory, it adds the weights up itself, and there is no second kernel or workspace
 // (one sequence of 512 tokens, 64/8 heads, 4-bit: 5.6 us on the GPU in place of 7.7; at 1,000
 // tokens a second kernel is ahead: 64 sequences, 32/8 heads, bf16, 25 us against 28).
-// Floor: HBM: K's row (2 D bytes in 16 bits, 5 D / 8 in four), 8 bytes of accumulator; the
-// scores' 8 G bytes mostly stay in L2 between the kernels (K is read with an evict-first
-// policy for that).
+// Floor: HBM: K's row (2 D bytes in 16 bits, 5 D / 8 in four), 8 bytes of accumulator.  The
+// scores' 8 G bytes more stay in L2 between the kernels while a batch's are well below its
+// 129 MB (K is read with an evict-first policy for that); a larger batch's go through HBM.
 //
 // Measured: 64 sequences of 128 to 2,048 tokens, 32/8 heads, bf16: 28.5 us a call, 0.76 of
 // copy bandwidth (the rest: the second kernel's launch and latency).  8 of 20,000 to 32,768,
 // 64/8 heads, 4-bit: 46.4 us, of which scores_kernel 36 at 4.0 TB/s, bound by instructions
-// (220 per 16 tokens and eight heads, 104 of them widening), and weights_kernel 10.
+// (220 per 16 tokens and eight heads, 104 of them widening), and weights_kernel 10; 32 of them,
+// whose scores (216 MB) pass L2: 190 us; f32 queries: 53.  f32 pools, the first batch: 56 us, 0.79.
 //
 // 16-bit pools go to m16n8k16 MMAs as they are, 4-bit ones are widened in registers
 // (kv4.cuh), f32 ones are multiplied on CUDA cores in fp32.
