@@ -294,6 +294,89 @@ pkv_status paged_kv_gather(const void* k_cache, const void* v_cache, const int32
                            const pkv_cache_desc* cache, void* stream);
 
 /* ----------------------------------------------------------------------------------
+ * Position rotation and norms of new tokens' queries and keys.  The pages have no
+ * counterpart: what a model with rotary positions does to q and k between its projection
+ * and the cache.
+ * ---------------------------------------------------------------------------------- */
+
+/* Which dimensions of a head turn together, i < rotary_dim / 2. */
+typedef enum {
+  PKV_ROTARY_HALF = 0,        /* i and i + rotary_dim / 2 */
+  PKV_ROTARY_INTERLEAVED = 1  /* 2i and 2i + 1 */
+} pkv_rotary_layout;
+
+typedef struct {
+  const double* inv_freq;  /* device [rotary_dim / 2]: radians per position */
+  int32_t rotary_dim;      /* the first rotary_dim dimensions of a head turn: a multiple of 16, 0 to head_dim */
+  int32_t layout;          /* pkv_rotary_layout */
+  float factor;            /* of cosines and sines (1 unless a scaling rule gives another) */
+  float eps;               /* of the norms; read where a weight is given */
+  const void* q_weight;    /* device [head_dim] in the tensors' dtype, 16-byte aligned: norm of each query head */
+  const void* k_weight;    /* the same for keys; NULL: no norm */
+} pkv_rotary;
+
+/* Frequencies of rotations scaled for longer contexts than a model was trained on. */
+typedef enum {
+  PKV_ROTARY_UNSCALED = 0,
+  PKV_ROTARY_LINEAR = 1,  /* positions interpolated: every frequency divided by `factor` */
+  PKV_ROTARY_BASE = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)): the lowest frequency divided by `factor` */
+  PKV_ROTARY_PARTS = 3    /* by turns within original_len: fast_turns or more are kept, slow_turns or fewer divided by
+                             `factor`, linear in between; cosines and sines times 0.1 ln(factor) + 1 */
+} pkv_rotary_rule;
+
+typedef struct {
+  int32_t rule;                   /* pkv_rotary_rule */
+  double factor;                  /* >= 1 */
+  double original_len;            /* PKV_ROTARY_PARTS only, as are the next two */
+  double fast_turns, slow_turns;  /* customarily 32 and 1 */
+} pkv_rotary_scaling;
+
+/*
+ * paged_rotary_frequencies -- host only: inv_freq[i] = base^(-2 i / rotary_dim), i <
+ * rotary_dim / 2, scaled by the rule (NULL: unscaled); *factor is what pkv_rotary.factor
+ * then wants.  inv_freq and factor are host memory.
+ */
+pkv_status paged_rotary_frequencies(double* inv_freq, int32_t rotary_dim, double base,
+                                    const pkv_rotary_scaling* scaling, float* factor);
+
+/*
+ * paged_qk_rotary -- norm and rotate queries and keys by their positions.  For every token
+ * t with positions[t] >= 0 and every head of q and k, with x its head_dim values:
+ *   y = x * weight / sqrt(mean(x^2) + eps)  (y = x where the weight is NULL);
+ *   each pair (y_a, y_b) of the layout becomes (y_a c - y_b s, y_b c + y_a s), with
+ *   c = factor cos(positions[t] * inv_freq[i]), s = factor sin(positions[t] * inv_freq[i]);
+ * the other dimensions stay y.  fp32 throughout, the angle without its whole turns exact to
+ * 2^-30 turns for positions up to 2^20 and frequencies up to 1; one rounding at the end (RNE).
+ * Negative positions are padding: nothing of the token is written.
+ *
+ * q, k, q_out, k_out: device, dtype f32, f16 or bf16; a token's heads lie one after the
+ * other ([num_heads][head_dim]), tokens are *_stride elements apart (at least the token's
+ * own, a multiple of 16 bytes): parts of a fused projection's rows are taken as they are.
+ * q_out may be q and k_out may be k (same strides); other overlaps are refused.
+ * num_q_heads or num_kv_heads 0: that tensor is not looked at.
+ * For 4-bit pools: rotate k with this call, then paged_kv4_append.
+ */
+pkv_status paged_qk_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const int32_t* positions,
+                           int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
+                           const pkv_rotary* rotary, void* q_out, int64_t q_out_stride, void* k_out,
+                           int64_t k_out_stride, void* stream);
+
+/*
+ * paged_kv_append_rotary -- paged_qk_rotary and paged_kv_append in one pass: q goes, normed
+ * and rotated, to q_out, k normed and rotated into its slot of k_cache, v as it is into its
+ * slot of v_cache (bit-exact).  Arguments as in those calls; q, k, v and q_out have the
+ * cache's dtype (f32, f16 or bf16) and heads of its head_dim, k and v its KV heads.
+ * Tokens with a negative slot or a negative position are padding: nothing of them is
+ * written, to q_out neither.  A slot >= num_blocks * block_size sets the device index flag
+ * and its token is skipped as well.  Slots must be distinct (duplicates race).
+ */
+pkv_status paged_kv_append_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                  int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,
+                                  int32_t num_tokens, int32_t num_q_heads, const pkv_rotary* rotary, void* q_out,
+                                  int64_t q_out_stride, void* k_cache, void* v_cache, const pkv_cache_desc* cache,
+                                  void* stream);
+
+/* ----------------------------------------------------------------------------------
  * 4-bit caches.  The pages have no counterpart: a smaller form of the same cache, for more
  * context in the same memory.
  *

@@ -20,6 +20,12 @@ and, to shorten sequences by what attention uses least:
 * :func:`paged_attention_weights` -- a decode step's attention weights, added per token
 * :func:`paged_kv_evict`         -- the heaviest and the most recent rows kept, in fresh blocks
 
+and, for models with rotary positions:
+
+* :func:`paged_qk_rotary`        -- queries and keys normed per head and rotated by position
+* :func:`paged_kv_append_rotary` -- the same on the way into the cache (and V as it is)
+* :func:`rotary_frequencies`     -- frequencies, also of rotations scaled for long contexts
+
 If the library has not been built the import still succeeds, but every call raises:
 there is no CPU fallback.
 """
@@ -41,6 +47,7 @@ __all__ = [
     "PATH_AUTO", "PATH_CUDA_CORE", "PATH_TENSOR_CORE",
     "paged_kv4_append", "paged_kv4_expand", "paged_attention_decode_kv4", "paged_attention_decode_kv4_workspace_bytes",
     "paged_attention_weights", "paged_attention_weights_workspace_bytes", "paged_kv_evict",
+    "paged_qk_rotary", "paged_kv_append_rotary", "rotary_frequencies",
     "PreparedCall", "prepare_kv_append", "prepare_block_copy", "prepare_attention_decode", "set_wait_limit",
 ]
 
@@ -76,6 +83,17 @@ class DecodePlan(ctypes.Structure):
     _fields_ = [("path", ctypes.c_int32), ("partition_tokens", ctypes.c_int32),
                 ("max_partitions", ctypes.c_int32), ("kernel_launches", ctypes.c_int32),
                 ("workspace_bytes", ctypes.c_size_t), ("kv_heads_per_item", ctypes.c_int32)]
+
+
+class Rotary(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("factor", ctypes.c_float), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p)]
+
+
+class RotaryScaling(ctypes.Structure):
+    _fields_ = [("rule", ctypes.c_int32), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("fast_turns", ctypes.c_double), ("slow_turns", ctypes.c_double)]
 
 
 _lock = threading.Lock()
@@ -118,6 +136,11 @@ def library():
                                         desc_p, vp],
             "paged_kv_evict": [vp, vp, i64, vp, i32, vp, vp, i32, vp, i32, i32, i32, i32, vp, vp, vp, desc_p, vp],
             "paged_kv4_expand": [vp, i32, vp, vp, desc_p, vp, vp, desc_p, vp],
+            "paged_rotary_frequencies": [vp, i32, ctypes.c_double, ctypes.POINTER(RotaryScaling),
+                                         ctypes.POINTER(ctypes.c_float)],
+            "paged_qk_rotary": [vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, ctypes.POINTER(Rotary), vp, i64, vp, i64, vp],
+            "paged_kv_append_rotary": [vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, ctypes.POINTER(Rotary), vp, i64, vp, vp,
+                                       desc_p, vp],
             "paged_kv_gather": [vp, vp, vp, i32, vp, i32, i32, vp, vp, desc_p, vp],
             "paged_block_swap_out": [vp, i32, vp, vp, vp, vp, desc_p, vp],
             "paged_attention_prefill": [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, i32,
@@ -674,6 +697,104 @@ def paged_kv_evict(weights, block_tables, context_lens, keep_lens, new_tables, k
           block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), keep_lens.data_ptr(), recent,
           new_tables.data_ptr(), new_tables.shape[1], S, max_context_len, kept.shape[2], kept.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), desc_ref)
+
+
+# ---- rotary positions
+
+_ROTARY_RULES = {None: 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None, factor: float = 1.0,
+                       original_len: float = 0.0, fast_turns: float = 32.0, slow_turns: float = 1.0):
+    """(inv_freq, factor) of a rotation: float64 [rotary_dim / 2] on the CPU, inv_freq[i] =
+    base^(-2 i / rotary_dim), and the factor of cosines and sines.  scaling for contexts
+    `factor` times as long: "linear" divides every frequency, "base" raises the base so that
+    the lowest one is divided, "parts" divides those that make up to slow_turns within
+    original_len, keeps those with fast_turns or more, and blends in between."""
+    if scaling not in _ROTARY_RULES:
+        raise PagedKVError(1, f"scaling {scaling!r}")
+    out = torch.empty(max(0, int(rotary_dim)) // 2, dtype=torch.float64)
+    rule = RotaryScaling(_ROTARY_RULES[scaling], factor, original_len, fast_turns, slow_turns)
+    f = ctypes.c_float()
+    _check(library().paged_rotary_frequencies(out.data_ptr() or 8, rotary_dim, base, ctypes.byref(rule), ctypes.byref(f)))
+    return out, f.value
+
+
+def _token_rows(t, what, dtype, device, tokens, head_dim):
+    """(address, token stride, heads) of a [T, H, head_dim] tensor whose tokens may lie apart."""
+    if t.dim() != 3 or t.dtype != dtype or t.get_device() != device or t.shape[0] != tokens or t.shape[2] != head_dim:
+        raise PagedKVError(1, f"{what} must be [T, heads, {head_dim}] of one dtype on one CUDA device")
+    heads, row = t.shape[1], t.shape[1] * head_dim
+    stride = t.stride()
+    if stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
+        raise PagedKVError(1, f"{what}: the heads of a token must lie one after the other")
+    return t.data_ptr(), stride[0] if tokens > 1 else row, heads
+
+
+def _rotary(inv_freq, interleaved, factor, q_weight, k_weight, eps, dtype, device, head_dim):
+    """The C struct of a rotation."""
+    pairs = 0 if inv_freq is None else inv_freq.numel()
+    if pairs and (inv_freq.dtype != torch.float64 or inv_freq.get_device() != device or not inv_freq.is_contiguous()):
+        raise PagedKVError(1, "inv_freq must be a contiguous float64 tensor on the call's device")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype != dtype or w.get_device() != device or not w.is_contiguous() or w.numel() != head_dim):
+            raise PagedKVError(1, "norm weights must be contiguous, [head_dim], of the tensors' dtype and device")
+    return Rotary(inv_freq.data_ptr() if pairs else 0, 2 * pairs, 1 if interleaved else 0, factor, eps,
+                  0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr())
+
+
+def paged_qk_rotary(q, k, positions, q_out, k_out, inv_freq, *, interleaved: bool = False, factor: float = 1.0,
+                    q_weight: torch.Tensor | None = None, k_weight: torch.Tensor | None = None,
+                    eps: float = 1e-6) -> None:
+    """q_out, k_out <- q [T, Hq, D] and k [T, Hkv, D] normed per head (where a weight [D] is
+    given) and rotated by positions (int32 [T]; negative: padding, left as it is).
+
+    inv_freq (float64 [R / 2], device, or None): the first R = 2 * numel dimensions of a head
+    turn, R a multiple of 16: dimension i with i + R / 2, or 2i with 2i + 1 if interleaved.
+    factor multiplies cosines and sines.  Tokens may lie apart (views of a fused
+    projection); q_out may be q and k_out may be k.
+    """
+    device, dtype, tokens = positions.get_device(), q.dtype, positions.numel()
+    if device < 0 or not positions.is_contiguous() or positions.dtype != torch.int32:
+        raise PagedKVError(1, "positions must be a contiguous int32 CUDA tensor")
+    d = q.shape[-1] if q.dim() else 0
+    qp, qs, hq = _token_rows(q, "q", dtype, device, tokens, d)
+    kp, ks, hkv = _token_rows(k, "k", dtype, device, tokens, d)
+    qop, qos, hqo = _token_rows(q_out, "q_out", dtype, device, tokens, d)
+    kop, kos, hko = _token_rows(k_out, "k_out", dtype, device, tokens, d)
+    if (hqo, hko) != (hq, hkv):
+        raise PagedKVError(1, "q_out and k_out must have the shapes of q and k")
+    rotary = _rotary(inv_freq, interleaved, factor, q_weight, k_weight, eps, dtype, device, d)
+    _call(library().paged_qk_rotary, device, qp, qs, kp, ks, positions.data_ptr(), tokens, hq, hkv, d,
+          _dtype_code(q, "q"), ctypes.byref(rotary), qop, qos, kop, kos)
+
+
+def paged_kv_append_rotary(q, k, v, positions, slot_mapping, k_cache, v_cache, q_out, inv_freq, *,
+                           interleaved: bool = False, factor: float = 1.0, q_weight: torch.Tensor | None = None,
+                           k_weight: torch.Tensor | None = None, eps: float = 1e-6) -> torch.Tensor:
+    """paged_qk_rotary and paged_kv_append in one pass: q normed and rotated -> q_out, k
+    normed and rotated and v as it is -> the cache rows given by slot_mapping (int64 [T]).
+    Tokens with a negative slot or position are padding.  q, k, v, q_out have the pools'
+    dtype (f32, f16 or bf16); the other arguments are those of paged_qk_rotary."""
+    device, dtype, tokens = _one_device(k_cache, v_cache, positions, slot_mapping), k_cache.dtype, positions.numel()
+    desc, desc_ref = _desc_of(k_cache.shape, dtype)
+    if desc.dtype == KV4:
+        raise PagedKVError(2, "4-bit pools: paged_qk_rotary, then paged_kv4_append")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != dtype:
+        raise PagedKVError(1, "the caches must be of one shape and dtype")
+    if positions.dtype != torch.int32 or slot_mapping.dtype != torch.int64 or slot_mapping.numel() != tokens:
+        raise PagedKVError(1, "positions must be int32 [T] and slot_mapping int64 [T]")
+    d = desc.head_dim
+    qp, qs, hq = _token_rows(q, "q", dtype, device, tokens, d)
+    kp, ks, hk = _token_rows(k, "k", dtype, device, tokens, d)
+    vp, vs, hv = _token_rows(v, "v", dtype, device, tokens, d)
+    qop, qos, hqo = _token_rows(q_out, "q_out", dtype, device, tokens, d)
+    if hqo != hq or hk != desc.num_kv_heads or hv != hk:
+        raise PagedKVError(1, "q_out must have q's shape, k and v the caches' KV heads")
+    rotary = _rotary(inv_freq, interleaved, factor, q_weight, k_weight, eps, dtype, device, d)
+    _call(library().paged_kv_append_rotary, device, qp, qs, kp, ks, vp, vs, positions.data_ptr(), slot_mapping.data_ptr(),
+          tokens, hq, ctypes.byref(rotary), qop, qos, k_cache.data_ptr(), v_cache.data_ptr(), desc_ref)
+    return q_out
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:

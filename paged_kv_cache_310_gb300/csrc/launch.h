@@ -95,6 +95,29 @@ cudaError_t launch_gather(const void* k_cache, const void* v_cache, const int32_
                           int32_t num_kv_heads, int32_t block_size, int32_t row_bytes,
                           int32_t num_blocks, int* err, cudaStream_t stream);
 
+// ---- norms and position rotation of new tokens' queries and keys
+struct RotaryParams {
+  const void* q;
+  const void* k;
+  const void* v;               // into pools only
+  const int32_t* positions;
+  const int64_t* slots;        // NULL: keys go to k_out, there are no values
+  const double* inv_freq;      // [rotary_dim / 2]
+  const void* q_weight;        // [head_dim] or NULL
+  const void* k_weight;
+  void* q_out;
+  void* k_out;
+  void* k_cache;
+  void* v_cache;
+  int* err;
+  int64_t q_stride, k_stride, v_stride, q_out_stride, k_out_stride;  // elements from a token to the next
+  int64_t num_slots;
+  int32_t num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, rotary_dim, interleaved;
+  float factor, eps;
+  int32_t tokens_per_cta;      // set by the launcher
+};
+cudaError_t launch_rotary(const RotaryParams& p, int dtype, cudaStream_t stream);
+
 // ---- 4-bit caches (PKV_KV4 pools)
 
 // The bit patterns that widening 4-bit codes uses.  Kernels get them as an argument: as
