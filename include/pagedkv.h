@@ -377,6 +377,50 @@ pkv_status paged_kv_append_rotary(const void* q, int64_t q_stride, const void* k
                                   void* stream);
 
 /* ----------------------------------------------------------------------------------
+ * Sliding windows.  The pages have no counterpart: layers whose tokens attend to the last
+ * `window` tokens, their own among them, and to the first `sinks` of the sequence.
+ *
+ * A token at position p attends to the positions j <= p with j > p - window or j < sinks;
+ * window >= 1, sinks >= 0.  A window or sinks past the sequence's start or end change nothing
+ * else: window >= context_lens[s] is attention over all tokens.  Table entries of blocks
+ * that hold no token attended to are never read, so a server can release those blocks; what
+ * lies in rows that no token of a call attends to (a NaN, too) does not matter.
+ * ---------------------------------------------------------------------------------- */
+
+/*
+ * paged_attention_decode_window -- paged_attention_decode over a window.  One new token per
+ * sequence, at position context_lens[s] - 1; the other arguments, types, groups, errors, the
+ * workspace's ownership and the early start as there.  16-bit caches run on tensor cores,
+ * groups up to 16; f32 caches on CUDA cores, groups up to 8, fp32 throughout.
+ * max_context_len: host upper bound on context_lens (a longer sequence sets the device
+ * index flag, and its rows of out are left as they are).  Cost goes by the tokens attended
+ * to, not by context_lens.
+ */
+size_t paged_attention_decode_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
+                                                     int32_t window, int32_t sinks, const pkv_cache_desc* cache);
+pkv_status paged_attention_decode_window(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                         const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t max_context_len, int32_t window, int32_t sinks, float scale, void* out,
+                                         int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                         const pkv_cache_desc* cache, void* stream);
+
+/*
+ * paged_attention_prefill_window -- paged_attention_prefill over windows, each new token's
+ * its own (arguments, types, limits, errors and workspace as there:
+ * paged_attention_prefill_workspace_bytes).  A NaN or an infinity in a V row that one of a
+ * call's new tokens attends to may reach the outputs of the sequence's other new tokens
+ * (they share its products); in a K row it reaches those that attend to it.
+ */
+pkv_status paged_attention_prefill_window(const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t* context_lens, const int32_t* query_start, int32_t num_seqs,
+                                          int32_t num_q_heads, int32_t num_query_tokens, int32_t max_context_len,
+                                          int32_t window, int32_t sinks, float scale, void* out, int32_t out_dtype,
+                                          void* workspace, size_t workspace_bytes, const pkv_cache_desc* cache,
+                                          void* stream);
+
+/* ----------------------------------------------------------------------------------
  * 4-bit caches.  The pages have no counterpart: a smaller form of the same cache, for more
  * context in the same memory.
  *

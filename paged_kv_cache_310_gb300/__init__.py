@@ -20,11 +20,13 @@ and, to shorten sequences by what attention uses least:
 * :func:`paged_attention_weights` -- a decode step's attention weights, added per token
 * :func:`paged_kv_evict`         -- the heaviest and the most recent rows kept, in fresh blocks
 
-and, for models with rotary positions:
+and, for models with rotary positions and sliding windows:
 
 * :func:`paged_qk_rotary`        -- queries and keys normed per head and rotated by position
 * :func:`paged_kv_append_rotary` -- the same on the way into the cache (and V as it is)
 * :func:`rotary_frequencies`     -- frequencies, also of rotations scaled for long contexts
+* :func:`paged_attention_decode_window`, :func:`paged_attention_prefill_window` -- attention over
+  the last tokens and the first few
 
 If the library has not been built the import still succeeds, but every call raises:
 there is no CPU fallback.
@@ -48,6 +50,7 @@ __all__ = [
     "paged_kv4_append", "paged_kv4_expand", "paged_attention_decode_kv4", "paged_attention_decode_kv4_workspace_bytes",
     "paged_attention_weights", "paged_attention_weights_workspace_bytes", "paged_kv_evict",
     "paged_qk_rotary", "paged_kv_append_rotary", "rotary_frequencies",
+    "paged_attention_decode_window", "paged_attention_decode_window_workspace_bytes", "paged_attention_prefill_window",
     "PreparedCall", "prepare_kv_append", "prepare_block_copy", "prepare_attention_decode", "set_wait_limit",
 ]
 
@@ -141,6 +144,11 @@ def library():
             "paged_qk_rotary": [vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, ctypes.POINTER(Rotary), vp, i64, vp, i64, vp],
             "paged_kv_append_rotary": [vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, ctypes.POINTER(Rotary), vp, i64, vp, vp,
                                        desc_p, vp],
+            "paged_attention_decode_window_workspace_bytes": [i32, i32, i32, i32, i32, desc_p],
+            "paged_attention_decode_window": [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, ctypes.c_float, vp, i32,
+                                              vp, sz, desc_p, vp],
+            "paged_attention_prefill_window": [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, ctypes.c_float,
+                                               vp, i32, vp, sz, desc_p, vp],
             "paged_kv_gather": [vp, vp, vp, i32, vp, i32, i32, vp, vp, desc_p, vp],
             "paged_block_swap_out": [vp, i32, vp, vp, vp, vp, desc_p, vp],
             "paged_attention_prefill": [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, i32,
@@ -163,6 +171,7 @@ def library():
         lib.paged_attention_workspace_bytes.restype = sz
         lib.paged_attention_no_alloc_limit.restype = sz
         lib.paged_attention_prefill_workspace_bytes.restype = sz
+        lib.paged_attention_decode_window_workspace_bytes.restype = sz
         lib.paged_attention_decode_kv4_workspace_bytes.restype = sz
         lib.paged_attention_weights_workspace_bytes.restype = sz
         lib.paged_kv_last_error.restype = ctypes.c_char_p
@@ -795,6 +804,83 @@ def paged_kv_append_rotary(q, k, v, positions, slot_mapping, k_cache, v_cache, q
     _call(library().paged_kv_append_rotary, device, qp, qs, kp, ks, vp, vs, positions.data_ptr(), slot_mapping.data_ptr(),
           tokens, hq, ctypes.byref(rotary), qop, qos, k_cache.data_ptr(), v_cache.data_ptr(), desc_ref)
     return q_out
+
+
+# ---- sliding windows
+
+def _window_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace, *more):
+    """Checks that both windowed calls make; (device, descriptor reference, sequences)."""
+    device = _one_device(q, k_cache, v_cache, block_tables, context_lens, out, workspace, *more)
+    desc, desc_ref = _desc_of(k_cache.shape, k_cache.dtype)
+    if desc.dtype == KV4:
+        raise PagedKVError(2, "windows over 4-bit pools")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise PagedKVError(1, "block_tables and context_lens must be int32")
+    if q.dim() != 3 or out.shape != q.shape or q.dtype != k_cache.dtype or q.shape[2] != desc.head_dim \
+            or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise PagedKVError(1, "shape/dtype mismatch between q, out and the caches")
+    S = context_lens.numel()
+    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+        raise PagedKVError(1, "block_tables must be [S, max_blocks]")
+    return device, desc_ref, S
+
+
+def paged_attention_decode_window_workspace_bytes(num_seqs, num_q_heads, max_context_len, window, sinks, k_cache) -> int:
+    return int(library().paged_attention_decode_window_workspace_bytes(
+        num_seqs, num_q_heads, max_context_len, window, sinks, _desc_of(k_cache.shape, k_cache.dtype)[1]))
+
+
+def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, out, *, window: int,
+                                  sinks: int = 0, max_context_len: int | None = None,
+                                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """out[s, h] = softmax(scale * q[s, h] . K_j) V_j over the last `window` of the
+    context_lens[s] tokens of s and its first `sinks`.
+
+    Tensors as in paged_attention_decode; table entries of blocks that hold no such token are
+    not read (-1 will do).  max_context_len: host upper bound on context_lens (computed with a
+    device sync when omitted).  workspace: uint8 device buffer of
+    paged_attention_decode_window_workspace_bytes, allocated for the call when omitted.
+    """
+    device, desc_ref, S = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    if q.shape[0] != S:
+        raise PagedKVError(1, "context_lens must be [S]")
+    out_code, Hq = _dtype_code(out, "out"), q.shape[1]
+    if max_context_len is None:
+        max_context_len = int(context_lens.max()) if S else 0
+    lib = library()
+    need = 0
+    if workspace is None:
+        need = lib.paged_attention_decode_window_workspace_bytes(S, Hq, max_context_len, window, sinks, desc_ref)
+    ws, ws_bytes, workspace = _scratch(workspace, need, device)
+    _call(lib.paged_attention_decode_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, Hq, max_context_len, window, sinks,
+          float(scale), out.data_ptr(), out_code, ws, ws_bytes, desc_ref)
+    return out
+
+
+def paged_attention_prefill_window(q, k_cache, v_cache, block_tables, context_lens, query_start, scale, out, *,
+                                   window: int, sinks: int = 0, max_context_len: int | None = None,
+                                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """paged_attention_prefill with a window: the new token at position p attends to the
+    positions j <= p with j > p - window or j < sinks.  Tensors as there; table entries of blocks
+    that hold no token attended to are not read.  workspace: uint8 device buffer, allocated for
+    the call when omitted."""
+    device, desc_ref, S = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace, query_start)
+    if query_start.dtype != torch.int32 or query_start.numel() != S + 1:
+        raise PagedKVError(1, "query_start must be int32 [S+1]")
+    T, Hq, _ = q.shape
+    out_code = _dtype_code(out, "out")
+    if max_context_len is None:
+        max_context_len = int(context_lens.max()) if S else 0
+    lib = library()
+    need = 0
+    if workspace is None:
+        need = lib.paged_attention_prefill_workspace_bytes(S, Hq, T, desc_ref)
+    ws, ws_bytes, workspace = _scratch(workspace, need, device)
+    _call(lib.paged_attention_prefill_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), S, Hq, T,
+          max_context_len, window, sinks, float(scale), out.data_ptr(), out_code, ws, ws_bytes, desc_ref)
+    return out
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:

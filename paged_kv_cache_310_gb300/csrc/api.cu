@@ -1,5 +1,6 @@
 // api.cu -- the extern "C" entry points of libpagedkv.so (declared in
 // include/pagedkv.h): argument checks, launch configuration, the device error flag.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -353,16 +354,27 @@ size_t paged_attention_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
   return plan.workspace;
 }
 
-pkv_status paged_attention_decode(const void* q, const void* k_cache, const void* v_cache,
-                                  const int32_t* block_tables, int32_t max_blocks_per_seq,
-                                  const int32_t* context_lens, int32_t num_seqs,
-                                  int32_t num_q_heads, int32_t max_context_len, float scale,
-                                  void* out, int32_t out_dtype, void* workspace,
-                                  size_t workspace_bytes, const pkv_cache_desc* cache,
-                                  const pkv_decode_config* config, void* stream) {
-  DecodePlan plan;
-  if (pkv_status st = plan_decode(num_seqs, num_q_heads, max_context_len, cache, config, &plan))
-    return st;
+size_t paged_attention_prefill_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_query_tokens,
+                                               const pkv_cache_desc* cache) {
+  if (!cache || cache->num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads ||
+      num_seqs < 0 || num_query_tokens < 0)
+    return 0;
+  const int group = num_q_heads / cache->num_kv_heads;
+  if (group > 16) return 0;
+  return 256 + (prefill_max_items(num_seqs, num_query_tokens, cache->num_kv_heads, group) * 16 + 255) / 256 * 256;
+}
+
+}  // extern "C"
+
+namespace {
+
+// What paged_attention_decode and its windowed form share.  The plan is for the tokens that a
+// sequence's kernels run over; max_context_len bounds all that it has (window 0: the same).
+pkv_status decode(const DecodePlan& plan, int32_t window, int32_t sinks, const void* q, const void* k_cache,
+                  const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                  const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len, float scale,
+                  void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes, const pkv_cache_desc* cache,
+                  void* stream) {
   if (num_seqs == 0) return PKV_OK;
   if (!q || !k_cache || !v_cache || !context_lens || !out)
     return fail(PKV_ERR_INVALID_ARG, "NULL pointer argument");
@@ -418,6 +430,10 @@ pkv_status paged_attention_decode(const void* q, const void* k_cache, const void
   p.out_f32 = out_dtype == PKV_F32 ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;  // log2(e): softmax is evaluated with exp2
   p.wait_limit_ns = g_wait_limit_ns.load();
+  p.window = window > 0 && window > max_context_len ? std::max(max_context_len, 1) : window;
+  p.sinks = sinks < max_context_len ? sinks : max_context_len;
+  p.sink_blocks = (p.sinks - 1) / p.block_size + (p.sinks > 0);
+  p.max_len = max_context_len;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = plan.path == PKV_PATH_TENSOR_CORE ? launch_decode_tc(p, cache->dtype, s)
@@ -428,22 +444,31 @@ pkv_status paged_attention_decode(const void* q, const void* k_cache, const void
   return PKV_OK;
 }
 
-size_t paged_attention_prefill_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_query_tokens,
-                                               const pkv_cache_desc* cache) {
-  if (!cache || cache->num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads ||
-      num_seqs < 0 || num_query_tokens < 0)
-    return 0;
-  const int group = num_q_heads / cache->num_kv_heads;
-  if (group > 16) return 0;
-  return 256 + (prefill_max_items(num_seqs, num_query_tokens, cache->num_kv_heads, group) * 16 + 255) / 256 * 256;
+pkv_status check_window(int32_t window, int32_t sinks) {
+  if (window < 1) return fail(PKV_ERR_INVALID_ARG, "window %d < 1", window);
+  if (sinks < 0) return fail(PKV_ERR_INVALID_ARG, "sinks %d < 0", sinks);
+  return PKV_OK;
 }
 
-pkv_status paged_attention_prefill(const void* q, const void* k_cache, const void* v_cache,
-                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
-                                   const int32_t* context_lens, const int32_t* query_start, int32_t num_seqs,
-                                   int32_t num_q_heads, int32_t num_query_tokens, int32_t max_context_len,
-                                   float scale, void* out, int32_t out_dtype, void* workspace,
-                                   size_t workspace_bytes, const pkv_cache_desc* cache, void* stream) {
+// The windowed decode's plan: as for sequences of the tokens that its kernels run over at most,
+// those of the sinks' and the window's blocks.  16-bit caches on tensor cores, f32 on CUDA
+// cores: fp32 throughout, where the tf32 kernel's split operands lose 2^-21 of a score.
+pkv_status plan_window(int32_t window, int32_t sinks, int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
+                       const pkv_cache_desc* cache, DecodePlan* plan) {
+  if (pkv_status st = check_window(window, sinks)) return st;
+  if (pkv_status st = check_cache(cache)) return st;
+  const int64_t bs = cache->block_size, most = (sinks + bs - 1) / bs * bs + static_cast<int64_t>(window) + bs - 1;
+  const pkv_decode_config config = {cache->dtype == PKV_F32 ? PKV_PATH_CUDA_CORE : PKV_PATH_TENSOR_CORE, 0};
+  return plan_decode(num_seqs, num_q_heads, max_context_len < most ? max_context_len : static_cast<int32_t>(most), cache,
+                     &config, plan);
+}
+
+// What paged_attention_prefill and its windowed form (window > 0) share.
+pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                   const int32_t* query_start, int32_t num_seqs, int32_t num_q_heads, int32_t num_query_tokens,
+                   int32_t max_context_len, float scale, void* out, int32_t out_dtype, void* workspace,
+                   size_t workspace_bytes, const pkv_cache_desc* cache, void* stream) {
   if (pkv_status st = check_cache(cache)) return st;
   if (num_seqs < 0 || num_seqs > (1 << 20)) return fail(PKV_ERR_INVALID_ARG, "num_seqs %d", num_seqs);
   if (num_q_heads <= 0 || num_q_heads % cache->num_kv_heads)
@@ -499,8 +524,72 @@ pkv_status paged_attention_prefill(const void* q, const void* k_cache, const voi
   p.out_f32 = out_dtype == PKV_F32 ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = g_wait_limit_ns.load();
+  p.window = window > 0 && window > max_context_len ? std::max(max_context_len, 1) : window;
+  p.sinks = sinks < max_context_len ? sinks : max_context_len;
+  p.sink_blocks = (p.sinks - 1) / p.block_size + (p.sinks > 0);
   cudaError_t e = launch_prefill_tc(p, cache->dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "prefill launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status paged_attention_decode(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t* context_lens, int32_t num_seqs,
+                                  int32_t num_q_heads, int32_t max_context_len, float scale,
+                                  void* out, int32_t out_dtype, void* workspace,
+                                  size_t workspace_bytes, const pkv_cache_desc* cache,
+                                  const pkv_decode_config* config, void* stream) {
+  DecodePlan plan;
+  if (pkv_status st = plan_decode(num_seqs, num_q_heads, max_context_len, cache, config, &plan))
+    return st;
+  return decode(plan, 0, 0, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                max_context_len, scale, out, out_dtype, workspace, workspace_bytes, cache, stream);
+}
+
+pkv_status paged_attention_prefill(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, const int32_t* query_start, int32_t num_seqs,
+                                   int32_t num_q_heads, int32_t num_query_tokens, int32_t max_context_len,
+                                   float scale, void* out, int32_t out_dtype, void* workspace,
+                                   size_t workspace_bytes, const pkv_cache_desc* cache, void* stream) {
+  return prefill(0, 0, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, num_seqs,
+                 num_q_heads, num_query_tokens, max_context_len, scale, out, out_dtype, workspace, workspace_bytes, cache,
+                 stream);
+}
+
+size_t paged_attention_decode_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
+                                                     int32_t window, int32_t sinks, const pkv_cache_desc* cache) {
+  DecodePlan plan;
+  if (plan_window(window, sinks, num_seqs, num_q_heads, max_context_len, cache, &plan) != PKV_OK) return 0;
+  return plan.workspace;
+}
+
+pkv_status paged_attention_decode_window(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                         const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t max_context_len, int32_t window, int32_t sinks, float scale, void* out,
+                                         int32_t out_dtype, void* workspace, size_t workspace_bytes,
+                                         const pkv_cache_desc* cache, void* stream) {
+  DecodePlan plan;
+  if (pkv_status st = plan_window(window, sinks, num_seqs, num_q_heads, max_context_len, cache, &plan)) return st;
+  return decode(plan, window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
+                num_q_heads, max_context_len, scale, out, out_dtype, workspace, workspace_bytes, cache, stream);
+}
+
+pkv_status paged_attention_prefill_window(const void* q, const void* k_cache, const void* v_cache,
+                                          const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                          const int32_t* context_lens, const int32_t* query_start, int32_t num_seqs,
+                                          int32_t num_q_heads, int32_t num_query_tokens, int32_t max_context_len,
+                                          int32_t window, int32_t sinks, float scale, void* out, int32_t out_dtype,
+                                          void* workspace, size_t workspace_bytes, const pkv_cache_desc* cache,
+                                          void* stream) {
+  if (pkv_status st = check_window(window, sinks)) return st;
+  return prefill(window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, num_seqs,
+                 num_q_heads, num_query_tokens, max_context_len, scale, out, out_dtype, workspace, workspace_bytes, cache,
+                 stream);
 }
 
 pkv_status paged_kv_gather(const void* k_cache, const void* v_cache, const int32_t* block_tables,

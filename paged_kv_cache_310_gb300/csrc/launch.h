@@ -31,6 +31,8 @@ struct DecodeParams {
   float scale_log2;  // softmax scale * log2(e): scores live in the exp2 domain
   uint64_t wait_limit_ns;  // bound of every pipeline wait (kWaitLimitNs unless a test lowers it)
   int32_t heads_per_item;  // KV heads of one tensor-core work item: 1, or 2 (head_dim 64, paired heads)
+  int32_t window, sinks;   // windowed attention (0: every token): see window.cuh
+  int32_t sink_blocks, max_len;  // windowed: blocks that hold sinks; the host's bound of context_lens
 };
 
 // Multi-token causal (prefill) attention, tensor cores; f16/bf16, head_dim 64 or 128.
@@ -51,6 +53,7 @@ struct PrefillParams {
   int32_t out_f32;
   float scale_log2;
   uint64_t wait_limit_ns;  // bound of every pipeline wait (kWaitLimitNs unless a test lowers it)
+  int32_t window, sinks, sink_blocks;  // windowed attention (0: every token): see window.cuh
 };
 int prefill_tile_tokens(int group);
 size_t prefill_max_items(int num_seqs, int num_query_tokens, int num_kv_heads, int group);

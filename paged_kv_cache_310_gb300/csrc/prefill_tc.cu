@@ -51,6 +51,7 @@
 #include "launch.h"
 #include "tc_util.cuh"
 #include "tcgen05.cuh"
+#include "window.cuh"
 
 namespace pkv {
 namespace {
@@ -126,10 +127,14 @@ struct PrefillArgs {
 // {s, g | ntile_a << 12 | ntile_b << 20, first query token of tile a, position of that token}
 struct Item {
   int s, g, na, nb, qrow0, pos0, last, nchunks;  // na, nb: tokens in tile a, tile b
+  int shift, gap;  // windowed: blocks left out, masked places from `sinks` on
   __device__ __forceinline__ int ntok(int tile) const { return tile ? nb : na; }
 };
 
-__device__ __forceinline__ Item unpack_item(int4 e, int tq) {
+// kWin: windowed; positions are then places (see window.cuh) of the pair's first token's view.
+template <bool kWin>
+__device__ __forceinline__ Item unpack_item(int4 e, const PrefillParams& p) {
+  const int tq = p.tile_tokens;
   Item t;
   t.s = e.x;
   t.g = e.y & 0xfff;
@@ -137,20 +142,30 @@ __device__ __forceinline__ Item unpack_item(int4 e, int tq) {
   t.nb = (static_cast<unsigned>(e.y) >> 20) & 0xff;
   t.qrow0 = e.z;
   t.pos0 = e.w;
+  t.shift = t.gap = 0;
+  if (kWin) {
+    const WindowView v = window_view(max(0, t.pos0 - p.window + 1), p.sinks, p.sink_blocks, p.block_size);
+    t.shift = v.shift;
+    t.gap = v.gap;
+    t.pos0 -= v.shift * p.block_size;
+  }
   t.last = t.pos0 + (t.nb ? tq + t.nb : t.na) - 1;  // position of the pair's last token
   t.nchunks = (t.last + kKC) / kKC;
   return t;
 }
 
+// The lowest n bits (none below 0, all from 64 on).
+__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
+
 // Extreme of a row's 64 raw scores (maximum, or minimum when the scale is negative),
-// keys past `lim` excluded when the chunk crosses the diagonal (overwritten in place
-// with the neutral value).
-template <bool kMin>
-__device__ __forceinline__ float chunk_extreme(float* sv, bool diagonal, int lim) {
+// keys past `lim` -- windowed: those without a bit in `seen` -- excluded when the mask cuts
+// the row's chunk (overwritten in place with the neutral value).
+template <bool kMin, bool kWin>
+__device__ __forceinline__ float chunk_extreme(float* sv, bool diagonal, int lim, uint64_t seen) {
   constexpr float kNone = kMin ? INFINITY : -INFINITY;
   if (diagonal) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i) sv[i] = i <= lim ? sv[i] : kNone;
+    for (int i = 0; i < 64; ++i) sv[i] = (kWin ? (seen >> i & 1) != 0 : i <= lim) ? sv[i] : kNone;
   }
   float e0 = kNone, e1 = kNone;
 #pragma unroll
@@ -164,7 +179,7 @@ __device__ __forceinline__ float chunk_extreme(float* sv, bool diagonal, int lim
 // One producer warp's copies of an item's chunks of K (or V) into its ring: per chunk
 // one 4-D box per block (blocks past the pair's last position from outside the tensor:
 // zero fill).  `c` counts the warp's chunks over all items.  Returns false on abort.
-template <int D>
+template <int D, bool kWin>
 __device__ __forceinline__ bool load_chunks(const PrefillParams& p, const Item& it, const CUtensorMap* map,
                                             unsigned char* ring, uint64_t* full, uint64_t* empty, int& c,
                                             int* issued_slot, uint64_t policy, volatile int* abort_flag) {
@@ -178,7 +193,8 @@ __device__ __forceinline__ bool load_chunks(const PrefillParams& p, const Item& 
     const int st = c % kStages;
     const int lb = k * blocks_per_chunk + lane;  // logical block of this lane
     const bool live = lane < blocks_per_chunk && lb * bs <= it.last;
-    int b = live ? (lb < p.max_blocks_per_seq ? table[lb] : -1) : 0;
+    const int tb = kWin && lb >= p.sink_blocks ? lb + it.shift : lb;  // its table entry
+    int b = live ? (tb < p.max_blocks_per_seq ? table[tb] : -1) : 0;
     bool ok = true;
     if (lane == 0) {
       ok = c < kStages || wait_role(&empty[st], ((c / kStages) - 1) & 1, abort_flag, p.err, p.wait_limit_ns);
@@ -202,7 +218,7 @@ __device__ __forceinline__ bool load_chunks(const PrefillParams& p, const Item& 
   return true;
 }
 
-template <typename T, int D>
+template <typename T, int D, bool kWin>
 __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_constant__ PrefillArgs a) {
   using L = PfLayout<D>;
   constexpr int kStages = L::kStages, kGroup = L::kGroup, kKVTile = L::kKVTile;
@@ -265,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     bool ok = true;
     ItemCursor cur;
     for (cur.init(p.work_list, num_items); cur.valid() && ok; cur.advance(), ++j) {
-      const Item it = unpack_item(cur.cur, TQ);
+      const Item it = unpack_item<kWin>(cur.cur, p);
       // ---- both tiles' queries into buffer j % kQBufs (free once item j - kQBufs's QKs completed) ----
       const int qb = j % kQBufs;
       if (lane == 0) {
@@ -287,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       }
       if (lane == 0) *qissued_slot = j + 1;
       // ---- K chunks (a stage is free once both tiles' QKs of its chunk completed) ----
-      ok = load_chunks<D>(p, it, &a.tk, smem, bars.kfull, bars.kempty, c, kissued_slot, pol_kv, abort_flag);
+      ok = load_chunks<D, kWin>(p, it, &a.tk, smem, bars.kfull, bars.kempty, c, kissued_slot, pol_kv, abort_flag);
     }
   } else if (warp == kVWarp) {
     // ============================ producer: V ============================
@@ -298,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     ItemCursor cur;
     for (cur.init(p.work_list, num_items); cur.valid() && ok; cur.advance()) {
       // a stage is free once both tiles' PVs of its chunk completed
-      ok = load_chunks<D>(p, unpack_item(cur.cur, TQ), &a.tv, smem + kOffV, bars.vfull, bars.vempty, c,
+      ok = load_chunks<D, kWin>(p, unpack_item<kWin>(cur.cur, p), &a.tv, smem + kOffV, bars.vfull, bars.vempty, c,
                           vissued_slot, pol_kv, abort_flag);
     }
   } else if (warp == kMmaWarp) {
@@ -320,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     // QK side: next chunk qc (global), its stage / phase, its place in the item
     ItemCursor qcur;
     qcur.init(p.work_list, num_items);
-    int qc = 0, qst = 0, qph = 0, qk = 0, qn = qcur.valid() ? unpack_item(qcur.cur, TQ).nchunks : 0;
+    int qc = 0, qst = 0, qph = 0, qk = 0, qn = qcur.valid() ? unpack_item<kWin>(qcur.cur, p).nchunks : 0;
     // PV side
     ItemCursor pcur;
     pcur.init(p.work_list, num_items);
@@ -359,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       if (++qk == qn) {
         qk = 0;
         qcur.advance();
-        qn = qcur.valid() ? unpack_item(qcur.cur, TQ).nchunks : 0;
+        qn = qcur.valid() ? unpack_item<kWin>(qcur.cur, p).nchunks : 0;
       }
       return true;
     };
@@ -405,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       if (++pk == pn) {
         pk = 0;
         pcur.advance();
-        pn = pcur.valid() ? unpack_item(pcur.cur, TQ).nchunks : 0;
+        pn = pcur.valid() ? unpack_item<kWin>(pcur.cur, p).nchunks : 0;
       }
       if (qcur.valid()) ok = qk_pair((seen & 8u) != 0);
     }
@@ -460,11 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
 
     ItemCursor cur;
     for (cur.init(p.work_list, num_items); cur.valid() && ok; cur.advance()) {
-      const Item it = unpack_item(cur.cur, TQ);
+      const Item it = unpack_item<kWin>(cur.cur, p);
       const bool row_valid = head < G && tok < it.ntok(grp);
       const int qpos = row_valid ? it.pos0 + grp * TQ + tok : it.last;  // padding rows act as the last token
       const int out_row = row_valid ? (it.qrow0 + grp * TQ + tok) * p.num_q_heads + it.g * G + head : -1;
-      float m = 0.f, l = 0.f;  // max used for this row's probabilities, running row sum
+      float m = kWin ? -INFINITY : 0.f, l = 0.f;  // max used for this row's probabilities, running row sum
       for (int k = 0; k < it.nchunks; ++k, ++c) {
         const int sb = c & 1;
         const uint32_t sbuf = lane_base + sb * 64;
@@ -475,18 +491,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         tc_fence_after();
         const int kbase = k * kKC;
         const int lim = qpos - kbase;            // keys of the chunk past lim are masked
-        const bool diagonal = lim < kKC - 1;     // only then does the mask cut this row
+        // windowed: so are those before its window, but for the sinks
+        const int low = kWin ? lim - p.window + 1 : 0, sink = kWin ? p.sinks - kbase : 0;
+        const bool diagonal = lim < kKC - 1 || (kWin && low > max(0, sink));  // only then does the mask cut this row
+        const uint64_t seen = kWin ? low_bits(lim + 1) & (~low_bits(low) | low_bits(sink)) : 0;
         // the row's 64 scores, held in registers for both passes
         float sv[64];
         tmem_load64(sbuf, sv);
         // pass 1: the row's chunk maximum of scale * score under the mask
-        const float cm = (neg_scale ? chunk_extreme<true>(sv, diagonal, lim)
-                                    : chunk_extreme<false>(sv, diagonal, lim)) * p.scale_log2;
+        float cm = (neg_scale ? chunk_extreme<true, kWin>(sv, diagonal, lim, seen)
+                              : chunk_extreme<false, kWin>(sv, diagonal, lim, seen)) * p.scale_log2;
+        if (kWin && seen == 0) cm = -INFINITY;  // whatever the scale
         // lazy rescale: keep m unless the chunk brings a score more than the slack above
-        // (a chunk entirely past this row's position gives cm = -inf and changes nothing)
+        // (a chunk that the mask leaves nothing of gives cm = -inf and changes nothing)
         float alpha = 1.f;
-        if (k == 0) {
-          m = cm;  // key 0 is never masked: finite
+        if (kWin ? m == -INFINITY : k == 0) {
+          // key 0 is never masked: finite.  Windowed, rows whose window starts in a later
+          // chunk stay at -inf until then, with sums and O of zero that need no rescale.
+          m = cm;
         } else if (cm > m + kRescaleSlack) {
           alpha = exp2f(m - cm);
           m = cm;
@@ -520,7 +542,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         // pass 2: probabilities as hi + lo parts, written over the 16 S columns they
         // came from: [hi of 16 keys | lo of 16 keys]
         float2 acc = make_float2(0.f, 0.f);
-        const float2 nm2 = make_float2(-m, -m);
+        const float used = kWin && m == -INFINITY ? 0.f : m;  // nothing seen yet: every p is masked
+        const float2 nm2 = make_float2(-used, -used);
 #pragma unroll
         for (int q = 0; q < kKC / 16; ++q) {
           uint32_t w[16];
@@ -529,8 +552,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             const float2 x = __ffma2_rn(make_float2(sv[q * 16 + 2 * i], sv[q * 16 + 2 * i + 1]), sc2, nm2);
             float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
             if (diagonal) {
-              p0 = q * 16 + 2 * i <= lim ? p0 : 0.f;
-              p1 = q * 16 + 2 * i + 1 <= lim ? p1 : 0.f;
+              const int i0 = q * 16 + 2 * i;
+              p0 = (kWin ? (seen >> i0 & 1) != 0 : i0 <= lim) ? p0 : 0.f;
+              p1 = (kWin ? (seen >> (i0 + 1) & 1) != 0 : i0 + 1 <= lim) ? p1 : 0.f;
             }
             const float2 pr = make_float2(p0, p1);
             float h0, h1;
@@ -544,18 +568,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         l += acc.x + acc.y;
         tmem_store_wait();
         tc_fence_before();
-        // V rows past the pair's last position inside loaded blocks: zero them (a NaN
-        // there would survive a zero weight).  Both groups write the same zeros.
+        // V rows past the pair's last position inside loaded blocks, and those of a window's
+        // gap: zero them (a NaN there would survive a zero weight).  Both groups write the
+        // same zeros.
         const int rows_needed = it.last + 1 - kbase;
-        if (rows_needed < kKC) {  // warp-uniform; V of this chunk must have landed first
+        const int gap0 = kWin ? max(0, p.sinks - kbase) : 0;
+        const int gap1 = kWin ? min(kKC, p.sinks + it.gap - kbase) : 0;
+        const bool unseen = rows_needed < kKC || (kWin && gap0 < gap1);
+        if (unseen) {  // warp-uniform; V of this chunk must have landed first
           if (!__all_sync(0xffffffffu, wait_role(&bars.vfull[c % kStages], (c / kStages) & 1, abort_flag, p.err, p.wait_limit_ns))) {
             ok = false;
             break;
           }
         }
-        if (t < kKC && rows_needed < kKC) {
+        if (t < kKC && unseen) {
           const int rows_loaded = min(kKC, (rows_needed + p.block_size - 1) / p.block_size * p.block_size);
-          if (t >= rows_needed && t < rows_loaded) {
+          if ((t >= rows_needed && t < rows_loaded) || (kWin && t >= gap0 && t < gap1)) {
             unsigned char* vrow = smem + kOffV + (c % kStages) * kKVTile + (t >> 3) * kGroup + (t & 7) * 128;
 #pragma unroll
             for (int q = 0; q < 8 * L::kBlocks; ++q)  // 128 bytes per 64-column block, 1 KB apart
@@ -674,14 +702,20 @@ bool make_query_map(CUtensorMap* m, const void* q, uint32_t heads, uint32_t toke
   });
 }
 
-template <typename T, int D>
-cudaError_t launch_prefill_t(const PrefillArgs& args, int grid, cudaStream_t stream) {
+template <typename T, int D, bool kWin>
+cudaError_t launch_prefill_w(const PrefillArgs& args, int grid, cudaStream_t stream) {
   constexpr int smem = PfLayout<D>::kSmemBytes;
   static std::atomic<unsigned long long> configured{0};  // devices whose limit is raised
-  cudaError_t e = ensure_smem_limit(prefill_tc_kernel<T, D>, smem, configured);
+  cudaError_t e = ensure_smem_limit(prefill_tc_kernel<T, D, kWin>, smem, configured);
   if (e != cudaSuccess) return e;
-  prefill_tc_kernel<T, D><<<grid, kThreads, smem, stream>>>(args);
+  prefill_tc_kernel<T, D, kWin><<<grid, kThreads, smem, stream>>>(args);
   return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t launch_prefill_t(const PrefillArgs& args, int grid, cudaStream_t stream) {
+  return args.p.window ? launch_prefill_w<T, D, true>(args, grid, stream)
+                       : launch_prefill_w<T, D, false>(args, grid, stream);
 }
 
 }  // namespace
