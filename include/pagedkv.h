@@ -345,8 +345,8 @@ pkv_status paged_rotary_frequencies(double* inv_freq, int32_t rotary_dim, double
  *   y = x * weight / sqrt(mean(x^2) + eps)  (y = x where the weight is NULL);
  *   each pair (y_a, y_b) of the layout becomes (y_a c - y_b s, y_b c + y_a s), with
  *   c = factor cos(positions[t] * inv_freq[i]), s = factor sin(positions[t] * inv_freq[i]);
- * the other dimensions stay y.  fp32 throughout, the angle without its whole turns exact to
- * 2^-30 turns for positions up to 2^20 and frequencies up to 1; one rounding at the end (RNE).
+ * the other dimensions stay y.  fp32 throughout, but for the angle, which is good to 2^-31
+ * turns at any position for frequencies up to 1; one rounding at the end (RNE).
  * Negative positions are padding: nothing of the token is written.
  *
  * q, k, q_out, k_out: device, dtype f32, f16 or bf16; a token's heads lie one after the
@@ -389,9 +389,9 @@ pkv_status paged_kv_append_rotary(const void* q, int64_t q_stride, const void* k
 
 /*
  * paged_attention_decode_window -- paged_attention_decode over a window.  One new token per
- * sequence, at position context_lens[s] - 1; the other arguments, types, groups, errors, the
- * workspace's ownership and the early start as there.  16-bit caches run on tensor cores,
- * groups up to 16; f32 caches on CUDA cores, groups up to 8, fp32 throughout.
+ * sequence, at position context_lens[s] - 1; the other arguments, types, errors and the
+ * workspace's ownership as there.  16-bit caches run on tensor cores in one kernel, groups
+ * up to 16, and need no workspace; f32 caches on CUDA cores, groups up to 8, fp32 throughout.
  * max_context_len: host upper bound on context_lens (a longer sequence sets the device
  * index flag, and its rows of out are left as they are).  Cost goes by the tokens attended
  * to, not by context_lens.

@@ -37,6 +37,7 @@ import ctypes
 import functools
 import os
 import re
+import struct
 import threading
 
 import torch
@@ -88,12 +89,6 @@ class DecodePlan(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("kv_heads_per_item", ctypes.c_int32)]
 
 
-class Rotary(ctypes.Structure):
-    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("layout", ctypes.c_int32),
-                ("factor", ctypes.c_float), ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
-                ("k_weight", ctypes.c_void_p)]
-
-
 class RotaryScaling(ctypes.Structure):
     _fields_ = [("rule", ctypes.c_int32), ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
                 ("fast_turns", ctypes.c_double), ("slow_turns", ctypes.c_double)]
@@ -141,9 +136,8 @@ def library():
             "paged_kv4_expand": [vp, i32, vp, vp, desc_p, vp, vp, desc_p, vp],
             "paged_rotary_frequencies": [vp, i32, ctypes.c_double, ctypes.POINTER(RotaryScaling),
                                          ctypes.POINTER(ctypes.c_float)],
-            "paged_qk_rotary": [vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, ctypes.POINTER(Rotary), vp, i64, vp, i64, vp],
-            "paged_kv_append_rotary": [vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, ctypes.POINTER(Rotary), vp, i64, vp, vp,
-                                       desc_p, vp],
+            "paged_qk_rotary": [vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp, i64, vp],
+            "paged_kv_append_rotary": [vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, vp, vp, i64, vp, vp, desc_p, vp],
             "paged_attention_decode_window_workspace_bytes": [i32, i32, i32, i32, i32, desc_p],
             "paged_attention_decode_window": [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, ctypes.c_float, vp, i32,
                                               vp, sz, desc_p, vp],
@@ -731,25 +725,36 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str |
 
 def _token_rows(t, what, dtype, device, tokens, head_dim):
     """(address, token stride, heads) of a [T, H, head_dim] tensor whose tokens may lie apart."""
-    if t.dim() != 3 or t.dtype != dtype or t.get_device() != device or t.shape[0] != tokens or t.shape[2] != head_dim:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != head_dim or t.dtype is not dtype or t.get_device() != device:
         raise PagedKVError(1, f"{what} must be [T, heads, {head_dim}] of one dtype on one CUDA device")
-    heads, row = t.shape[1], t.shape[1] * head_dim
-    stride = t.stride()
-    if stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
+    heads = shape[1]
+    if stride[2] != 1 or (stride[1] != head_dim and heads > 1):
         raise PagedKVError(1, f"{what}: the heads of a token must lie one after the other")
-    return t.data_ptr(), stride[0] if tokens > 1 else row, heads
+    return t.data_ptr(), stride[0] if tokens > 1 else heads * head_dim, heads
 
 
-def _rotary(inv_freq, interleaved, factor, q_weight, k_weight, eps, dtype, device, head_dim):
+_pack_rotary = struct.Struct("@PiiffPP").pack  # pkv_rotary, field by field: quicker than a ctypes.Structure
+
+
+def _rotary(inv_freq, interleaved, factor, q_weight, k_weight, eps, dtype, device, head_dim) -> bytes:
     """The C struct of a rotation."""
-    pairs = 0 if inv_freq is None else inv_freq.numel()
-    if pairs and (inv_freq.dtype != torch.float64 or inv_freq.get_device() != device or not inv_freq.is_contiguous()):
-        raise PagedKVError(1, "inv_freq must be a contiguous float64 tensor on the call's device")
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype != dtype or w.get_device() != device or not w.is_contiguous() or w.numel() != head_dim):
-            raise PagedKVError(1, "norm weights must be contiguous, [head_dim], of the tensors' dtype and device")
-    return Rotary(inv_freq.data_ptr() if pairs else 0, 2 * pairs, 1 if interleaved else 0, factor, eps,
-                  0 if q_weight is None else q_weight.data_ptr(), 0 if k_weight is None else k_weight.data_ptr())
+    pairs = freq = qw = kw = 0
+    if inv_freq is not None:
+        pairs, freq = inv_freq.numel(), inv_freq.data_ptr()
+        if inv_freq.dtype is not torch.float64 or inv_freq.get_device() != device or not inv_freq.is_contiguous():
+            raise PagedKVError(1, "inv_freq must be a contiguous float64 tensor on the call's device")
+    if q_weight is not None:
+        qw = _norm_weight(q_weight, dtype, device, head_dim)
+    if k_weight is not None:
+        kw = _norm_weight(k_weight, dtype, device, head_dim)
+    return _pack_rotary(freq, 2 * pairs, 1 if interleaved else 0, factor, eps, qw, kw)
+
+
+def _norm_weight(w, dtype, device, head_dim) -> int:
+    if w.dtype is not dtype or w.get_device() != device or not w.is_contiguous() or w.numel() != head_dim:
+        raise PagedKVError(1, "norm weights must be contiguous, [head_dim], of the tensors' dtype and device")
+    return w.data_ptr()
 
 
 def paged_qk_rotary(q, k, positions, q_out, k_out, inv_freq, *, interleaved: bool = False, factor: float = 1.0,
@@ -775,7 +780,7 @@ def paged_qk_rotary(q, k, positions, q_out, k_out, inv_freq, *, interleaved: boo
         raise PagedKVError(1, "q_out and k_out must have the shapes of q and k")
     rotary = _rotary(inv_freq, interleaved, factor, q_weight, k_weight, eps, dtype, device, d)
     _call(library().paged_qk_rotary, device, qp, qs, kp, ks, positions.data_ptr(), tokens, hq, hkv, d,
-          _dtype_code(q, "q"), ctypes.byref(rotary), qop, qos, kop, kos)
+          _dtype_code(q, "q"), rotary, qop, qos, kop, kos)
 
 
 def paged_kv_append_rotary(q, k, v, positions, slot_mapping, k_cache, v_cache, q_out, inv_freq, *,
@@ -802,7 +807,7 @@ def paged_kv_append_rotary(q, k, v, positions, slot_mapping, k_cache, v_cache, q
         raise PagedKVError(1, "q_out must have q's shape, k and v the caches' KV heads")
     rotary = _rotary(inv_freq, interleaved, factor, q_weight, k_weight, eps, dtype, device, d)
     _call(library().paged_kv_append_rotary, device, qp, qs, kp, ks, vp, vs, positions.data_ptr(), slot_mapping.data_ptr(),
-          tokens, hq, ctypes.byref(rotary), qop, qos, k_cache.data_ptr(), v_cache.data_ptr(), desc_ref)
+          tokens, hq, rotary, qop, qos, k_cache.data_ptr(), v_cache.data_ptr(), desc_ref)
     return q_out
 
 

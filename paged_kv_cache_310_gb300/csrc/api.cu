@@ -85,6 +85,7 @@ struct DecodePlan {
   size_t workspace; // bytes
   size_t list_bytes;  // work list (tensor-core path): 256-byte header + entries
   size_t ml_bytes;    // partition (max, sum) pairs
+  int rows_cluster;   // windowed 16-bit caches: CTAs of window_rows_kernel per (sequence, KV head); else 0
 };
 
 int round_up(int x, int m) { return (x + m - 1) / m * m; }
@@ -148,6 +149,7 @@ pkv_status plan_decode(int32_t num_seqs, int32_t num_q_heads, int32_t max_len,
     part = max_len <= auto_part ? (max_len < 128 ? 128 : round_up(max_len, 128)) : auto_part;
   }
   plan->path = path;
+  plan->rows_cluster = 0;
   plan->part_tokens = part;
   plan->max_parts = max_len == 0 ? 1 : (max_len + part - 1) / part;
   if (path == PKV_PATH_TENSOR_CORE && plan->max_parts >= 32768)
@@ -368,6 +370,69 @@ size_t paged_attention_prefill_workspace_bytes(int32_t num_seqs, int32_t num_q_h
 
 namespace {
 
+pkv_status check_window(int32_t window, int32_t sinks) {
+  if (window < 1) return fail(PKV_ERR_INVALID_ARG, "window %d < 1", window);
+  if (sinks < 0) return fail(PKV_ERR_INVALID_ARG, "sinks %d < 0", sinks);
+  return PKV_OK;
+}
+
+// CTAs that share the tokens of one of `items` (columns, KV head) in window_rows_kernel: as
+// many as the GPU holds at once (two an SM), of 64 tokens or more each.
+int rows_cluster(int64_t items, int64_t tokens) {
+  int size = 1;
+  while (size < 8 && 2 * size * items <= 2 * 152 && tokens > 64 * size) size *= 2;
+  return size;
+}
+
+// The windowed decode's plan.  16-bit caches: one kernel, no workspace.  f32 caches: the CUDA-core
+// kernel over sequences of the tokens that it runs over at most, those of the sinks' and the
+// window's blocks: fp32 throughout, where the tf32 kernel's split operands lose 2^-21 of a score.
+pkv_status plan_window(int32_t window, int32_t sinks, int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
+                       const pkv_cache_desc* cache, DecodePlan* plan) {
+  if (pkv_status st = check_window(window, sinks)) return st;
+  if (pkv_status st = check_cache(cache)) return st;
+  const int64_t bs = cache->block_size, most = (sinks + bs - 1) / bs * bs + static_cast<int64_t>(window) + bs - 1;
+  const int32_t tokens = max_context_len < most ? max_context_len : static_cast<int32_t>(most);
+  const bool f32 = cache->dtype == PKV_F32;
+  const pkv_decode_config config = {f32 ? PKV_PATH_CUDA_CORE : PKV_PATH_TENSOR_CORE, 0};
+  if (pkv_status st = plan_decode(num_seqs, num_q_heads, tokens, cache, &config, plan)) return st;
+  if (!f32) {
+    plan->rows_cluster = rows_cluster(static_cast<int64_t>(num_seqs) * cache->num_kv_heads, tokens);
+    plan->workspace = 0;
+  }
+  return PKV_OK;
+}
+
+// What a launch of window_rows_kernel needs, from the checked arguments of either call.
+WindowRowsParams rows_params(int32_t window, int32_t sinks, const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                             int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len, float scale, void* out,
+                             int32_t out_dtype, const pkv_cache_desc* cache, int* flag) {
+  WindowRowsParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.out = out;
+  p.err = flag;
+  p.num_seqs = num_seqs;
+  p.num_q_heads = num_q_heads;
+  p.num_kv_heads = cache->num_kv_heads;
+  p.group = num_q_heads / cache->num_kv_heads;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.block_size = cache->block_size;
+  p.num_blocks = cache->num_blocks;
+  p.head_dim = cache->head_dim;
+  p.max_len = max_context_len;
+  p.window = std::min(window, std::max(max_context_len, 1));
+  p.sinks = std::min(sinks, max_context_len);
+  p.sink_blocks = (p.sinks - 1) / p.block_size + (p.sinks > 0);
+  p.out_f32 = out_dtype == PKV_F32 ? 1 : 0;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  return p;
+}
+
 // What paged_attention_decode and its windowed form share.  The plan is for the tokens that a
 // sequence's kernels run over; max_context_len bounds all that it has (window 0: the same).
 pkv_status decode(const DecodePlan& plan, int32_t window, int32_t sinks, const void* q, const void* k_cache,
@@ -397,6 +462,14 @@ pkv_status decode(const DecodePlan& plan, int32_t window, int32_t sinks, const v
   }
   int* flag = nullptr;
   if (pkv_status st = device_flag(&flag)) return st;
+
+  if (plan.rows_cluster > 0) {
+    WindowRowsParams p = rows_params(window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                                     num_seqs, num_q_heads, max_context_len, scale, out, out_dtype, cache, flag);
+    p.cluster = plan.rows_cluster;
+    cudaError_t e = launch_window_rows(p, cache->dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "windowed decode launch");
+  }
 
   DecodeParams p{};
   p.q = q;
@@ -444,25 +517,6 @@ pkv_status decode(const DecodePlan& plan, int32_t window, int32_t sinks, const v
   return PKV_OK;
 }
 
-pkv_status check_window(int32_t window, int32_t sinks) {
-  if (window < 1) return fail(PKV_ERR_INVALID_ARG, "window %d < 1", window);
-  if (sinks < 0) return fail(PKV_ERR_INVALID_ARG, "sinks %d < 0", sinks);
-  return PKV_OK;
-}
-
-// The windowed decode's plan: as for sequences of the tokens that its kernels run over at most,
-// those of the sinks' and the window's blocks.  16-bit caches on tensor cores, f32 on CUDA
-// cores: fp32 throughout, where the tf32 kernel's split operands lose 2^-21 of a score.
-pkv_status plan_window(int32_t window, int32_t sinks, int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
-                       const pkv_cache_desc* cache, DecodePlan* plan) {
-  if (pkv_status st = check_window(window, sinks)) return st;
-  if (pkv_status st = check_cache(cache)) return st;
-  const int64_t bs = cache->block_size, most = (sinks + bs - 1) / bs * bs + static_cast<int64_t>(window) + bs - 1;
-  const pkv_decode_config config = {cache->dtype == PKV_F32 ? PKV_PATH_CUDA_CORE : PKV_PATH_TENSOR_CORE, 0};
-  return plan_decode(num_seqs, num_q_heads, max_context_len < most ? max_context_len : static_cast<int32_t>(most), cache,
-                     &config, plan);
-}
-
 // What paged_attention_prefill and its windowed form (window > 0) share.
 pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_cache, const void* v_cache,
                    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
@@ -499,6 +553,18 @@ pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_c
   if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   int* flag = nullptr;
   if (pkv_status st = device_flag(&flag)) return st;
+  // few new tokens per sequence: passes over K and V for kRowsPerGroup query rows each
+  const int per = kRowsPerGroup / group;
+  const int64_t groups = num_query_tokens / per + static_cast<int64_t>(num_seqs);
+  if (window > 0 && groups <= 65535 && static_cast<int64_t>(num_query_tokens) * group <= 2 * kRowsPerGroup * static_cast<int64_t>(num_seqs)) {
+    WindowRowsParams p = rows_params(window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                                     num_seqs, num_q_heads, max_context_len, scale, out, out_dtype, cache, flag);
+    p.query_start = query_start;
+    p.num_query_tokens = num_query_tokens;
+    p.cluster = rows_cluster(groups * cache->num_kv_heads, std::min<int64_t>(max_context_len, static_cast<int64_t>(window) + sinks + per));
+    cudaError_t e = launch_window_rows(p, cache->dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "windowed prefill launch");
+  }
   PrefillParams p{};
   p.q = q;
   p.k_cache = k_cache;

@@ -388,7 +388,7 @@ cudaError_t launch_simt_w(const DecodeParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-// Windowed 16-bit caches are the tensor-core kernel's alone.
+// Windowed 16-bit caches have a kernel of their own (window_rows.cu).
 template <typename T, int D, int GM>
 cudaError_t launch_simt_t(const DecodeParams& p, cudaStream_t stream) {
   if (!p.window) return launch_simt_w<T, D, GM, false>(p, stream);
@@ -412,8 +412,9 @@ cudaError_t launch_simt_d(const DecodeParams& p, cudaStream_t stream) {
 template <typename T>
 cudaError_t launch_merge_t(const DecodeParams& p, cudaStream_t stream) {
   const int grid = p.num_q_heads * p.num_seqs;  // (query head, sequence), head fastest
-  return p.window ? launch_dependent(merge_kernel<T, true>, grid, 128, 0, stream, p)
-                  : launch_dependent(merge_kernel<T, false>, grid, 128, 0, stream, p);
+  if (!p.window) return launch_dependent(merge_kernel<T, false>, grid, 128, 0, stream, p);
+  if constexpr (sizeof(T) == 4) return launch_dependent(merge_kernel<T, true>, grid, 128, 0, stream, p);
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace

@@ -69,7 +69,6 @@
 #include "launch.h"
 #include "tcgen05.cuh"
 #include "tc_util.cuh"
-#include "window.cuh"
 
 namespace pkv {
 namespace {
@@ -254,41 +253,26 @@ struct TcArgs {
 };
 
 // One work item = (sequence, KV head, partition) with at least one token, packed by
-// the work-list kernel as {s, g, t0, ntok | nparts << 16}; windowed (kWin: tokens are places
-// of the sequence without its gap's blocks, see window.cuh) as {s | part << 16, shift,
-// g | gap << 16, ntok | nparts << 16}.
+// the work-list kernel as {s, g, t0, ntok | nparts << 16}.
 struct Item {
   int s, g, part, t0, ntok, nchunks, nparts;
-  int shift, gap;  // windowed
 };
 
-template <bool kWin>
 __device__ __forceinline__ Item unpack_item(int4 e, int part_tokens) {
   Item it;
-  if (kWin) {
-    it.s = e.x & 0xffff;
-    it.part = static_cast<int>(static_cast<unsigned>(e.x) >> 16);
-    it.shift = e.y;
-    it.g = e.z & 0xffff;
-    it.gap = e.z >> 16;
-    it.t0 = it.part * part_tokens;
-  } else {
-    it.s = e.x;
-    it.g = e.y;
-    it.t0 = e.z;
-    it.part = it.t0 / part_tokens;
-    it.shift = it.gap = 0;
-  }
+  it.s = e.x;
+  it.g = e.y;
+  it.t0 = e.z;
   it.ntok = e.w & 0xffff;
   it.nparts = static_cast<int>(static_cast<unsigned>(e.w) >> 16);
+  it.part = it.t0 / part_tokens;
   it.nchunks = (it.ntok + kChunk - 1) / kChunk;
   return it;
 }
 
 // kPair (head_dim D = 64, an even number of KV heads): an item covers two adjacent KV
 // heads and runs with head_dim-128 operands (see the paired-heads note above).
-// kWin: windowed (see window.cuh).
-template <typename T, int D, int GM, bool kPair, bool kWin>
+template <typename T, int D, int GM, bool kPair>
 __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(const __grid_constant__ TcArgs a) {
   static_assert(kPair ? D == 64 && (GM == 16 || GM == 32) : GM <= 16, "paired heads: head_dim 64");
   constexpr int DL = kPair ? 128 : D;  // operand width: dimensions of a K/V row in shared memory
@@ -436,7 +420,7 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
         e.w = __shfl_sync(0xffffffffu, e.w, 0);
         if (!ok || !item_valid(e)) break;
       }
-      const Item it = unpack_item<kWin>(e, p.part_tokens);
+      const Item it = unpack_item(e, p.part_tokens);
       int4 nxt = make_int4(0, 0, 0, 0);  // lane 0: the entry of item j + 1
       const int qb = j & 1;
       if (lane == 0) {
@@ -468,8 +452,7 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
         // block ids first: their latency overlaps the wait for a free stage
         const int lb = it.t0 / bs + k * blocks_per_chunk + lane;  // logical block of this lane
         const bool live = lane < blocks_per_chunk && lb * bs < it.t0 + it.ntok;
-        const int tb = kWin && lb >= p.sink_blocks ? lb + it.shift : lb;  // its table entry
-        int b = live ? (tb < p.max_blocks_per_seq ? table[tb] : -1) : 0;
+        int b = live ? (lb < p.max_blocks_per_seq ? table[lb] : -1) : 0;
         if (lane == 0) {
           ok = c < kKStages || wait_role(&bars.kempty[st], ((c / kKStages) - 1) & 1, abort_flag, p.err, p.wait_limit_ns);
           if (ok) mbar_arrive_expect_tx(&bars.kfull[st], kTileBytes);
@@ -526,14 +509,13 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
         if (lane == 0) mbar_arrive(&bars.iempty[r]);
         if (!item_valid(e)) break;
       }
-      const Item it = unpack_item<kWin>(e, p.part_tokens);
+      const Item it = unpack_item(e, p.part_tokens);
       const int32_t* table = p.block_tables + static_cast<size_t>(it.s) * p.max_blocks_per_seq;
       for (int k = 0; k < it.nchunks && ok; ++k, ++c) {
         const int st = c % kVStages;
         const int lb = it.t0 / bs + k * blocks_per_chunk + lane;
         const bool live = lane < blocks_per_chunk && lb * bs < it.t0 + it.ntok;
-        const int tb = kWin && lb >= p.sink_blocks ? lb + it.shift : lb;  // its table entry
-        int b = live ? (tb < p.max_blocks_per_seq ? table[tb] : -1) : 0;
+        int b = live ? (lb < p.max_blocks_per_seq ? table[lb] : -1) : 0;
         if (lane == 0) {
           ok = c < kVStages || wait_role(&bars.vempty[st], ((c / kVStages) - 1) & 1, abort_flag, p.err, p.wait_limit_ns);
           if (ok) mbar_arrive_expect_tx(&bars.vfull[st], kTileBytes);
@@ -584,8 +566,8 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
     if constexpr (!kDyn) {
       qcur.init(p.work_list, num_items);
       pcur.init(p.work_list, num_items);
-      qn = qcur.valid() ? unpack_item<kWin>(qcur.cur, p.part_tokens).nchunks : 0;
-      pn = pcur.valid() ? unpack_item<kWin>(pcur.cur, p.part_tokens).nchunks : 0;
+      qn = qcur.valid() ? unpack_item(qcur.cur, p.part_tokens).nchunks : 0;
+      pn = pcur.valid() ? unpack_item(pcur.cur, p.part_tokens).nchunks : 0;
       qdone = !qcur.valid();
     }
     int qc = 0, pc = 0;           // next chunk to QK, next chunk to PV
@@ -599,7 +581,7 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
         if (qn == 0 && !qdone &&
             __all_sync(0xffffffffu, mbar_test_wait(&bars.ifull[qj % kItemRing], (qj / kItemRing) & 1))) {
           const int4 e = ring[qj % kItemRing];
-          if (item_valid(e)) qn = unpack_item<kWin>(e, p.part_tokens).nchunks;
+          if (item_valid(e)) qn = unpack_item(e, p.part_tokens).nchunks;
           else qdone = true;
           progressed = true;
         }
@@ -613,7 +595,7 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
       if (pc < qc && (seen & 4) && (pk > 0 || pj < 2 || (seen & 8)) && (seen & 16)) {
         if constexpr (kDyn) {
           if (pk == 0) {  // PV starts item pj: its chunk count, then the slot is free
-            pn = unpack_item<kWin>(ring[pj % kItemRing], p.part_tokens).nchunks;
+            pn = unpack_item(ring[pj % kItemRing], p.part_tokens).nchunks;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.iempty[pj % kItemRing]);
           }
@@ -652,7 +634,7 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
           ++pj;
           if constexpr (!kDyn) {
             pcur.advance();
-            pn = pcur.valid() ? unpack_item<kWin>(pcur.cur, p.part_tokens).nchunks : 0;
+            pn = pcur.valid() ? unpack_item(pcur.cur, p.part_tokens).nchunks : 0;
           }
         }
         progressed = true;
@@ -687,7 +669,7 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
             qn = 0;
           } else {
             qcur.advance();
-            qn = qcur.valid() ? unpack_item<kWin>(qcur.cur, p.part_tokens).nchunks : 0;
+            qn = qcur.valid() ? unpack_item(qcur.cur, p.part_tokens).nchunks : 0;
             qdone = !qcur.valid();
           }
         }
@@ -864,7 +846,7 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
         }
         if (!item_valid(e)) break;
       }
-      const Item it = unpack_item<kWin>(e, p.part_tokens);
+      const Item it = unpack_item(e, p.part_tokens);
       // padded heads (columns past the group) get m = +inf: their scores then come out as -inf and
       // their probabilities as 0 without a test (their l and O are never stored)
 #pragma unroll
@@ -894,11 +876,7 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
           if (lane == 0) mbar_arrive(&bars.sfree[sb]);
         }
         const int rows_valid = min(kChunk, it.ntok - k * kChunk);
-        // windowed: the masked places from gap0 to gap1 - 1 of this chunk.  There are at most
-        // 126, so every chunk has a token that counts (the last one ends with the newest).
-        const int gap0 = kWin ? max(0, p.sinks - (it.t0 + k * kChunk)) : 0;
-        const int gap1 = kWin ? min(rows_valid, p.sinks + it.gap - (it.t0 + k * kChunk)) : 0;
-        const bool valid = wok && t < rows_valid && !(kWin && t >= gap0 && t < gap1);
+        const bool valid = wok && t < rows_valid;
         // Lazy rescale: the running max m of a head only has to bound its scores
         // loosely (probabilities up to 2^kSlack stay exact enough in hi + lo and
         // in fp32 sums), so it moves only when some score of the chunk exceeds it
@@ -989,17 +967,15 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
           *reinterpret_cast<uint4*>(pdst + (PG::kNP / 16 + gh) * kGB) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
         }
         // rows of the last loaded block past the context end: zero their V rows (only an
-        // item's last chunk can have them; the first warp of each quarter does it), and
-        // those of a window's gap
+        // item's last chunk can have them; the first warp of each quarter does it)
         const bool last = k == it.nchunks - 1;
-        const bool cut = kWin && gap0 < gap1;
-        if (((last && rows_valid < kChunk) || cut) && h0 == 0) {
+        if (last && rows_valid < kChunk && h0 == 0) {
           const int rows_loaded = min(kChunk, (rows_valid + p.block_size - 1) / p.block_size * p.block_size);
           // (warp-uniform) the chunk's V must have landed before its tail rows are zeroed
-          const bool v_ok = (rows_valid >= rows_loaded && !cut) ||
+          const bool v_ok = rows_valid >= rows_loaded ||
                             __all_sync(0xffffffffu, wait_role(&bars.vfull[c % kVStages], (c / kVStages) & 1,
                                                               abort_flag, p.err, p.wait_limit_ns));
-          if (v_ok && ((t >= rows_valid && t < rows_loaded) || (kWin && t >= gap0 && t < gap1))) {
+          if (v_ok && t >= rows_valid && t < rows_loaded) {
             unsigned char* vrow = smem + kOffV + (c % kVStages) * kTileBytes + (t >> 3) * kGroupBytes + (t & 7) * 128;
 #pragma unroll
             for (int q = 0; q < 8 * L::kBlocks; ++q)  // 128 bytes per 64-column block, 1 KB apart
@@ -1096,20 +1072,7 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
 constexpr int kListThreads = 1024;
 constexpr int kMaxChunkCounts = kTcMaxPartition / kChunk;
 
-// Windowed: lengths are those without the gap's blocks (p.max_parts * p.part_tokens holds the
-// longest), and lengths above the host's bound set the flag.
-template <bool kWin>
-__device__ __forceinline__ bool listed_len(const DecodeParams& p, int s, int& len, WindowView& view) {
-  const int L = p.context_lens[s];
-  len = L;
-  if (!kWin) return L >= 0 && L <= p.max_parts * p.part_tokens;
-  if (L < 0 || L > p.max_len) return false;
-  view = window_view(max(0, L - p.window), p.sinks, p.sink_blocks, p.block_size);
-  len = L - view.shift * p.block_size;
-  return true;
-}
-
-template <typename T, bool kWin>
+template <typename T>
 __global__ void __launch_bounds__(kListThreads) work_list_kernel(const __grid_constant__ DecodeParams p) {
   grid_dependents_launch();  // the decode kernel may start its prologue now
   __shared__ int hist[kMaxChunkCounts + 1];
@@ -1119,9 +1082,8 @@ __global__ void __launch_bounds__(kListThreads) work_list_kernel(const __grid_co
   for (int i = threadIdx.x; i <= kMaxChunkCounts; i += kListThreads) hist[i] = 0;
   __syncthreads();
   for (int s = threadIdx.x; s < p.num_seqs; s += kListThreads) {
-    int L;
-    WindowView view;
-    if (!listed_len<kWin>(p, s, L, view)) {
+    const int L = p.context_lens[s];
+    if (L < 0 || L > p.max_parts * p.part_tokens) {
       set_error(p.err, kErrLength);
       continue;
     }
@@ -1144,17 +1106,14 @@ __global__ void __launch_bounds__(kListThreads) work_list_kernel(const __grid_co
   }
   __syncthreads();
   for (int s = threadIdx.x; s < p.num_seqs; s += kListThreads) {
-    int L;
-    WindowView view;
-    if (!listed_len<kWin>(p, s, L, view) || L == 0) continue;
+    const int L = p.context_lens[s];
+    if (L <= 0 || L > p.max_parts * p.part_tokens) continue;
     const int nparts = (L + p.part_tokens - 1) / p.part_tokens;
     for (int part = 0; part < nparts; ++part) {
       const int t0 = part * p.part_tokens;
       const int ntok = min(p.part_tokens, L - t0);
       const int pos = atomicAdd(&next[(ntok + kChunk - 1) / kChunk], H);
-      for (int g = 0; g < H; ++g)
-        p.work_list[pos + g] = kWin ? make_int4(s | (part << 16), view.shift, g | (view.gap << 16), ntok | (nparts << 16))
-                                    : make_int4(s, g, t0, ntok | (nparts << 16));
+      for (int g = 0; g < H; ++g) p.work_list[pos + g] = make_int4(s, g, t0, ntok | (nparts << 16));
     }
   }
   // empty contexts: the neutral output, one warp per sequence
@@ -1187,26 +1146,13 @@ bool make_map(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows
   });
 }
 
-template <typename T, int D, int GM, bool kPair, bool kWin>
-cudaError_t launch_tc_w(const TcArgs& args, int grid, cudaStream_t stream) {
-  constexpr int smem = TcLayout<kPair ? 128 : D, GM>::kSmemBytes;
-  static std::atomic<unsigned long long> configured{0};  // devices whose limit is raised
-  cudaError_t e = ensure_smem_limit(decode_tc_kernel<T, D, GM, kPair, kWin>, smem, configured);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(decode_tc_kernel<T, D, GM, kPair, kWin>, grid, TcRoles<GM>::kThreads, smem, stream, args);
-}
-
 template <typename T, int D, int GM, bool kPair = false>
 cudaError_t launch_tc_t(const TcArgs& args, int grid, cudaStream_t stream) {
-  if (!args.p.window) return launch_tc_w<T, D, GM, kPair, false>(args, grid, stream);
-  if constexpr (!kPair) return launch_tc_w<T, D, GM, false, true>(args, grid, stream);
-  return cudaErrorInvalidValue;
-}
-
-template <typename T>
-cudaError_t launch_work_list(const DecodeParams& p, cudaStream_t stream) {
-  return p.window ? launch_dependent(work_list_kernel<T, true>, 1, kListThreads, 0, stream, p)
-                  : launch_dependent(work_list_kernel<T, false>, 1, kListThreads, 0, stream, p);
+  constexpr int smem = TcLayout<kPair ? 128 : D, GM>::kSmemBytes;
+  static std::atomic<unsigned long long> configured{0};  // devices whose limit is raised
+  cudaError_t e = ensure_smem_limit(decode_tc_kernel<T, D, GM, kPair>, smem, configured);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(decode_tc_kernel<T, D, GM, kPair>, grid, TcRoles<GM>::kThreads, smem, stream, args);
 }
 
 template <typename T, int D>
@@ -1248,15 +1194,13 @@ cudaError_t launch_decode_tc(const DecodeParams& p, int dtype, cudaStream_t stre
     const int sms = sm_count();
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int grid = items < sms ? items : sms;
-    cudaError_t e = launch_dependent(work_list_kernel<float, false>, 1, kListThreads, 0, stream, p);
+    cudaError_t e = launch_dependent(work_list_kernel<float>, 1, kListThreads, 0, stream, p);
     if (e != cudaSuccess || grid == 0) return e;
     return launch_decode_tc32(p, grid, stream);
   }
   TcArgs args;
   args.p = p;
-  // windowed calls keep KV heads apart: a pair's block-diagonal queries multiply one head's zeros
-  // with the other's rows, where a NaN or an infinity would reach both
-  const bool pair = !p.window && tc_heads_per_item(dtype, p.head_dim, p.num_kv_heads) == 2;
+  const bool pair = tc_heads_per_item(dtype, p.head_dim, p.num_kv_heads) == 2;
   args.p.heads_per_item = pair ? 2 : 1;
   const bool bf16 = dtype == PKV_BF16;
   const uint64_t pool_rows = static_cast<uint64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
@@ -1273,7 +1217,8 @@ cudaError_t launch_decode_tc(const DecodeParams& p, int dtype, cudaStream_t stre
   const int sms = sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   const int grid = items < sms ? items : sms;
-  cudaError_t e = bf16 ? launch_work_list<__nv_bfloat16>(args.p, stream) : launch_work_list<__half>(args.p, stream);
+  cudaError_t e = bf16 ? launch_dependent(work_list_kernel<__nv_bfloat16>, 1, kListThreads, 0, stream, args.p)
+                       : launch_dependent(work_list_kernel<__half>, 1, kListThreads, 0, stream, args.p);
   if (e != cudaSuccess || grid == 0) return e;
   return bf16 ? launch_tc_d<__nv_bfloat16>(args, grid, stream) : launch_tc_d<__half>(args, grid, stream);
 }

@@ -31,7 +31,7 @@ struct DecodeParams {
   float scale_log2;  // softmax scale * log2(e): scores live in the exp2 domain
   uint64_t wait_limit_ns;  // bound of every pipeline wait (kWaitLimitNs unless a test lowers it)
   int32_t heads_per_item;  // KV heads of one tensor-core work item: 1, or 2 (head_dim 64, paired heads)
-  int32_t window, sinks;   // windowed attention (0: every token): see window.cuh
+  int32_t window, sinks;   // windowed attention (CUDA cores, f32; 0: every token): see window.cuh
   int32_t sink_blocks, max_len;  // windowed: blocks that hold sinks; the host's bound of context_lens
 };
 
@@ -98,6 +98,27 @@ cudaError_t launch_gather(const void* k_cache, const void* v_cache, const int32_
                           int32_t num_kv_heads, int32_t block_size, int32_t row_bytes,
                           int32_t num_blocks, int* err, cudaStream_t stream);
 
+// Windowed attention of few query rows in one kernel: one new token per sequence, or a few
+// (f16/bf16, head_dim 64/128, group <= 16).
+struct WindowRowsParams {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  const int32_t* query_start;  // [S + 1]; NULL: one new token per sequence
+  void* out;
+  int* err;
+  int32_t num_seqs, num_q_heads, num_kv_heads, group, max_blocks_per_seq;
+  int32_t block_size, num_blocks, head_dim, num_query_tokens;
+  int32_t max_len, window, sinks, sink_blocks;
+  int32_t cluster;  // CTAs that share a sequence's tokens: 1, 2, 4 or 8
+  int32_t out_f32;
+  float scale_log2;
+};
+constexpr int kRowsPerGroup = 32;  // query rows (new tokens x query heads of a KV head) that share a pass over K and V
+cudaError_t launch_window_rows(const WindowRowsParams& p, int dtype, cudaStream_t stream);
+
 // ---- norms and position rotation of new tokens' queries and keys
 struct RotaryParams {
   const void* q;
@@ -117,7 +138,7 @@ struct RotaryParams {
   int64_t num_slots;
   int32_t num_tokens, num_q_heads, num_kv_heads, head_dim, block_size, rotary_dim, interleaved;
   float factor, eps;
-  int32_t tokens_per_cta;      // set by the launcher
+  int32_t warps_per_token;     // set by the launcher
 };
 cudaError_t launch_rotary(const RotaryParams& p, int dtype, cudaStream_t stream);
 

@@ -2,6 +2,7 @@
 refuse before any device work."""
 import ctypes
 import math
+import struct
 
 import numpy as np
 import pytest
@@ -60,7 +61,7 @@ STEP = 0x10000000
 
 
 def rotary(inv_freq=P, dim=64, layout=0, factor=1.0, eps=1e-6, qw=0, kw=0):
-    return ctypes.byref(pkv.Rotary(inv_freq, dim, layout, factor, eps, qw, kw))
+    return struct.pack("@PiiffPP", inv_freq, dim, layout, factor, eps, qw, kw)
 
 
 def qk(lib, q=P + STEP, qs=1024, k=P + 2 * STEP, ks=256, pos=P, tokens=5, hq=8, hkv=2, d=128, dtype=pkv.BF16, rot=None,

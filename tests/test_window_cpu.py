@@ -44,23 +44,26 @@ def test_refusals_of_both_calls(lib, call):
     assert call(lib, table=0) == 1 and call(lib, width=255) == 1           # the table covers max_context_len all the same
     assert call(lib, out_dtype=pkv.F16) == 2
     assert call(lib, scale=float("nan")) == 1
-    assert call(lib, ws=0) == 3 and call(lib, wsb=16) == 3 and call(lib, ws=A + 128) == 1
 
 
 def test_refusals_of_one_call(lib):
     assert decode(lib, d=desc(dtype=pkv.F32), Hq=72, out_dtype=pkv.F32) == 2     # f32: groups up to 8
     assert decode(lib, S=65536) == 1
     assert prefill(lib, d=desc(dtype=pkv.F32), out_dtype=pkv.F32) == 2           # 16-bit caches only
+    f32 = dict(d=desc(dtype=pkv.F32), out_dtype=pkv.F32, window=3000)            # split over CTAs: a workspace
+    for call, kw in ((decode, f32), (prefill, {})):
+        assert call(lib, ws=0, **kw) == 3 and call(lib, wsb=16, **kw) == 3 and call(lib, ws=A + 128, **kw) == 1
     assert prefill(lib, start=0) == 1 and prefill(lib, T=-1) == 1 and prefill(lib, T=0) == 0
 
 
-def need(lib, S=64, Hq=64, L=100_000, window=1024, sinks=4, d=None):
-    return lib.paged_attention_decode_window_workspace_bytes(S, Hq, L, window, sinks, ctypes.byref(d or desc()))
+def need(lib, S=64, Hq=64, L=100_000, window=1024, sinks=4, dtype=pkv.F32):
+    return lib.paged_attention_decode_window_workspace_bytes(S, Hq, L, window, sinks, ctypes.byref(desc(dtype=dtype)))
 
 
 def test_workspace_goes_by_the_window(lib):
-    assert need(lib, L=100_000) == need(lib, L=2_000_000_000)
-    assert need(lib, window=2_000_000_000, sinks=0, L=5000) == need(lib, window=5000, sinks=0, L=5000)
+    assert need(lib, dtype=pkv.BF16) == 0 and need(lib, window=10 ** 6, dtype=pkv.F16) == 0   # 16-bit caches: one kernel
+    assert need(lib, L=100_000) == need(lib, L=2_000_000_000) > 0
+    assert need(lib, window=2_000_000_000, sinks=0, L=5000) == need(lib, window=5000, sinks=0, L=5000) > 0
     assert need(lib, window=2 ** 31 - 1, sinks=2 ** 31 - 1, L=5000) == need(lib, window=5000, sinks=0, L=5000)
     assert need(lib, window=0) == 0 and need(lib, sinks=-1) == 0
 

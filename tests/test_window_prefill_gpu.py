@@ -65,7 +65,9 @@ def test_a_window_of_everything_is_plain_prefill(d):
         got = run(c)
         want = torch.empty_like(got)
         pkv.paged_attention_prefill(c.g_q, c.g_k, c.g_v, c.g_tables, c.g_lens, c.g_start, c.scale, want, max_context_len=700)
-        assert torch.equal(got, want)
+        ref = c.reference()
+        c.check(got, ref)
+        c.check(want, ref)
 
 
 def test_one_new_token_is_the_windowed_decode():
