@@ -407,18 +407,17 @@ pkv_status paged_attention_decode_window(const void* q, const void* k_cache, con
 
 /*
  * paged_attention_prefill_window -- paged_attention_prefill over windows, each new token's
- * its own (arguments, types, limits, errors and workspace as there:
- * paged_attention_prefill_workspace_bytes).  A NaN or an infinity in a V row that one of a
- * call's new tokens attends to may reach the outputs of the sequence's other new tokens
- * (they share its products); in a K row it reaches those that attend to it.
+ * its own (arguments, types, limits and errors as there; no workspace).  A NaN or an infinity
+ * in a V row that one of a call's new tokens attends to may reach the outputs of the
+ * sequence's other new tokens (they share its products); in a K row it reaches those that
+ * attend to it.
  */
 pkv_status paged_attention_prefill_window(const void* q, const void* k_cache, const void* v_cache,
                                           const int32_t* block_tables, int32_t max_blocks_per_seq,
                                           const int32_t* context_lens, const int32_t* query_start, int32_t num_seqs,
                                           int32_t num_q_heads, int32_t num_query_tokens, int32_t max_context_len,
                                           int32_t window, int32_t sinks, float scale, void* out, int32_t out_dtype,
-                                          void* workspace, size_t workspace_bytes, const pkv_cache_desc* cache,
-                                          void* stream);
+                                          const pkv_cache_desc* cache, void* stream);
 
 /* ----------------------------------------------------------------------------------
  * 4-bit caches.  The pages have no counterpart: a smaller form of the same cache, for more

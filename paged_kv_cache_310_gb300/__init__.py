@@ -142,7 +142,7 @@ def library():
             "paged_attention_decode_window": [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, ctypes.c_float, vp, i32,
                                               vp, sz, desc_p, vp],
             "paged_attention_prefill_window": [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, ctypes.c_float,
-                                               vp, i32, vp, sz, desc_p, vp],
+                                               vp, i32, desc_p, vp],
             "paged_kv_gather": [vp, vp, vp, i32, vp, i32, i32, vp, vp, desc_p, vp],
             "paged_block_swap_out": [vp, i32, vp, vp, vp, vp, desc_p, vp],
             "paged_attention_prefill": [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, i32,
@@ -813,9 +813,9 @@ def paged_kv_append_rotary(q, k, v, positions, slot_mapping, k_cache, v_cache, q
 
 # ---- sliding windows
 
-def _window_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace, *more):
+def _window_args(q, k_cache, v_cache, block_tables, context_lens, out, more):
     """Checks that both windowed calls make; (device, descriptor reference, sequences)."""
-    device = _one_device(q, k_cache, v_cache, block_tables, context_lens, out, workspace, *more)
+    device = _one_device(q, k_cache, v_cache, block_tables, context_lens, out, more)
     desc, desc_ref = _desc_of(k_cache.shape, k_cache.dtype)
     if desc.dtype == KV4:
         raise PagedKVError(2, "windows over 4-bit pools")
@@ -864,27 +864,20 @@ def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_len
 
 
 def paged_attention_prefill_window(q, k_cache, v_cache, block_tables, context_lens, query_start, scale, out, *,
-                                   window: int, sinks: int = 0, max_context_len: int | None = None,
-                                   workspace: torch.Tensor | None = None) -> torch.Tensor:
+                                   window: int, sinks: int = 0, max_context_len: int | None = None) -> torch.Tensor:
     """paged_attention_prefill with a window: the new token at position p attends to the
     positions j <= p with j > p - window or j < sinks.  Tensors as there; table entries of blocks
-    that hold no token attended to are not read.  workspace: uint8 device buffer, allocated for
-    the call when omitted."""
-    device, desc_ref, S = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace, query_start)
+    that hold no token attended to are not read.  No workspace."""
+    device, desc_ref, S = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, query_start)
     if query_start.dtype != torch.int32 or query_start.numel() != S + 1:
         raise PagedKVError(1, "query_start must be int32 [S+1]")
     T, Hq, _ = q.shape
     out_code = _dtype_code(out, "out")
     if max_context_len is None:
         max_context_len = int(context_lens.max()) if S else 0
-    lib = library()
-    need = 0
-    if workspace is None:
-        need = lib.paged_attention_prefill_workspace_bytes(S, Hq, T, desc_ref)
-    ws, ws_bytes, workspace = _scratch(workspace, need, device)
-    _call(lib.paged_attention_prefill_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+    _call(library().paged_attention_prefill_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
           block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), S, Hq, T,
-          max_context_len, window, sinks, float(scale), out.data_ptr(), out_code, ws, ws_bytes, desc_ref)
+          max_context_len, window, sinks, float(scale), out.data_ptr(), out_code, desc_ref)
     return out
 
 

@@ -377,10 +377,10 @@ pkv_status check_window(int32_t window, int32_t sinks) {
 }
 
 // CTAs that share the tokens of one of `items` (columns, KV head) in window_rows_kernel: as
-// many as the GPU holds at once (two an SM), of 64 tokens or more each.
+// many as the GPU holds at once (three an SM), of 64 tokens or more each.
 int rows_cluster(int64_t items, int64_t tokens) {
   int size = 1;
-  while (size < 8 && 2 * size * items <= 2 * 152 && tokens > 64 * size) size *= 2;
+  while (size < 8 && 2 * size * items <= 3 * 152 && tokens > 64 * size) size *= 2;
   return size;
 }
 
@@ -517,6 +517,38 @@ pkv_status decode(const DecodePlan& plan, int32_t window, int32_t sinks, const v
   return PKV_OK;
 }
 
+struct WindowPrefillPlan {
+  enum Kernel { kRows, kShared, kPairs } kernel;
+  int cluster;  // kRows
+};
+
+// Which kernel a windowed prefill takes: the one with the shortest estimate, for sequences that
+// share the new tokens out evenly (the host knows no more of them).  Fitted, within a fifth, on
+// calls of 1 to 64 sequences with 3 to 2,000 new tokens each, windows of 130 to 4,096, in us:
+//  * rows: 10 + 0.85 per 1,000 tiles of 16 tokens for 16 query rows (32 sequences of 4 new tokens,
+//    64/8 heads, D 64, window 1,024: 38 against 47 with shared tiles);
+//  * shared tiles: 12 + 2.1 a step of 128 tokens for one tile (64 sequences of 8, D 128: 100 against
+//    134 with rows, 137 with pairs);
+//  * pairs: 10 + 1.55 a step of 64 tokens for two tiles (4 sequences of 256: 74 against 93 with
+//    shared tiles, 240 with rows).
+WindowPrefillPlan plan_window_prefill(const PrefillParams& p) {
+  const int64_t S = p.num_seqs, H = p.num_kv_heads, T = p.num_query_tokens, sms = 152;
+  auto groups = [&](int64_t span) { return S * ((T + S * span - 1) / (S * span)); };
+  auto keys = [&](int64_t span) { return std::min<int64_t>(p.max_context_len, static_cast<int64_t>(p.window) + p.sinks + span); };
+  auto rounds = [&](int64_t items) { return (items + sms - 1) / sms; };
+  const int64_t per = kRowsPerGroup / p.group, tq = p.tile_tokens;
+  const int64_t row_groups = groups(per);
+  const double rows = 10. + 0.85e-3 * static_cast<double>(row_groups * H * (keys(per) / 16 + 1));
+  const double shared = 12. + 2.1 * static_cast<double>(rounds(groups(tq) * H) * (keys(tq) / 128 + 1));
+  const double pairs = 10. + 1.55 * static_cast<double>(rounds(groups(2 * tq) * H) * (keys(2 * tq) / 64 + 1));
+  WindowPrefillPlan plan{shared < pairs ? WindowPrefillPlan::kShared : WindowPrefillPlan::kPairs, 1};
+  if (rows < std::min(shared, pairs) && T / per + S <= 65535) {  // a grid's third dimension
+    plan.kernel = WindowPrefillPlan::kRows;
+    plan.cluster = rows_cluster(row_groups * H, keys(per));
+  }
+  return plan;
+}
+
 // What paged_attention_prefill and its windowed form (window > 0) share.
 pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_cache, const void* v_cache,
                    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
@@ -547,24 +579,14 @@ pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_c
   const int64_t need_blocks = (static_cast<int64_t>(max_context_len) + cache->block_size - 1) / cache->block_size;
   if (max_blocks_per_seq < need_blocks)
     return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq %d < ceil(max_context_len / block_size)", max_blocks_per_seq);
-  const size_t need = paged_attention_prefill_workspace_bytes(num_seqs, num_q_heads, num_query_tokens, cache);
-  if (!workspace || workspace_bytes < need)
-    return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
-  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (window == 0) {  // the work list
+    const size_t need = paged_attention_prefill_workspace_bytes(num_seqs, num_q_heads, num_query_tokens, cache);
+    if (!workspace || workspace_bytes < need)
+      return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  }
   int* flag = nullptr;
   if (pkv_status st = device_flag(&flag)) return st;
-  // few new tokens per sequence: passes over K and V for kRowsPerGroup query rows each
-  const int per = kRowsPerGroup / group;
-  const int64_t groups = num_query_tokens / per + static_cast<int64_t>(num_seqs);
-  if (window > 0 && groups <= 65535 && static_cast<int64_t>(num_query_tokens) * group <= 2 * kRowsPerGroup * static_cast<int64_t>(num_seqs)) {
-    WindowRowsParams p = rows_params(window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
-                                     num_seqs, num_q_heads, max_context_len, scale, out, out_dtype, cache, flag);
-    p.query_start = query_start;
-    p.num_query_tokens = num_query_tokens;
-    p.cluster = rows_cluster(groups * cache->num_kv_heads, std::min<int64_t>(max_context_len, static_cast<int64_t>(window) + sinks + per));
-    cudaError_t e = launch_window_rows(p, cache->dtype, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "windowed prefill launch");
-  }
   PrefillParams p{};
   p.q = q;
   p.k_cache = k_cache;
@@ -573,8 +595,6 @@ pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_c
   p.context_lens = context_lens;
   p.query_start = query_start;
   p.out = out;
-  p.work_count = static_cast<int*>(workspace);
-  p.work_list = reinterpret_cast<int4*>(static_cast<char*>(workspace) + 256);
   p.err = flag;
   p.num_seqs = num_seqs;
   p.num_q_heads = num_q_heads;
@@ -590,11 +610,32 @@ pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_c
   p.out_f32 = out_dtype == PKV_F32 ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = g_wait_limit_ns.load();
-  p.window = window > 0 && window > max_context_len ? std::max(max_context_len, 1) : window;
-  p.sinks = sinks < max_context_len ? sinks : max_context_len;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (window == 0) {
+    p.work_count = static_cast<int*>(workspace);
+    p.work_list = reinterpret_cast<int4*>(static_cast<char*>(workspace) + 256);
+    cudaError_t e = launch_prefill_tc(p, cache->dtype, s);
+    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "prefill launch");
+  }
+  // windowed
+  p.window = std::min(window, std::max(max_context_len, 1));
+  p.sinks = std::min(sinks, max_context_len);
   p.sink_blocks = (p.sinks - 1) / p.block_size + (p.sinks > 0);
-  cudaError_t e = launch_prefill_tc(p, cache->dtype, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "prefill launch");
+  if (window_prefill_items(p, true) > (int64_t{1} << 30))
+    return fail(PKV_ERR_UNSUPPORTED, "too many (new tokens, kv head) items");
+  const WindowPrefillPlan plan = plan_window_prefill(p);
+  cudaError_t e;
+  if (plan.kernel == WindowPrefillPlan::kRows) {
+    WindowRowsParams r = rows_params(window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                                     num_seqs, num_q_heads, max_context_len, scale, out, out_dtype, cache, flag);
+    r.query_start = query_start;
+    r.num_query_tokens = num_query_tokens;
+    r.cluster = plan.cluster;
+    e = launch_window_rows(r, cache->dtype, s);
+  } else {
+    e = launch_window_prefill(p, plan.kernel == WindowPrefillPlan::kShared, cache->dtype, s);
+  }
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "windowed prefill launch");
 }
 
 }  // namespace
@@ -650,12 +691,10 @@ pkv_status paged_attention_prefill_window(const void* q, const void* k_cache, co
                                           const int32_t* context_lens, const int32_t* query_start, int32_t num_seqs,
                                           int32_t num_q_heads, int32_t num_query_tokens, int32_t max_context_len,
                                           int32_t window, int32_t sinks, float scale, void* out, int32_t out_dtype,
-                                          void* workspace, size_t workspace_bytes, const pkv_cache_desc* cache,
-                                          void* stream) {
+                                          const pkv_cache_desc* cache, void* stream) {
   if (pkv_status st = check_window(window, sinks)) return st;
   return prefill(window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, num_seqs,
-                 num_q_heads, num_query_tokens, max_context_len, scale, out, out_dtype, workspace, workspace_bytes, cache,
-                 stream);
+                 num_q_heads, num_query_tokens, max_context_len, scale, out, out_dtype, nullptr, 0, cache, stream);
 }
 
 pkv_status paged_kv_gather(const void* k_cache, const void* v_cache, const int32_t* block_tables,

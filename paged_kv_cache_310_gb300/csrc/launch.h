@@ -58,6 +58,10 @@ struct PrefillParams {
 int prefill_tile_tokens(int group);
 size_t prefill_max_items(int num_seqs, int num_query_tokens, int num_kv_heads, int group);
 cudaError_t launch_prefill_tc(const PrefillParams& p, int dtype, cudaStream_t stream);
+// The windowed form (p.window > 0), without a work list; shared: items of one tile of
+// p.tile_tokens new tokens, whose chunks two warpgroups share; else of two tiles.
+cudaError_t launch_window_prefill(const PrefillParams& p, bool shared, int dtype, cudaStream_t stream);
+int64_t window_prefill_items(const PrefillParams& p, bool shared);
 
 // CUDA-core split-K decode (any supported dtype, head_dim 64/128, group <= 8).
 cudaError_t launch_decode_simt(const DecodeParams& p, int dtype, cudaStream_t stream);
@@ -116,7 +120,7 @@ struct WindowRowsParams {
   int32_t out_f32;
   float scale_log2;
 };
-constexpr int kRowsPerGroup = 32;  // query rows (new tokens x query heads of a KV head) that share a pass over K and V
+constexpr int kRowsPerGroup = 16;  // query rows (new tokens x query heads of a KV head) that share a pass over K and V
 cudaError_t launch_window_rows(const WindowRowsParams& p, int dtype, cudaStream_t stream);
 
 // ---- norms and position rotation of new tokens' queries and keys

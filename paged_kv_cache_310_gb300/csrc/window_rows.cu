@@ -37,8 +37,10 @@ template <int D, int NT>
 struct Rows {
   static constexpr int kCols = 8 * NT;
   static constexpr int kTileBytes = kTile * D * 2;          // K or V of a tile: 2 or 4 KB
-  static constexpr int kStages = NT > 2 ? 3 * 128 / D : D == 128 ? 2 : 3;
-  static constexpr int kCtas = NT > 2 ? 2 : D == 64 && NT == 1 ? 4 : NT == 1 ? 3 : 2;  // of an SM
+  static constexpr int kStages = D == 128 ? 2 : 3;          // 16 or 12 KB a warp
+  // CTAs of an SM, by registers and shared memory.  (Rings half as deep again and two CTAs: 14.4 us
+  // against 10.3 on 64 sequences, 64/8 heads, D 64, window 128; 90 against 88 on 128, D 128, 1,024.)
+  static constexpr int kCtas = D == 64 && NT == 1 ? 4 : 3;
   static constexpr int kRing = 2 * kStages * kTileBytes;    // of a warp
   static constexpr int kPitch = D + 4;                      // floats of a column's products
   static constexpr int kJoin = kWarps * kCols * kPitch * 4; // the warps' products, over the rings
@@ -46,7 +48,7 @@ struct Rows {
   static constexpr int kOffStats = kMain;                   // [kWarps][kCols] maxima and sums
   static constexpr int kOffFactor = kOffStats + kWarps * kCols * 8;  // [kCols][8 kWarps] factors of the parts
   static constexpr int kOffQ = kOffFactor + kCols * 8 * kWarps * 4;
-  static constexpr bool kSharedQ = NT > 2;                  // queries in shared memory, not in registers
+  static constexpr bool kSharedQ = NT > 1;                  // queries in shared memory, not in registers
   static constexpr int kBytes = kOffQ + (kSharedQ ? kCols * D * 2 : 0);
 };
 
@@ -492,7 +494,7 @@ cudaError_t launch_t(const WindowRowsParams& p, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t launch_d(const WindowRowsParams& p, cudaStream_t stream) {
-  if (p.query_start) return launch_t<T, D, 4, false>(p, stream);
+  if (p.query_start) return launch_t<T, D, 2, false>(p, stream);
   return p.group <= 8 ? launch_t<T, D, 1, true>(p, stream) : launch_t<T, D, 2, true>(p, stream);
 }
 

@@ -28,9 +28,9 @@ def decode(lib, d=None, q=A, table=A, width=256, lens=A, S=4, Hq=64, L=4096, win
 
 
 def prefill(lib, d=None, q=A, table=A, width=256, lens=A, S=4, Hq=64, L=4096, window=100, sinks=4, scale=0.1, out=A,
-            out_dtype=pkv.BF16, ws=A, wsb=1 << 40, T=100, start=A):
+            out_dtype=pkv.BF16, T=100, start=A):
     return lib.paged_attention_prefill_window(q, A, A, table, width, lens, start, S, Hq, T, L, window, sinks, scale, out,
-                                              out_dtype, ws, wsb, ctypes.byref(d or desc()), None)
+                                              out_dtype, ctypes.byref(d or desc()), None)
 
 
 @pytest.mark.parametrize("call", [decode, prefill])
@@ -51,8 +51,7 @@ def test_refusals_of_one_call(lib):
     assert decode(lib, S=65536) == 1
     assert prefill(lib, d=desc(dtype=pkv.F32), out_dtype=pkv.F32) == 2           # 16-bit caches only
     f32 = dict(d=desc(dtype=pkv.F32), out_dtype=pkv.F32, window=3000)            # split over CTAs: a workspace
-    for call, kw in ((decode, f32), (prefill, {})):
-        assert call(lib, ws=0, **kw) == 3 and call(lib, wsb=16, **kw) == 3 and call(lib, ws=A + 128, **kw) == 1
+    assert decode(lib, ws=0, **f32) == 3 and decode(lib, wsb=16, **f32) == 3 and decode(lib, ws=A + 128, **f32) == 1
     assert prefill(lib, start=0) == 1 and prefill(lib, T=-1) == 1 and prefill(lib, T=0) == 0
 
 

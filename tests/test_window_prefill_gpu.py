@@ -143,8 +143,7 @@ def test_binding_refusals():
     good = dict(q=c.g_q, k_cache=c.g_k, v_cache=c.g_v, block_tables=c.g_tables, context_lens=c.g_lens, query_start=c.g_start,
                 scale=1.0, out=torch.empty_like(c.g_q), window=3, max_context_len=100)
     for bad in (dict(query_start=c.g_start[:2]), dict(query_start=c.g_start.long()), dict(window=0), dict(sinks=-1),
-                dict(q=c.g_q.float()), dict(k_cache=c.g_k.float(), v_cache=c.g_v.float(), q=c.g_q.float()),
-                dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
+                dict(q=c.g_q.float()), dict(k_cache=c.g_k.float(), v_cache=c.g_v.float(), q=c.g_q.float())):
         with pytest.raises(pkv.PagedKVError):
             pkv.paged_attention_prefill_window(**{**good, **bad})
     assert pkv.device_error() == 0
