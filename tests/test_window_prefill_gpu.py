@@ -53,6 +53,58 @@ def test_windows_far_shorter_than_a_tile(group, window, sinks):
     c.check(run(c, "f32"))
 
 
+def kernel_of(c):
+    """Which kernel the call's estimates choose: sequences that share the new tokens out evenly."""
+    group, sms, s, t = c.hq // c.hkv, 152, len(c.lens), sum(c.new)
+    tq = 8 * (16 // group)
+    items = lambda span: s * -(-t // (s * span)) * c.hkv
+    keys = lambda span: min(c.max_len, c.window + c.sinks + span)
+    cost = dict(rows=10 + 0.85e-3 * items(16 // group) * (keys(16 // group) // 16 + 1),
+                shared=12 + 2.1 * -(-items(tq) // sms) * (keys(tq) // 128 + 1),
+                pairs=10 + 1.55 * -(-items(2 * tq) // sms) * (keys(2 * tq) // 64 + 1))
+    return min(cost, key=cost.get)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d,bs,group,hkv,lens,new,window,sinks", [
+    (128, 16, 8, 2, [1200, 40], [1000, 3], 600, 5), (128, 8, 1, 3, [3000], [2500], 900, 0), (64, 16, 4, 4, [2500], [1100], 700, 70),
+    (64, 64, 16, 2, [900, 700], [250, 201], 500, 1), (128, 32, 5, 2, [2000, 0, 1500], [600, 0, 700], 900, 33),
+    (64, 8, 7, 2, [1111], [1000], 555, 130)])
+def test_tiles_shared_by_two_warpgroups(d, bs, group, hkv, lens, new, window, sinks, dtype):
+    c = Case(314_160 + d + bs, lens, window, sinks, group * hkv, hkv, d, bs, dtype, new=new)
+    assert kernel_of(c) == "shared"
+    ref = c.reference()
+    for out_dtype in (dtype, "f32"):
+        c.check(run(c, out_dtype), ref)
+    assert pkv.device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d,bs,group,hkv,lens,new,window,sinks", [
+    (128, 16, 8, 2, [4100], [4000], 64, 5), (128, 8, 1, 12, [3000, 30], [2900, 30], 1000, 0), (64, 16, 4, 8, [2000, 1999], [1500, 1501], 300, 70),
+    (64, 64, 16, 4, [1200, 700], [1000, 650], 129, 1), (128, 32, 5, 4, [2000, 0, 1500], [1900, 0, 1400], 200, 33)])
+def test_pairs_of_tiles(d, bs, group, hkv, lens, new, window, sinks, dtype):
+    c = Case(314_170 + d + bs, lens, window, sinks, group * hkv, hkv, d, bs, dtype, new=new)
+    assert kernel_of(c) == "pairs"
+    ref = c.reference()
+    for out_dtype in (dtype, "f32"):
+        c.check(run(c, out_dtype), ref)
+    assert pkv.device_error() == 0
+
+
+@pytest.mark.parametrize("seqs", [33, 200, 1024, 1025, 2500])
+@pytest.mark.parametrize("new,window,hq,kernel", [(16, 100, 8, "shared"), (40, 40, 16, "pairs")])
+def test_many_sequences(new, window, hq, kernel, seqs):
+    # up to 32 sequences a lane knows one, up to 1,024 a lane counts up to 32, beyond nobody counts
+    gen = torch.Generator().manual_seed(314_180 + seqs)
+    lens = torch.randint(new, 70 + new, (seqs,), generator=gen).tolist()
+    new = [max(0, new - i % 5 * (i % 3)) for i in range(seqs)]
+    c = Case(314_181 + seqs, lens, window, 2, hq, 1, 64, 8, "bf16", new=new)
+    assert kernel_of(c) == kernel or seqs == 33
+    c.check(run(c))
+    assert pkv.device_error() == 0
+
+
 def test_long_contexts():
     c = Case(314_200, [20_000, 5001], 4096, 64, 16, 2, 128, 16, "bf16", new=[8, 300])
     c.check(run(c))
