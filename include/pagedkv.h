@@ -389,21 +389,17 @@ pkv_status paged_kv_append_rotary(const void* q, int64_t q_stride, const void* k
 
 /*
  * paged_attention_decode_window -- paged_attention_decode over a window.  One new token per
- * sequence, at position context_lens[s] - 1; the other arguments, types, errors and the
- * workspace's ownership as there.  16-bit caches run on tensor cores in one kernel, groups
- * up to 16, and need no workspace; f32 caches on CUDA cores, groups up to 8, fp32 throughout.
- * max_context_len: host upper bound on context_lens (a longer sequence sets the device
+ * sequence, at position context_lens[s] - 1; the other arguments, types and errors as there,
+ * groups up to 16 for every dtype, and no workspace.  16-bit caches run on tensor cores, f32
+ * caches on CUDA cores, fp32 throughout.  max_context_len: host upper bound on context_lens (a longer sequence sets the device
  * index flag, and its rows of out are left as they are).  Cost goes by the tokens attended
  * to, not by context_lens.
  */
-size_t paged_attention_decode_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
-                                                     int32_t window, int32_t sinks, const pkv_cache_desc* cache);
 pkv_status paged_attention_decode_window(const void* q, const void* k_cache, const void* v_cache,
                                          const int32_t* block_tables, int32_t max_blocks_per_seq,
                                          const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
                                          int32_t max_context_len, int32_t window, int32_t sinks, float scale, void* out,
-                                         int32_t out_dtype, void* workspace, size_t workspace_bytes,
-                                         const pkv_cache_desc* cache, void* stream);
+                                         int32_t out_dtype, const pkv_cache_desc* cache, void* stream);
 
 /*
  * paged_attention_prefill_window -- paged_attention_prefill over windows, each new token's

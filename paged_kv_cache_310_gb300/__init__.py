@@ -51,7 +51,7 @@ __all__ = [
     "paged_kv4_append", "paged_kv4_expand", "paged_attention_decode_kv4", "paged_attention_decode_kv4_workspace_bytes",
     "paged_attention_weights", "paged_attention_weights_workspace_bytes", "paged_kv_evict",
     "paged_qk_rotary", "paged_kv_append_rotary", "rotary_frequencies",
-    "paged_attention_decode_window", "paged_attention_decode_window_workspace_bytes", "paged_attention_prefill_window",
+    "paged_attention_decode_window", "paged_attention_prefill_window",
     "PreparedCall", "prepare_kv_append", "prepare_block_copy", "prepare_attention_decode", "set_wait_limit",
 ]
 
@@ -138,9 +138,8 @@ def library():
                                          ctypes.POINTER(ctypes.c_float)],
             "paged_qk_rotary": [vp, i64, vp, i64, vp, i32, i32, i32, i32, i32, vp, vp, i64, vp, i64, vp],
             "paged_kv_append_rotary": [vp, i64, vp, i64, vp, i64, vp, vp, i32, i32, vp, vp, i64, vp, vp, desc_p, vp],
-            "paged_attention_decode_window_workspace_bytes": [i32, i32, i32, i32, i32, desc_p],
             "paged_attention_decode_window": [vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, ctypes.c_float, vp, i32,
-                                              vp, sz, desc_p, vp],
+                                              desc_p, vp],
             "paged_attention_prefill_window": [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, ctypes.c_float,
                                                vp, i32, desc_p, vp],
             "paged_kv_gather": [vp, vp, vp, i32, vp, i32, i32, vp, vp, desc_p, vp],
@@ -165,7 +164,6 @@ def library():
         lib.paged_attention_workspace_bytes.restype = sz
         lib.paged_attention_no_alloc_limit.restype = sz
         lib.paged_attention_prefill_workspace_bytes.restype = sz
-        lib.paged_attention_decode_window_workspace_bytes.restype = sz
         lib.paged_attention_decode_kv4_workspace_bytes.restype = sz
         lib.paged_attention_weights_workspace_bytes.restype = sz
         lib.paged_kv_last_error.restype = ctypes.c_char_p
@@ -830,36 +828,23 @@ def _window_args(q, k_cache, v_cache, block_tables, context_lens, out, more):
     return device, desc_ref, S
 
 
-def paged_attention_decode_window_workspace_bytes(num_seqs, num_q_heads, max_context_len, window, sinks, k_cache) -> int:
-    return int(library().paged_attention_decode_window_workspace_bytes(
-        num_seqs, num_q_heads, max_context_len, window, sinks, _desc_of(k_cache.shape, k_cache.dtype)[1]))
-
-
 def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, out, *, window: int,
-                                  sinks: int = 0, max_context_len: int | None = None,
-                                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+                                  sinks: int = 0, max_context_len: int | None = None) -> torch.Tensor:
     """out[s, h] = softmax(scale * q[s, h] . K_j) V_j over the last `window` of the
     context_lens[s] tokens of s and its first `sinks`.
 
     Tensors as in paged_attention_decode; table entries of blocks that hold no such token are
     not read (-1 will do).  max_context_len: host upper bound on context_lens (computed with a
-    device sync when omitted).  workspace: uint8 device buffer of
-    paged_attention_decode_window_workspace_bytes, allocated for the call when omitted.
+    device sync when omitted).  One kernel, no workspace.
     """
-    device, desc_ref, S = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, workspace)
+    device, desc_ref, S = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, None)
     if q.shape[0] != S:
         raise PagedKVError(1, "context_lens must be [S]")
-    out_code, Hq = _dtype_code(out, "out"), q.shape[1]
     if max_context_len is None:
         max_context_len = int(context_lens.max()) if S else 0
-    lib = library()
-    need = 0
-    if workspace is None:
-        need = lib.paged_attention_decode_window_workspace_bytes(S, Hq, max_context_len, window, sinks, desc_ref)
-    ws, ws_bytes, workspace = _scratch(workspace, need, device)
-    _call(lib.paged_attention_decode_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, Hq, max_context_len, window, sinks,
-          float(scale), out.data_ptr(), out_code, ws, ws_bytes, desc_ref)
+    _call(library().paged_attention_decode_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, q.shape[1], max_context_len, window,
+          sinks, float(scale), out.data_ptr(), _dtype_code(out, "out"), desc_ref)
     return out
 
 

@@ -1,6 +1,5 @@
 // api.cu -- the extern "C" entry points of libpagedkv.so (declared in
 // include/pagedkv.h): argument checks, launch configuration, the device error flag.
-#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -85,7 +84,6 @@ struct DecodePlan {
   size_t workspace; // bytes
   size_t list_bytes;  // work list (tensor-core path): 256-byte header + entries
   size_t ml_bytes;    // partition (max, sum) pairs
-  int rows_cluster;   // windowed 16-bit caches: CTAs of window_rows_kernel per (sequence, KV head); else 0
 };
 
 int round_up(int x, int m) { return (x + m - 1) / m * m; }
@@ -149,7 +147,6 @@ pkv_status plan_decode(int32_t num_seqs, int32_t num_q_heads, int32_t max_len,
     part = max_len <= auto_part ? (max_len < 128 ? 128 : round_up(max_len, 128)) : auto_part;
   }
   plan->path = path;
-  plan->rows_cluster = 0;
   plan->part_tokens = part;
   plan->max_parts = max_len == 0 ? 1 : (max_len + part - 1) / part;
   if (path == PKV_PATH_TENSOR_CORE && plan->max_parts >= 32768)
@@ -175,6 +172,8 @@ pkv_status plan_decode(int32_t num_seqs, int32_t num_q_heads, int32_t max_len,
 }  // namespace
 
 pkv_status record_error(pkv_status status, const char* message) { return fail(status, "%s", message); }
+
+uint64_t wait_limit_ns() { return g_wait_limit_ns.load(); }
 
 }  // namespace pkv
 
@@ -356,90 +355,16 @@ size_t paged_attention_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
   return plan.workspace;
 }
 
-size_t paged_attention_prefill_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_query_tokens,
-                                               const pkv_cache_desc* cache) {
-  if (!cache || cache->num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads ||
-      num_seqs < 0 || num_query_tokens < 0)
-    return 0;
-  const int group = num_q_heads / cache->num_kv_heads;
-  if (group > 16) return 0;
-  return 256 + (prefill_max_items(num_seqs, num_query_tokens, cache->num_kv_heads, group) * 16 + 255) / 256 * 256;
-}
-
-}  // extern "C"
-
-namespace {
-
-pkv_status check_window(int32_t window, int32_t sinks) {
-  if (window < 1) return fail(PKV_ERR_INVALID_ARG, "window %d < 1", window);
-  if (sinks < 0) return fail(PKV_ERR_INVALID_ARG, "sinks %d < 0", sinks);
-  return PKV_OK;
-}
-
-// CTAs that share the tokens of one of `items` (columns, KV head) in window_rows_kernel: as
-// many as the GPU holds at once (three an SM), of 64 tokens or more each.
-int rows_cluster(int64_t items, int64_t tokens) {
-  int size = 1;
-  while (size < 8 && 2 * size * items <= 3 * 152 && tokens > 64 * size) size *= 2;
-  return size;
-}
-
-// The windowed decode's plan.  16-bit caches: one kernel, no workspace.  f32 caches: the CUDA-core
-// kernel over sequences of the tokens that it runs over at most, those of the sinks' and the
-// window's blocks: fp32 throughout, where the tf32 kernel's split operands lose 2^-21 of a score.
-pkv_status plan_window(int32_t window, int32_t sinks, int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
-                       const pkv_cache_desc* cache, DecodePlan* plan) {
-  if (pkv_status st = check_window(window, sinks)) return st;
-  if (pkv_status st = check_cache(cache)) return st;
-  const int64_t bs = cache->block_size, most = (sinks + bs - 1) / bs * bs + static_cast<int64_t>(window) + bs - 1;
-  const int32_t tokens = max_context_len < most ? max_context_len : static_cast<int32_t>(most);
-  const bool f32 = cache->dtype == PKV_F32;
-  const pkv_decode_config config = {f32 ? PKV_PATH_CUDA_CORE : PKV_PATH_TENSOR_CORE, 0};
-  if (pkv_status st = plan_decode(num_seqs, num_q_heads, tokens, cache, &config, plan)) return st;
-  if (!f32) {
-    plan->rows_cluster = rows_cluster(static_cast<int64_t>(num_seqs) * cache->num_kv_heads, tokens);
-    plan->workspace = 0;
-  }
-  return PKV_OK;
-}
-
-// What a launch of window_rows_kernel needs, from the checked arguments of either call.
-WindowRowsParams rows_params(int32_t window, int32_t sinks, const void* q, const void* k_cache, const void* v_cache,
-                             const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
-                             int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len, float scale, void* out,
-                             int32_t out_dtype, const pkv_cache_desc* cache, int* flag) {
-  WindowRowsParams p{};
-  p.q = q;
-  p.k_cache = k_cache;
-  p.v_cache = v_cache;
-  p.block_tables = block_tables;
-  p.context_lens = context_lens;
-  p.out = out;
-  p.err = flag;
-  p.num_seqs = num_seqs;
-  p.num_q_heads = num_q_heads;
-  p.num_kv_heads = cache->num_kv_heads;
-  p.group = num_q_heads / cache->num_kv_heads;
-  p.max_blocks_per_seq = max_blocks_per_seq;
-  p.block_size = cache->block_size;
-  p.num_blocks = cache->num_blocks;
-  p.head_dim = cache->head_dim;
-  p.max_len = max_context_len;
-  p.window = std::min(window, std::max(max_context_len, 1));
-  p.sinks = std::min(sinks, max_context_len);
-  p.sink_blocks = (p.sinks - 1) / p.block_size + (p.sinks > 0);
-  p.out_f32 = out_dtype == PKV_F32 ? 1 : 0;
-  p.scale_log2 = scale * 1.4426950408889634f;
-  return p;
-}
-
-// What paged_attention_decode and its windowed form share.  The plan is for the tokens that a
-// sequence's kernels run over; max_context_len bounds all that it has (window 0: the same).
-pkv_status decode(const DecodePlan& plan, int32_t window, int32_t sinks, const void* q, const void* k_cache,
-                  const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
-                  const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len, float scale,
-                  void* out, int32_t out_dtype, void* workspace, size_t workspace_bytes, const pkv_cache_desc* cache,
-                  void* stream) {
+pkv_status paged_attention_decode(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                  const int32_t* context_lens, int32_t num_seqs,
+                                  int32_t num_q_heads, int32_t max_context_len, float scale,
+                                  void* out, int32_t out_dtype, void* workspace,
+                                  size_t workspace_bytes, const pkv_cache_desc* cache,
+                                  const pkv_decode_config* config, void* stream) {
+  DecodePlan plan;
+  if (pkv_status st = plan_decode(num_seqs, num_q_heads, max_context_len, cache, config, &plan))
+    return st;
   if (num_seqs == 0) return PKV_OK;
   if (!q || !k_cache || !v_cache || !context_lens || !out)
     return fail(PKV_ERR_INVALID_ARG, "NULL pointer argument");
@@ -462,14 +387,6 @@ pkv_status decode(const DecodePlan& plan, int32_t window, int32_t sinks, const v
   }
   int* flag = nullptr;
   if (pkv_status st = device_flag(&flag)) return st;
-
-  if (plan.rows_cluster > 0) {
-    WindowRowsParams p = rows_params(window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
-                                     num_seqs, num_q_heads, max_context_len, scale, out, out_dtype, cache, flag);
-    p.cluster = plan.rows_cluster;
-    cudaError_t e = launch_window_rows(p, cache->dtype, static_cast<cudaStream_t>(stream));
-    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "windowed decode launch");
-  }
 
   DecodeParams p{};
   p.q = q;
@@ -503,10 +420,6 @@ pkv_status decode(const DecodePlan& plan, int32_t window, int32_t sinks, const v
   p.out_f32 = out_dtype == PKV_F32 ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;  // log2(e): softmax is evaluated with exp2
   p.wait_limit_ns = g_wait_limit_ns.load();
-  p.window = window > 0 && window > max_context_len ? std::max(max_context_len, 1) : window;
-  p.sinks = sinks < max_context_len ? sinks : max_context_len;
-  p.sink_blocks = (p.sinks - 1) / p.block_size + (p.sinks > 0);
-  p.max_len = max_context_len;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = plan.path == PKV_PATH_TENSOR_CORE ? launch_decode_tc(p, cache->dtype, s)
@@ -517,44 +430,22 @@ pkv_status decode(const DecodePlan& plan, int32_t window, int32_t sinks, const v
   return PKV_OK;
 }
 
-struct WindowPrefillPlan {
-  enum Kernel { kRows, kShared, kPairs } kernel;
-  int cluster;  // kRows
-};
-
-// Which kernel a windowed prefill takes: the one with the shortest estimate, for sequences that
-// share the new tokens out evenly (the host knows no more of them).  Fitted, within a fifth, on
-// calls of 1 to 64 sequences with 3 to 2,000 new tokens each, windows of 130 to 4,096, in us:
-//  * rows: 10 + 0.85 per 1,000 tiles of 16 tokens for 16 query rows (32 sequences of 4 new tokens,
-//    64/8 heads, D 64, window 1,024: 38 against 47 with shared tiles);
-//  * shared tiles: 12 + 2.1 a step of 128 tokens for one tile (64 sequences of 8, D 128: 100 against
-//    134 with rows, 137 with pairs);
-//  * pairs: 10 + 1.55 a step of 64 tokens for two tiles (4 sequences of 256: 74 against 93 with
-//    shared tiles, 240 with rows).
-WindowPrefillPlan plan_window_prefill(const PrefillParams& p) {
-  const int64_t S = p.num_seqs, H = p.num_kv_heads, T = p.num_query_tokens, sms = 152;
-  auto groups = [&](int64_t span) { return S * ((T + S * span - 1) / (S * span)); };
-  auto keys = [&](int64_t span) { return std::min<int64_t>(p.max_context_len, static_cast<int64_t>(p.window) + p.sinks + span); };
-  auto rounds = [&](int64_t items) { return (items + sms - 1) / sms; };
-  const int64_t per = kRowsPerGroup / p.group, tq = p.tile_tokens;
-  const int64_t row_groups = groups(per);
-  const double rows = 10. + 0.85e-3 * static_cast<double>(row_groups * H * (keys(per) / 16 + 1));
-  const double shared = 12. + 2.1 * static_cast<double>(rounds(groups(tq) * H) * (keys(tq) / 128 + 1));
-  const double pairs = 10. + 1.55 * static_cast<double>(rounds(groups(2 * tq) * H) * (keys(2 * tq) / 64 + 1));
-  WindowPrefillPlan plan{shared < pairs ? WindowPrefillPlan::kShared : WindowPrefillPlan::kPairs, 1};
-  if (rows < std::min(shared, pairs) && T / per + S <= 65535) {  // a grid's third dimension
-    plan.kernel = WindowPrefillPlan::kRows;
-    plan.cluster = rows_cluster(row_groups * H, keys(per));
-  }
-  return plan;
+size_t paged_attention_prefill_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_query_tokens,
+                                               const pkv_cache_desc* cache) {
+  if (!cache || cache->num_kv_heads <= 0 || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads ||
+      num_seqs < 0 || num_query_tokens < 0)
+    return 0;
+  const int group = num_q_heads / cache->num_kv_heads;
+  if (group > 16) return 0;
+  return 256 + (prefill_max_items(num_seqs, num_query_tokens, cache->num_kv_heads, group) * 16 + 255) / 256 * 256;
 }
 
-// What paged_attention_prefill and its windowed form (window > 0) share.
-pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_cache, const void* v_cache,
-                   const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
-                   const int32_t* query_start, int32_t num_seqs, int32_t num_q_heads, int32_t num_query_tokens,
-                   int32_t max_context_len, float scale, void* out, int32_t out_dtype, void* workspace,
-                   size_t workspace_bytes, const pkv_cache_desc* cache, void* stream) {
+pkv_status paged_attention_prefill(const void* q, const void* k_cache, const void* v_cache,
+                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                   const int32_t* context_lens, const int32_t* query_start, int32_t num_seqs,
+                                   int32_t num_q_heads, int32_t num_query_tokens, int32_t max_context_len,
+                                   float scale, void* out, int32_t out_dtype, void* workspace,
+                                   size_t workspace_bytes, const pkv_cache_desc* cache, void* stream) {
   if (pkv_status st = check_cache(cache)) return st;
   if (num_seqs < 0 || num_seqs > (1 << 20)) return fail(PKV_ERR_INVALID_ARG, "num_seqs %d", num_seqs);
   if (num_q_heads <= 0 || num_q_heads % cache->num_kv_heads)
@@ -579,12 +470,10 @@ pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_c
   const int64_t need_blocks = (static_cast<int64_t>(max_context_len) + cache->block_size - 1) / cache->block_size;
   if (max_blocks_per_seq < need_blocks)
     return fail(PKV_ERR_INVALID_ARG, "max_blocks_per_seq %d < ceil(max_context_len / block_size)", max_blocks_per_seq);
-  if (window == 0) {  // the work list
-    const size_t need = paged_attention_prefill_workspace_bytes(num_seqs, num_q_heads, num_query_tokens, cache);
-    if (!workspace || workspace_bytes < need)
-      return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
-    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  }
+  const size_t need = paged_attention_prefill_workspace_bytes(num_seqs, num_q_heads, num_query_tokens, cache);
+  if (!workspace || workspace_bytes < need)
+    return fail(PKV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : 0);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u) return fail(PKV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   int* flag = nullptr;
   if (pkv_status st = device_flag(&flag)) return st;
   PrefillParams p{};
@@ -595,6 +484,8 @@ pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_c
   p.context_lens = context_lens;
   p.query_start = query_start;
   p.out = out;
+  p.work_count = static_cast<int*>(workspace);
+  p.work_list = reinterpret_cast<int4*>(static_cast<char*>(workspace) + 256);
   p.err = flag;
   p.num_seqs = num_seqs;
   p.num_q_heads = num_q_heads;
@@ -610,91 +501,8 @@ pkv_status prefill(int32_t window, int32_t sinks, const void* q, const void* k_c
   p.out_f32 = out_dtype == PKV_F32 ? 1 : 0;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = g_wait_limit_ns.load();
-  const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (window == 0) {
-    p.work_count = static_cast<int*>(workspace);
-    p.work_list = reinterpret_cast<int4*>(static_cast<char*>(workspace) + 256);
-    cudaError_t e = launch_prefill_tc(p, cache->dtype, s);
-    return e == cudaSuccess ? PKV_OK : cuda_fail(e, "prefill launch");
-  }
-  // windowed
-  p.window = std::min(window, std::max(max_context_len, 1));
-  p.sinks = std::min(sinks, max_context_len);
-  p.sink_blocks = (p.sinks - 1) / p.block_size + (p.sinks > 0);
-  if (window_prefill_items(p, true) > (int64_t{1} << 30))
-    return fail(PKV_ERR_UNSUPPORTED, "too many (new tokens, kv head) items");
-  const WindowPrefillPlan plan = plan_window_prefill(p);
-  cudaError_t e;
-  if (plan.kernel == WindowPrefillPlan::kRows) {
-    WindowRowsParams r = rows_params(window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
-                                     num_seqs, num_q_heads, max_context_len, scale, out, out_dtype, cache, flag);
-    r.query_start = query_start;
-    r.num_query_tokens = num_query_tokens;
-    r.cluster = plan.cluster;
-    e = launch_window_rows(r, cache->dtype, s);
-  } else {
-    e = launch_window_prefill(p, plan.kernel == WindowPrefillPlan::kShared, cache->dtype, s);
-  }
-  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "windowed prefill launch");
-}
-
-}  // namespace
-
-extern "C" {
-
-pkv_status paged_attention_decode(const void* q, const void* k_cache, const void* v_cache,
-                                  const int32_t* block_tables, int32_t max_blocks_per_seq,
-                                  const int32_t* context_lens, int32_t num_seqs,
-                                  int32_t num_q_heads, int32_t max_context_len, float scale,
-                                  void* out, int32_t out_dtype, void* workspace,
-                                  size_t workspace_bytes, const pkv_cache_desc* cache,
-                                  const pkv_decode_config* config, void* stream) {
-  DecodePlan plan;
-  if (pkv_status st = plan_decode(num_seqs, num_q_heads, max_context_len, cache, config, &plan))
-    return st;
-  return decode(plan, 0, 0, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
-                max_context_len, scale, out, out_dtype, workspace, workspace_bytes, cache, stream);
-}
-
-pkv_status paged_attention_prefill(const void* q, const void* k_cache, const void* v_cache,
-                                   const int32_t* block_tables, int32_t max_blocks_per_seq,
-                                   const int32_t* context_lens, const int32_t* query_start, int32_t num_seqs,
-                                   int32_t num_q_heads, int32_t num_query_tokens, int32_t max_context_len,
-                                   float scale, void* out, int32_t out_dtype, void* workspace,
-                                   size_t workspace_bytes, const pkv_cache_desc* cache, void* stream) {
-  return prefill(0, 0, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, num_seqs,
-                 num_q_heads, num_query_tokens, max_context_len, scale, out, out_dtype, workspace, workspace_bytes, cache,
-                 stream);
-}
-
-size_t paged_attention_decode_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t max_context_len,
-                                                     int32_t window, int32_t sinks, const pkv_cache_desc* cache) {
-  DecodePlan plan;
-  if (plan_window(window, sinks, num_seqs, num_q_heads, max_context_len, cache, &plan) != PKV_OK) return 0;
-  return plan.workspace;
-}
-
-pkv_status paged_attention_decode_window(const void* q, const void* k_cache, const void* v_cache,
-                                         const int32_t* block_tables, int32_t max_blocks_per_seq,
-                                         const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads,
-                                         int32_t max_context_len, int32_t window, int32_t sinks, float scale, void* out,
-                                         int32_t out_dtype, void* workspace, size_t workspace_bytes,
-                                         const pkv_cache_desc* cache, void* stream) {
-  DecodePlan plan;
-  if (pkv_status st = plan_window(window, sinks, num_seqs, num_q_heads, max_context_len, cache, &plan)) return st;
-  return decode(plan, window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs,
-                num_q_heads, max_context_len, scale, out, out_dtype, workspace, workspace_bytes, cache, stream);
-}
-
-pkv_status paged_attention_prefill_window(const void* q, const void* k_cache, const void* v_cache,
-                                          const int32_t* block_tables, int32_t max_blocks_per_seq,
-                                          const int32_t* context_lens, const int32_t* query_start, int32_t num_seqs,
-                                          int32_t num_q_heads, int32_t num_query_tokens, int32_t max_context_len,
-                                          int32_t window, int32_t sinks, float scale, void* out, int32_t out_dtype,
-                                          const pkv_cache_desc* cache, void* stream) {
-  if (pkv_status st = check_window(window, sinks)) return st;
-  return prefill(window, sinks, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, query_start, num_seqs,
-                 num_q_heads, num_query_tokens, max_context_len, scale, out, out_dtype, nullptr, 0, cache, stream);
+  cudaError_t e = launch_prefill_tc(p, cache->dtype, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PKV_OK : cuda_fail(e, "prefill launch");
 }
 
 pkv_status paged_kv_gather(const void* k_cache, const void* v_cache, const int32_t* block_tables,

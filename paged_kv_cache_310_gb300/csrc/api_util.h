@@ -14,6 +14,8 @@ pkv_status fail(pkv_status st, const char* fmt, ...);
 pkv_status cuda_fail(cudaError_t e, const char* what);
 // Device address of the error flag on the current device (looked up once per device).
 pkv_status device_flag(int** out);
+// Bound of the pipeline waits of kernels launched now.
+uint64_t wait_limit_ns();
 // Checks a pool descriptor; PKV_KV4 pools only where `kv4` says the call takes them.
 pkv_status check_cache(const pkv_cache_desc* c, bool kv4 = false);
 

@@ -34,7 +34,6 @@
 
 #include "common.cuh"
 #include "launch.h"
-#include "window.cuh"
 
 namespace pkv {
 namespace {
@@ -77,20 +76,7 @@ __device__ __forceinline__ void store_out(void* out, size_t i, float x, int out_
     static_cast<T*>(out)[i] = Elem<T>::from_float(x);
 }
 
-// The length that the kernels run over, and, windowed (kWin), the blocks left out and the places
-// masked (see window.cuh); false: outside the bounds.
-template <bool kWin>
-__device__ __forceinline__ bool sequence_len(const DecodeParams& p, int s, int& len, WindowView& view) {
-  len = p.context_lens[s];
-  view.shift = view.gap = 0;
-  if (!kWin) return len >= 0 && len <= p.max_parts * p.part_tokens;
-  if (len < 0 || len > p.max_len) return false;
-  view = window_view(max(0, len - p.window), p.sinks, p.sink_blocks, p.block_size);
-  len -= view.shift * p.block_size;
-  return true;
-}
-
-template <typename T, int D, int GM, bool kWin>
+template <typename T, int D, int GM>
 __global__ void __launch_bounds__(kThreads)
 decode_simt_kernel(const __grid_constant__ DecodeParams p) {
   using C = Simt<T, D, GM>;
@@ -103,9 +89,8 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
   // with partitions the next kernel is this call's merge, which waits for this grid
   // before it reads anything: let it launch once every CTA here has started
   if (p.max_parts > 1) grid_dependents_launch();
-  int L;
-  WindowView view;
-  if (!sequence_len<kWin>(p, s, L, view)) {
+  const int L = p.context_lens[s];
+  if (L < 0 || L > p.max_parts * p.part_tokens) {
     if (part == 0 && threadIdx.x == 0) set_error(p.err, kErrLength);
     return;
   }
@@ -150,8 +135,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
     const int nblk = (ntok + bs - 1) / bs;
     const int32_t* row = p.block_tables + static_cast<size_t>(s) * p.max_blocks_per_seq;
     for (int i = lane; i < nblk; i += 32) {
-      const int at = kWin && first + i >= p.sink_blocks ? first + i + view.shift : first + i;
-      int b = at < p.max_blocks_per_seq ? row[at] : -1;
+      int b = first + i < p.max_blocks_per_seq ? row[first + i] : -1;
       if (b < 0 || b >= p.num_blocks) {
         set_error(p.err, kErrIndex);
         b = 0;  // keep the copy in bounds; the flag reports the bad table
@@ -232,8 +216,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
       for (int i = 0; i < C::kRowsPerSlot; ++i) {
         const int r = slot + i * C::kSlots;
-        const int masked = kWin ? t0 + c * C::kChunk + r - p.sinks : -1;  // place within the gap
-        const bool valid = r < rows && !(kWin && masked >= 0 && masked < view.gap);
+        const bool valid = r < rows;
         float kf[C::kVec];
         if (valid) {
           E::load16(ks + r * C::kRowBytes + li * 16, kf);
@@ -271,8 +254,7 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
       for (int i = 0; i < C::kRowsPerSlot; ++i) {
         const int r = slot + i * C::kSlots;
-        const int masked = kWin ? t0 + c * C::kChunk + r - p.sinks : -1;
-        if (r < rows && !(kWin && masked >= 0 && masked < view.gap)) {
+        if (r < rows) {
           float vf[C::kVec];
           E::load16(vs + r * C::kRowBytes + li * 16, vf);
 #pragma unroll
@@ -351,13 +333,12 @@ decode_simt_kernel(const __grid_constant__ DecodeParams p) {
 
 // One CTA per (query head, sequence), launched as a programmatic dependent of the
 // partition kernel: it may be resident while that kernel runs and waits for it here.
-template <typename T, bool kWin>
+template <typename T>
 __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ DecodeParams p) {
   grid_dependency_wait();
   const int h = blockIdx.x % p.num_q_heads, s = blockIdx.x / p.num_q_heads;
-  int L;
-  WindowView view;
-  if (!sequence_len<kWin>(p, s, L, view)) return;
+  const int L = p.context_lens[s];
+  if (L < 0 || L > p.max_parts * p.part_tokens) return;
   const int np = (L + p.part_tokens - 1) / p.part_tokens;
   if (np <= 1) return;
   const size_t row = static_cast<size_t>(s) * p.num_q_heads + h;
@@ -376,24 +357,16 @@ __global__ void __launch_bounds__(128) merge_kernel(const __grid_constant__ Deco
   }
 }
 
-template <typename T, int D, int GM, bool kWin>
-cudaError_t launch_simt_w(const DecodeParams& p, cudaStream_t stream) {
+template <typename T, int D, int GM>
+cudaError_t launch_simt_t(const DecodeParams& p, cudaStream_t stream) {
   using C = Simt<T, D, GM>;
   const size_t smem = C::smem_bytes(p.part_tokens, p.block_size);
   static std::atomic<unsigned long long> configured{0};  // devices whose limit is raised
-  cudaError_t e = ensure_smem_limit(decode_simt_kernel<T, D, GM, kWin>, 200 * 1024, configured);
+  cudaError_t e = ensure_smem_limit(decode_simt_kernel<T, D, GM>, 200 * 1024, configured);
   if (e != cudaSuccess) return e;
   dim3 grid(p.max_parts, p.num_kv_heads, p.num_seqs);
-  decode_simt_kernel<T, D, GM, kWin><<<grid, kThreads, smem, stream>>>(p);
+  decode_simt_kernel<T, D, GM><<<grid, kThreads, smem, stream>>>(p);
   return cudaGetLastError();
-}
-
-// Windowed 16-bit caches have a kernel of their own (window_rows.cu).
-template <typename T, int D, int GM>
-cudaError_t launch_simt_t(const DecodeParams& p, cudaStream_t stream) {
-  if (!p.window) return launch_simt_w<T, D, GM, false>(p, stream);
-  if constexpr (sizeof(T) == 4) return launch_simt_w<T, D, GM, true>(p, stream);
-  return cudaErrorInvalidValue;
 }
 
 template <typename T, int D>
@@ -409,14 +382,6 @@ cudaError_t launch_simt_d(const DecodeParams& p, cudaStream_t stream) {
   return p.head_dim == 64 ? launch_simt_g<T, 64>(p, stream) : launch_simt_g<T, 128>(p, stream);
 }
 
-template <typename T>
-cudaError_t launch_merge_t(const DecodeParams& p, cudaStream_t stream) {
-  const int grid = p.num_q_heads * p.num_seqs;  // (query head, sequence), head fastest
-  if (!p.window) return launch_dependent(merge_kernel<T, false>, grid, 128, 0, stream, p);
-  if constexpr (sizeof(T) == 4) return launch_dependent(merge_kernel<T, true>, grid, 128, 0, stream, p);
-  return cudaErrorInvalidValue;
-}
-
 }  // namespace
 
 cudaError_t launch_decode_simt(const DecodeParams& p, int dtype, cudaStream_t stream) {
@@ -429,10 +394,11 @@ cudaError_t launch_decode_simt(const DecodeParams& p, int dtype, cudaStream_t st
 
 cudaError_t launch_merge(const DecodeParams& p, int dtype, cudaStream_t stream) {
   if (p.max_parts <= 1) return cudaSuccess;
+  const int grid = p.num_q_heads * p.num_seqs;  // (query head, sequence), head fastest
   switch (dtype) {
-    case PKV_F32: return launch_merge_t<float>(p, stream);
-    case PKV_F16: return launch_merge_t<__half>(p, stream);
-    default: return launch_merge_t<__nv_bfloat16>(p, stream);
+    case PKV_F32: return launch_dependent(merge_kernel<float>, grid, 128, 0, stream, p);
+    case PKV_F16: return launch_dependent(merge_kernel<__half>, grid, 128, 0, stream, p);
+    default: return launch_dependent(merge_kernel<__nv_bfloat16>, grid, 128, 0, stream, p);
   }
 }
 

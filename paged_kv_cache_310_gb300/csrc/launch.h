@@ -31,8 +31,6 @@ struct DecodeParams {
   float scale_log2;  // softmax scale * log2(e): scores live in the exp2 domain
   uint64_t wait_limit_ns;  // bound of every pipeline wait (kWaitLimitNs unless a test lowers it)
   int32_t heads_per_item;  // KV heads of one tensor-core work item: 1, or 2 (head_dim 64, paired heads)
-  int32_t window, sinks;   // windowed attention (CUDA cores, f32; 0: every token): see window.cuh
-  int32_t sink_blocks, max_len;  // windowed: blocks that hold sinks; the host's bound of context_lens
 };
 
 // Multi-token causal (prefill) attention, tensor cores; f16/bf16, head_dim 64 or 128.
@@ -53,7 +51,7 @@ struct PrefillParams {
   int32_t out_f32;
   float scale_log2;
   uint64_t wait_limit_ns;  // bound of every pipeline wait (kWaitLimitNs unless a test lowers it)
-  int32_t window, sinks, sink_blocks;  // windowed attention (0: every token): see window.cuh
+  int32_t window, sinks, sink_blocks;  // the windowed form's: see window.cuh
 };
 int prefill_tile_tokens(int group);
 size_t prefill_max_items(int num_seqs, int num_query_tokens, int num_kv_heads, int group);
@@ -102,8 +100,8 @@ cudaError_t launch_gather(const void* k_cache, const void* v_cache, const int32_
                           int32_t num_kv_heads, int32_t block_size, int32_t row_bytes,
                           int32_t num_blocks, int* err, cudaStream_t stream);
 
-// Windowed attention of few query rows in one kernel: one new token per sequence, or a few
-// (f16/bf16, head_dim 64/128, group <= 16).
+// Windowed attention of few query rows in one kernel: one new token per sequence (any dtype), or a
+// few (f16/bf16); head_dim 64/128, group <= 16.
 struct WindowRowsParams {
   const void* q;
   const void* k_cache;
@@ -122,6 +120,7 @@ struct WindowRowsParams {
 };
 constexpr int kRowsPerGroup = 16;  // query rows (new tokens x query heads of a KV head) that share a pass over K and V
 cudaError_t launch_window_rows(const WindowRowsParams& p, int dtype, cudaStream_t stream);
+cudaError_t launch_window_rows_f32(const WindowRowsParams& p, cudaStream_t stream);  // one new token per sequence
 
 // ---- norms and position rotation of new tokens' queries and keys
 struct RotaryParams {

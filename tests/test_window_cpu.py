@@ -1,4 +1,4 @@
-"""The windowed calls without a GPU: workspace sizes, and what they refuse before any device work."""
+"""The windowed calls without a GPU: what they refuse before any device work."""
 import ctypes
 
 import pytest
@@ -22,9 +22,9 @@ def desc(num_blocks=64, block_size=16, num_kv_heads=8, head_dim=128, dtype=pkv.B
 
 
 def decode(lib, d=None, q=A, table=A, width=256, lens=A, S=4, Hq=64, L=4096, window=100, sinks=4, scale=0.1, out=A,
-           out_dtype=pkv.BF16, ws=A, wsb=1 << 40):
-    return lib.paged_attention_decode_window(q, A, A, table, width, lens, S, Hq, L, window, sinks, scale, out, out_dtype, ws,
-                                             wsb, ctypes.byref(d or desc()), None)
+           out_dtype=pkv.BF16):
+    return lib.paged_attention_decode_window(q, A, A, table, width, lens, S, Hq, L, window, sinks, scale, out, out_dtype,
+                                             ctypes.byref(d or desc()), None)
 
 
 def prefill(lib, d=None, q=A, table=A, width=256, lens=A, S=4, Hq=64, L=4096, window=100, sinks=4, scale=0.1, out=A,
@@ -47,24 +47,14 @@ def test_refusals_of_both_calls(lib, call):
 
 
 def test_refusals_of_one_call(lib):
-    assert decode(lib, d=desc(dtype=pkv.F32), Hq=72, out_dtype=pkv.F32) == 2     # f32: groups up to 8
     assert decode(lib, S=65536) == 1
+    assert decode(lib, d=desc(dtype=pkv.F32), out_dtype=pkv.BF16) == 2           # the cache's dtype or f32
     assert prefill(lib, d=desc(dtype=pkv.F32), out_dtype=pkv.F32) == 2           # 16-bit caches only
-    f32 = dict(d=desc(dtype=pkv.F32), out_dtype=pkv.F32, window=3000)            # split over CTAs: a workspace
-    assert decode(lib, ws=0, **f32) == 3 and decode(lib, wsb=16, **f32) == 3 and decode(lib, ws=A + 128, **f32) == 1
+    assert prefill(lib, d=desc(num_kv_heads=4096), Hq=4096) == 2
+    assert prefill(lib, d=desc(num_blocks=1 << 24)) == 2                         # rows past 32-bit coordinates
     assert prefill(lib, start=0) == 1 and prefill(lib, T=-1) == 1 and prefill(lib, T=0) == 0
-
-
-def need(lib, S=64, Hq=64, L=100_000, window=1024, sinks=4, dtype=pkv.F32):
-    return lib.paged_attention_decode_window_workspace_bytes(S, Hq, L, window, sinks, ctypes.byref(desc(dtype=dtype)))
-
-
-def test_workspace_goes_by_the_window(lib):
-    assert need(lib, dtype=pkv.BF16) == 0 and need(lib, window=10 ** 6, dtype=pkv.F16) == 0   # 16-bit caches: one kernel
-    assert need(lib, L=100_000) == need(lib, L=2_000_000_000) > 0
-    assert need(lib, window=2_000_000_000, sinks=0, L=5000) == need(lib, window=5000, sinks=0, L=5000) > 0
-    assert need(lib, window=2 ** 31 - 1, sinks=2 ** 31 - 1, L=5000) == need(lib, window=5000, sinks=0, L=5000)
-    assert need(lib, window=0) == 0 and need(lib, sinks=-1) == 0
+    assert prefill(lib, S=1 << 20, T=1 << 30, Hq=1024, d=desc(num_kv_heads=1024)) == 2  # more items than are counted
+    assert prefill(lib, S=(1 << 20) + 1) == 1
 
 
 def test_binding_refusals_without_a_gpu(lib):
