@@ -495,6 +495,7 @@ def paged_kv_gather(k_cache, v_cache, block_tables, context_lens, k_out, v_out, 
 # are short on the GPU, so the binding passes plain integers and asks PyTorch little.
 
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # handle alone: 2 us less than the Stream object
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device  # CUDA is up: there are tensors on it
 
 
 def _one_device(first, *rest) -> int:
@@ -511,7 +512,7 @@ def _one_device(first, *rest) -> int:
 def _call(fn, device: int, *args) -> None:
     """fn(*args, stream) with `device` current, on that device's current stream."""
     stream = _raw_stream(device) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
-    if device == torch.cuda.current_device():
+    if device == _get_device():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
@@ -723,13 +724,17 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str |
 
 def _token_rows(t, what, dtype, device, tokens, head_dim):
     """(address, token stride, heads) of a [T, H, head_dim] tensor whose tokens may lie apart."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[0] != tokens or shape[2] != head_dim or t.dtype is not dtype or t.get_device() != device:
+    if t.dim() != 3 or t.dtype is not dtype or t.get_device() != device:
         raise PagedKVError(1, f"{what} must be [T, heads, {head_dim}] of one dtype on one CUDA device")
-    heads = shape[1]
-    if stride[2] != 1 or (stride[1] != head_dim and heads > 1):
+    n, heads, d = t.shape
+    if n != tokens or d != head_dim:
+        raise PagedKVError(1, f"{what} must be [T, heads, {head_dim}]")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * d, heads
+    apart, head, one = t.stride()
+    if one != 1 or (head != d and heads > 1):
         raise PagedKVError(1, f"{what}: the heads of a token must lie one after the other")
-    return t.data_ptr(), stride[0] if tokens > 1 else heads * head_dim, heads
+    return t.data_ptr(), apart if n > 1 else heads * d, heads
 
 
 _pack_rotary = struct.Struct("@PiiffPP").pack  # pkv_rotary, field by field: quicker than a ctypes.Structure
@@ -812,20 +817,22 @@ def paged_kv_append_rotary(q, k, v, positions, slot_mapping, k_cache, v_cache, q
 # ---- sliding windows
 
 def _window_args(q, k_cache, v_cache, block_tables, context_lens, out, more):
-    """Checks that both windowed calls make; (device, descriptor reference, sequences)."""
+    """Checks that both windowed calls make; (device, descriptor reference, out's dtype code,
+    rows and heads of q, sequences, table width)."""
     device = _one_device(q, k_cache, v_cache, block_tables, context_lens, out, more)
-    desc, desc_ref = _desc_of(k_cache.shape, k_cache.dtype)
+    dtype, pool, rows, tables = k_cache.dtype, k_cache.shape, q.shape, block_tables.shape
+    desc, desc_ref = _desc_of(pool, dtype)
     if desc.dtype == KV4:
         raise PagedKVError(2, "windows over 4-bit pools")
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    if block_tables.dtype is not torch.int32 or context_lens.dtype is not torch.int32:
         raise PagedKVError(1, "block_tables and context_lens must be int32")
-    if q.dim() != 3 or out.shape != q.shape or q.dtype != k_cache.dtype or q.shape[2] != desc.head_dim \
-            or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    if len(rows) != 3 or rows[2] != desc.head_dim or out.shape != rows or q.dtype is not dtype or v_cache.dtype is not dtype \
+            or v_cache.shape != pool:
         raise PagedKVError(1, "shape/dtype mismatch between q, out and the caches")
     S = context_lens.numel()
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
+    if len(tables) != 2 or tables[0] != S:
         raise PagedKVError(1, "block_tables must be [S, max_blocks]")
-    return device, desc_ref, S
+    return device, desc_ref, _dtype_code(out, "out"), rows[0], rows[1], S, tables[1]
 
 
 def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, out, *, window: int,
@@ -837,14 +844,14 @@ def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_len
     not read (-1 will do).  max_context_len: host upper bound on context_lens (computed with a
     device sync when omitted).  One kernel, no workspace.
     """
-    device, desc_ref, S = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, None)
-    if q.shape[0] != S:
+    device, desc_ref, out_code, T, Hq, S, width = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, None)
+    if T != S:
         raise PagedKVError(1, "context_lens must be [S]")
     if max_context_len is None:
         max_context_len = int(context_lens.max()) if S else 0
     _call(library().paged_attention_decode_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), S, q.shape[1], max_context_len, window,
-          sinks, float(scale), out.data_ptr(), _dtype_code(out, "out"), desc_ref)
+          block_tables.data_ptr(), width, context_lens.data_ptr(), S, Hq, max_context_len, window, sinks, float(scale),
+          out.data_ptr(), out_code, desc_ref)
     return out
 
 
@@ -853,16 +860,14 @@ def paged_attention_prefill_window(q, k_cache, v_cache, block_tables, context_le
     """paged_attention_prefill with a window: the new token at position p attends to the
     positions j <= p with j > p - window or j < sinks.  Tensors as there; table entries of blocks
     that hold no token attended to are not read.  No workspace."""
-    device, desc_ref, S = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, query_start)
-    if query_start.dtype != torch.int32 or query_start.numel() != S + 1:
+    device, desc_ref, out_code, T, Hq, S, width = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, query_start)
+    if query_start.dtype is not torch.int32 or query_start.numel() != S + 1:
         raise PagedKVError(1, "query_start must be int32 [S+1]")
-    T, Hq, _ = q.shape
-    out_code = _dtype_code(out, "out")
     if max_context_len is None:
         max_context_len = int(context_lens.max()) if S else 0
     _call(library().paged_attention_prefill_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), query_start.data_ptr(), S, Hq, T,
-          max_context_len, window, sinks, float(scale), out.data_ptr(), out_code, desc_ref)
+          block_tables.data_ptr(), width, context_lens.data_ptr(), query_start.data_ptr(), S, Hq, T, max_context_len, window,
+          sinks, float(scale), out.data_ptr(), out_code, desc_ref)
     return out
 
 
