@@ -390,10 +390,11 @@ pkv_status paged_kv_append_rotary(const void* q, int64_t q_stride, const void* k
 /*
  * paged_attention_decode_window -- paged_attention_decode over a window.  One new token per
  * sequence, at position context_lens[s] - 1; the other arguments, types and errors as there,
- * groups up to 16 for every dtype, and no workspace.  16-bit caches run on tensor cores, f32
- * caches on CUDA cores, fp32 throughout.  max_context_len: host upper bound on context_lens (a longer sequence sets the device
- * index flag, and its rows of out are left as they are).  Cost goes by the tokens attended
- * to, not by context_lens.
+ * groups up to 16 for every dtype, one kernel, no workspace.  16-bit caches run on tensor
+ * cores, their weights in two 16-bit parts; f32 caches on CUDA cores, fp32 throughout.
+ * max_context_len: host upper bound on context_lens, at most 2^30 (a longer sequence sets the
+ * device index flag, and its rows of out are left as they are).  Cost goes by the tokens
+ * attended to, not by context_lens.
  */
 pkv_status paged_attention_decode_window(const void* q, const void* k_cache, const void* v_cache,
                                          const int32_t* block_tables, int32_t max_blocks_per_seq,

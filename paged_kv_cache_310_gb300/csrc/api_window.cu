@@ -37,6 +37,9 @@ pkv_status check_sizes(const Args& a) {
   if (a.num_q_heads / a.cache->num_kv_heads > kMaxGroup)
     return fail(PKV_ERR_UNSUPPORTED, "query-head groups of %d (at most %d)", a.num_q_heads / a.cache->num_kv_heads, kMaxGroup);
   if (a.num_query_tokens < 0 || a.max_context_len < 0) return fail(PKV_ERR_INVALID_ARG, "negative size");
+  if (a.max_context_len > (1 << 30)) return fail(PKV_ERR_UNSUPPORTED, "max_context_len %d above 2^30", a.max_context_len);
+  if (static_cast<int64_t>(a.num_query_tokens) * a.num_q_heads > INT32_MAX)
+    return fail(PKV_ERR_UNSUPPORTED, "more than 2^31 - 1 query rows");
   return PKV_OK;
 }
 
