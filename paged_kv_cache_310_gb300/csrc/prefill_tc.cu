@@ -303,14 +303,14 @@ struct CursorOf<Mode::kPlain> {
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
 // Extreme of a row's 64 raw scores (maximum, or minimum when the scale is negative),
-// keys past `lim` -- windowed: those without a bit in `seen` -- excluded when the mask cuts
-// the row's chunk (overwritten in place with the neutral value).
-template <bool kMin, bool kWin>
-__device__ __forceinline__ float chunk_extreme(float* sv, bool diagonal, int lim, uint64_t seen) {
+// keys past `lim` excluded when the chunk crosses the diagonal (overwritten in place
+// with the neutral value).
+template <bool kMin>
+__device__ __forceinline__ float chunk_extreme(float* sv, bool diagonal, int lim) {
   constexpr float kNone = kMin ? INFINITY : -INFINITY;
   if (diagonal) {
 #pragma unroll
-    for (int i = 0; i < 64; ++i) sv[i] = (kWin ? (seen >> i & 1) != 0 : i <= lim) ? sv[i] : kNone;
+    for (int i = 0; i < 64; ++i) sv[i] = i <= lim ? sv[i] : kNone;
   }
   float e0 = kNone, e1 = kNone;
 #pragma unroll
@@ -319,6 +319,30 @@ __device__ __forceinline__ float chunk_extreme(float* sv, bool diagonal, int lim
     e1 = kMin ? fmin3(e1, sv[i + 2], sv[i + 3]) : fmax3(e1, sv[i + 2], sv[i + 3]);
   }
   return kMin ? fminf(e0, e1) : fmaxf(e0, e1);
+}
+
+// Windowed: a row's 64 scores times the scale, in place; where the mask cuts the chunk, keys
+// without a bit in `seen` become -inf, so that their weights come out as 0 without another test.
+// Returns the maximum.
+__device__ __forceinline__ float scaled_maximum(float* sv, float2 scale, bool cut, uint64_t seen) {
+#pragma unroll
+  for (int i = 0; i < 64; i += 2) {
+    const float2 x = __fmul2_rn(make_float2(sv[i], sv[i + 1]), scale);
+    sv[i] = x.x;
+    sv[i + 1] = x.y;
+  }
+  if (cut) {
+    const uint32_t low = static_cast<uint32_t>(seen), high = static_cast<uint32_t>(seen >> 32);
+#pragma unroll
+    for (int i = 0; i < 64; ++i) sv[i] = ((i < 32 ? low : high) & (1u << (i % 32))) ? sv[i] : -INFINITY;
+  }
+  float e0 = -INFINITY, e1 = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < 64; i += 4) {
+    e0 = fmax3(e0, sv[i], sv[i + 1]);
+    e1 = fmax3(e1, sv[i + 2], sv[i + 3]);
+  }
+  return fmaxf(e0, e1);
 }
 
 // One producer warp's copies of an item's chunks of K (or V) into its ring: per chunk
@@ -729,9 +753,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         // pass 1: the row's chunk maximum of scale * score under the mask
         if (!kShared || !idle) {
           tmem_load64(sbuf, sv);
-          cm = (neg_scale ? chunk_extreme<true, kWin>(sv, diagonal, lim, seen)
-                          : chunk_extreme<false, kWin>(sv, diagonal, lim, seen)) * p.scale_log2;
-          if (kWin && seen == 0) cm = -INFINITY;  // whatever the scale
+          if (kWin) cm = scaled_maximum(sv, sc2, diagonal, seen);
+          else cm = (neg_scale ? chunk_extreme<true>(sv, diagonal, lim) : chunk_extreme<false>(sv, diagonal, lim)) * p.scale_log2;
         }
         // lazy rescale: keep m unless the chunk brings a score more than the slack above
         // (a chunk that the mask leaves nothing of gives cm = -inf and changes nothing)
@@ -775,19 +798,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         // came from: [hi of 16 keys | lo of 16 keys]
         if (!kShared || !idle) {
           float2 acc = make_float2(0.f, 0.f);
-          const float used = kWin && m == -INFINITY ? 0.f : m;  // nothing seen yet: every p is masked
+          const float used = kWin && m == -INFINITY ? 0.f : m;  // nothing seen yet: every score is -inf
           const float2 nm2 = make_float2(-used, -used);
 #pragma unroll
           for (int q = 0; q < kKC / 16; ++q) {
             uint32_t w[16];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float2 x = __ffma2_rn(make_float2(sv[q * 16 + 2 * i], sv[q * 16 + 2 * i + 1]), sc2, nm2);
+              const float2 s = make_float2(sv[q * 16 + 2 * i], sv[q * 16 + 2 * i + 1]);
+              const float2 x = kWin ? __fadd2_rn(s, nm2) : __ffma2_rn(s, sc2, nm2);
               float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
-              if (diagonal) {
-                const int i0 = q * 16 + 2 * i;
-                p0 = (kWin ? (seen >> i0 & 1) != 0 : i0 <= lim) ? p0 : 0.f;
-                p1 = (kWin ? (seen >> (i0 + 1) & 1) != 0 : i0 + 1 <= lim) ? p1 : 0.f;
+              if (!kWin && diagonal) {
+                p0 = q * 16 + 2 * i <= lim ? p0 : 0.f;
+                p1 = q * 16 + 2 * i + 1 <= lim ? p1 : 0.f;
               }
               const float2 pr = make_float2(p0, p1);
               float h0, h1;
