@@ -146,8 +146,8 @@ struct PrefillPlan {
 // Which kernel a windowed prefill takes: the one with the shortest estimate, for sequences that
 // share the new tokens out evenly (the host knows no more of them).  Fitted, within a fifth, on
 // calls of 1 to 64 sequences with 3 to 2,000 new tokens each, windows of 130 to 4,096, in us:
-//  * rows: 10 + 0.85 per 1,000 tiles of 16 tokens for 16 query rows (32 sequences of 4 new tokens,
-//    64/8 heads, D 64, window 1,024: 38 against 47 with shared tiles);
+//  * rows: 10 + 0.85 (D 128) or 0.65 (D 64) per 1,000 tiles of 16 tokens for 16 query rows (32
+//    sequences of 4 new tokens, 64/8 heads, D 64, window 1,024: 30 against 47 with shared tiles);
 //  * shared tiles: 12 + 2.1 a step of 128 tokens for one tile (64 sequences of 8, D 128: 100 against
 //    134 with rows, 137 with pairs);
 //  * pairs: 10 + 1.55 a step of 64 tokens for two tiles (4 sequences of 256: 74 against 93 with
@@ -159,7 +159,7 @@ PrefillPlan plan_prefill(const Args& a) {
   auto rounds = [&](int64_t items) { return (items + kSms - 1) / kSms; };
   const int64_t per = kRowsPerGroup / group, tq = prefill_tile_tokens(group);
   const int64_t row_groups = groups(per);
-  const double rows = 10. + 0.85e-3 * static_cast<double>(row_groups * H * (keys_of(a, per) / 16 + 1));
+  const double rows = 10. + (a.cache->head_dim == 64 ? 0.65e-3 : 0.85e-3) * static_cast<double>(row_groups * H * (keys_of(a, per) / 16 + 1));
   const double shared = 12. + 2.1 * static_cast<double>(rounds(groups(tq) * H) * (keys_of(a, tq) / 128 + 1));
   const double pairs = 10. + 1.55 * static_cast<double>(rounds(groups(2 * tq) * H) * (keys_of(a, 2 * tq) / 64 + 1));
   PrefillPlan plan{shared < pairs ? PrefillPlan::kShared : PrefillPlan::kPairs, 1};

@@ -28,8 +28,9 @@ struct Rows {
   static constexpr int kCols = 8 * NT;
   static constexpr int kStages = D == 128 ? 2 : 3;          // 16 or 12 KB a warp
   // CTAs of an SM, by registers and shared memory.  (Rings half as deep again and two CTAs: 14.4 us
-  // against 10.3 on 64 sequences, 64/8 heads, D 64, window 128; 90 against 88 on 128, D 128, 1,024.)
-  static constexpr int kCtas = D == 64 && NT == 1 ? 4 : 3;
+  // against 10.3 on 64 sequences, 64/8 heads, D 64, window 128; 90 against 88 on 128, D 128, 1,024.
+  // Three instead of four at D 64 with 16 columns: 38 against 31 on 64 sequences, 128/8 heads, 1,024.)
+  static constexpr int kCtas = D == 64 ? 4 : 3;
   static constexpr int kRing = 2 * kStages * kTile * D * 2;  // of a warp
   static constexpr int kPitch = D + 4;                      // floats of a column's products
   static constexpr int kJoin = kWarps * kCols * kPitch * 4; // the warps' products, over the rings

@@ -59,7 +59,7 @@ def kernel_of(c):
     tq = 8 * (16 // group)
     items = lambda span: s * -(-t // (s * span)) * c.hkv
     keys = lambda span: min(c.max_len, c.window + c.sinks + span)
-    cost = dict(rows=10 + 0.85e-3 * items(16 // group) * (keys(16 // group) // 16 + 1),
+    cost = dict(rows=10 + (0.65e-3 if c.d == 64 else 0.85e-3) * items(16 // group) * (keys(16 // group) // 16 + 1),
                 shared=12 + 2.1 * -(-items(tq) // sms) * (keys(tq) // 128 + 1),
                 pairs=10 + 1.55 * -(-items(2 * tq) // sms) * (keys(2 * tq) // 64 + 1))
     return min(cost, key=cost.get)
