@@ -62,8 +62,8 @@
  *    for f16/bf16 and up to 8 for f32 (tf32 MMAs on split operands: scores to about
  *    2^-21 relative, within the f32 tolerance for logits of a few units; for logits
  *    of tens of units choose PKV_PATH_CUDA_CORE, fp32 throughout); prefill on tensor
- *    cores for f16/bf16, groups up to 16.  4-bit pools (PKV_KV4) and eviction have their
- *    own calls below; block copies and swaps take 4-bit pools too.
+ *    cores for f16/bf16, groups up to 16.  4-bit pools (PKV_KV4), eviction, rotary positions and
+ *    sliding windows have their own calls below; block copies and swaps take 4-bit pools too.
  */
 #ifndef PAGEDKV_H
 #define PAGEDKV_H

@@ -92,8 +92,8 @@ WindowRowsParams rows_params(const Args& a, int cluster, int* flag) {
   return p;
 }
 
-PrefillParams prefill_params(const Args& a) {
-  PrefillParams p{};
+WindowPrefillParams prefill_params(const Args& a) {
+  WindowPrefillParams p{};
   p.q = a.q;
   p.k_cache = a.k_cache;
   p.v_cache = a.v_cache;
@@ -212,7 +212,7 @@ pkv_status paged_attention_prefill_window(const void* q, const void* k_cache, co
   if (pkv_status st = check_pointers(a)) return st;
   if (static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size > (int64_t{1} << 30))
     return fail(PKV_ERR_UNSUPPORTED, "pool too large for 32-bit row coordinates");
-  PrefillParams p = prefill_params(a);
+  WindowPrefillParams p = prefill_params(a);
   if (window_prefill_items(p, true) > (int64_t{1} << 30))
     return fail(PKV_ERR_UNSUPPORTED, "too many (new tokens, KV head) items");
   if (pkv_status st = device_flag(&p.err)) return st;

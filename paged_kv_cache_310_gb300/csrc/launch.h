@@ -51,15 +51,17 @@ struct PrefillParams {
   int32_t out_f32;
   float scale_log2;
   uint64_t wait_limit_ns;  // bound of every pipeline wait (kWaitLimitNs unless a test lowers it)
-  int32_t window, sinks, sink_blocks;  // the windowed form's: see window.cuh
 };
 int prefill_tile_tokens(int group);
 size_t prefill_max_items(int num_seqs, int num_query_tokens, int num_kv_heads, int group);
 cudaError_t launch_prefill_tc(const PrefillParams& p, int dtype, cudaStream_t stream);
-// The windowed form (p.window > 0), without a work list; shared: items of one tile of
-// p.tile_tokens new tokens, whose chunks two warpgroups share; else of two tiles.
-cudaError_t launch_window_prefill(const PrefillParams& p, bool shared, int dtype, cudaStream_t stream);
-int64_t window_prefill_items(const PrefillParams& p, bool shared);
+// The windowed form, without a work list; shared: items of one tile of p.tile_tokens new tokens,
+// whose chunks two warpgroups share; else of two tiles.
+struct WindowPrefillParams : PrefillParams {
+  int32_t window, sinks, sink_blocks;  // see window.cuh
+};
+cudaError_t launch_window_prefill(const WindowPrefillParams& p, bool shared, int dtype, cudaStream_t stream);
+int64_t window_prefill_items(const WindowPrefillParams& p, bool shared);
 
 // CUDA-core split-K decode (any supported dtype, head_dim 64/128, group <= 8).
 cudaError_t launch_decode_simt(const DecodeParams& p, int dtype, cudaStream_t stream);

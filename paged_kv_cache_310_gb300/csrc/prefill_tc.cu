@@ -44,14 +44,6 @@
 //    once PV(c) has been issued).  The whole warp runs it with warp-uniform control
 //    flow; one batched barrier probe per chunk covers everything it needs, and one
 //    elected lane issues.
-//
-// Windowed calls (Mode::kWindow, kShared; see window.cuh) run over an item's sinks and window as
-// one sequence and mask the rest.  A window bounds what an item costs, so there is no work list:
-// item i is pair i / Hkv of the batch for KV head i % Hkv (WindowCursor), dealt out in turn, where
-// the list kernel took 20 us for 2,300 new tokens.  In Mode::kShared an item is one tile and both
-// softmax warpgroups work on it, each on every other chunk, with sums and O of its own that are
-// joined at the item's end: half the steps for tiles that have no partner (a few new tokens per
-// sequence), twice the items for short batches.
 #include <climits>
 #include <type_traits>
 
@@ -59,7 +51,6 @@
 #include "launch.h"
 #include "tc_util.cuh"
 #include "tcgen05.cuh"
-#include "window.cuh"
 
 namespace pkv {
 namespace {
@@ -79,49 +70,40 @@ constexpr int kMaxBuckets = 1024;          // chunk-count buckets of the work li
 // measured 5 % slower).
 constexpr int kQBufs = 2;
 
-// kPlain: every token up to its own, work from a list; kWindow, kShared: windowed, see above.
-enum class Mode { kPlain, kWindow, kShared };
-
 // Shared-memory layout for head_dim D (64 or 128): K, V and Q tiles as [8-row group]
 // [64-column block][8 rows][128 B], 128-byte swizzled.
-template <int D, Mode kMode>
+template <int D>
 struct PfLayout {
-  static constexpr bool kShared = kMode == Mode::kShared;
   static constexpr int kBlocks = D / 64;                  // 64-column blocks of a row
   static constexpr int kGroup = 8 * D * 2;                // one 8-row group: all its blocks
   static constexpr int kKVTile = kKC * D * 2;             // K (or V) of one chunk: 8 or 16 KB
-  // stages per ring (K and V have one each); shared tiles: two steps of two chunks
-  static constexpr int kStages = kShared ? 4 : (kQBufs == 2 ? 3 : 5) * 128 / D;
+  static constexpr int kStages = (kQBufs == 2 ? 3 : 5) * 128 / D;  // per ring (K and V have one each)
   static constexpr int kQBytes = kRows * D * 2;           // one tile's queries: 16 or 32 KB
-  static constexpr int kQItem = (kShared ? 1 : kGroups) * kQBytes;  // an item's tiles
+  static constexpr int kQItem = kGroups * kQBytes;        // both tiles of an item
   static constexpr int kOffV = kStages * kKVTile;
   static constexpr int kOffQ = 2 * kStages * kKVTile;
   static constexpr int kOffBar = kOffQ + kQBufs * kQItem;
   // K ring full/empty, V ring full/empty, qfull[2], qempty[2], then per tile: sfull[2],
   // pfull[2], pvdone[2]; drain
-  // shared tiles: joined halves full, empty
-  static constexpr int kNumBars = 4 * kStages + 4 + kGroups * 6 + 3;
+  static constexpr int kNumBars = 4 * kStages + 4 + kGroups * 6 + 1;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  // shared tiles: the second warpgroup's O on its way to the first, 64 dimensions at a time, and
-  // its rows' maxima and sums
-  static constexpr int kOffJoin = (kOffMisc + 64 + 127) / 128 * 128;
-  static constexpr int kSmemBytes = kShared ? kOffJoin + kRows * (64 + 2) * 4 : kOffMisc + 64;
+  static constexpr int kSmemBytes = kOffMisc + 64;
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
   static_assert(kOffQ % 1024 == 0 && kSmemBytes <= 232448, "shared memory");
 };
 
 struct Bars {
-  uint64_t *kfull, *kempty, *vfull, *vempty, *qfull, *qempty, *grp, *drain, *jfull, *jempty;
+  uint64_t *kfull, *kempty, *vfull, *vempty, *qfull, *qempty, *grp, *drain;
   // per tile g (addresses computed, so a runtime tile index needs no local-memory table)
   __device__ __forceinline__ uint64_t* sfull(int g, int i) const { return grp + 6 * g + i; }
   __device__ __forceinline__ uint64_t* pfull(int g, int i) const { return grp + 6 * g + 2 + i; }
   __device__ __forceinline__ uint64_t* pvdone(int g, int i) const { return grp + 6 * g + 4 + i; }
 };
 
-template <typename L>
+template <int D>
 __device__ __forceinline__ Bars carve(unsigned char* smem) {
-  constexpr int kStages = L::kStages;
-  uint64_t* b = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  constexpr int kStages = PfLayout<D>::kStages;
+  uint64_t* b = reinterpret_cast<uint64_t*>(smem + PfLayout<D>::kOffBar);
   Bars r;
   r.kfull = b;
   r.kempty = b + kStages;
@@ -131,8 +113,6 @@ __device__ __forceinline__ Bars carve(unsigned char* smem) {
   r.qempty = r.qfull + 2;
   r.grp = r.qempty + 2;
   r.drain = r.grp + 6 * kGroups;
-  r.jfull = r.drain + 1;
-  r.jempty = r.jfull + 1;
   return r;
 }
 
@@ -146,15 +126,10 @@ struct PrefillArgs {
 // {s, g | ntile_a << 12 | ntile_b << 20, first query token of tile a, position of that token}
 struct Item {
   int s, g, na, nb, qrow0, pos0, last, nchunks;  // na, nb: tokens in tile a, tile b
-  int shift, gap;  // windowed: blocks left out, masked places from `sinks` on
   __device__ __forceinline__ int ntok(int tile) const { return tile ? nb : na; }
 };
 
-// Windowed: positions are places (see window.cuh) of the item's first token's view.
-template <Mode kMode>
-__device__ __forceinline__ Item unpack_item(int4 e, const PrefillParams& p) {
-  constexpr bool kWin = kMode != Mode::kPlain;
-  const int tq = p.tile_tokens;
+__device__ __forceinline__ Item unpack_item(int4 e, int tq) {
   Item t;
   t.s = e.x;
   t.g = e.y & 0xfff;
@@ -162,145 +137,10 @@ __device__ __forceinline__ Item unpack_item(int4 e, const PrefillParams& p) {
   t.nb = (static_cast<unsigned>(e.y) >> 20) & 0xff;
   t.qrow0 = e.z;
   t.pos0 = e.w;
-  t.shift = t.gap = 0;
-  if (kWin) {
-    const WindowView v = window_view(max(0, t.pos0 - p.window + 1), p.sinks, p.sink_blocks, p.block_size);
-    t.shift = v.shift;
-    t.gap = v.gap;
-    t.pos0 -= v.shift * p.block_size;
-  }
   t.last = t.pos0 + (t.nb ? tq + t.nb : t.na) - 1;  // position of the pair's last token
   t.nchunks = (t.last + kKC) / kKC;
-  if (kMode == Mode::kShared) t.nchunks = (t.nchunks + 1) / 2 * 2;  // steps of two; the odd one's is masked
   return t;
 }
-
-// Windowed: this CTA's items without a list, one after the other from blockIdx.x on in steps of
-// the grid.  The batch's new tokens go in groups of a `span` (the tokens of an item), a
-// sequence's after the one before's; item i is group i / Hkv for KV head i % Hkv.  Up to 1024
-// sequences a warp counts their groups, 32 shares of up to 32 sequences, and finds a group's share
-// and then its sequence by a vote each (shares of one stay in the lanes' registers).  Beyond, where there are many more items than CTAs anyway,
-// group z is group z - base(s) of sequence s, base(s) = query_start[s] / span + s: bases rise
-// by at least a sequence's groups, and some numbers have no group.  (Always numbering so left
-// up to half of the CTAs idle on 128 items: 80 us against 43.)  A warp's lanes call together.
-struct WindowCursor {
-  const PrefillParams* p;
-  int count, k, idx, span;
-  int share, before, upto;  // sequences of a lane's share, groups before it and up to its end (share 0: not counted)
-  int lane_q0, lane_n, lane_len;  // shares of one sequence: its first new token, new tokens, length
-  int4 cur;
-
-  __device__ __forceinline__ int groups(int s) const {
-    return max(0, (p->query_start[s + 1] - p->query_start[s] + span - 1) / span);
-  }
-  // the sum of v over the lanes up to this one
-  __device__ static __forceinline__ int sum_upto(int v) {
-    const int lane = threadIdx.x % 32;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, v, off);
-      if (lane >= off) v += u;
-    }
-    return v;
-  }
-  // the entry of item i: no tokens in tile a where there are none
-  __device__ __forceinline__ int4 entry(int item) const {
-    const int lane = threadIdx.x % 32, H = p->num_kv_heads, z = item / H, g = item - z * H, S = p->num_seqs;
-    int s, t0, q0, n, L;
-    if (share == 1) {
-      s = __popc(__ballot_sync(0xffffffffu, upto <= z)) & 31;
-      t0 = (z - __shfl_sync(0xffffffffu, before, s)) * span;
-      q0 = __shfl_sync(0xffffffffu, lane_q0, s);
-      n = __shfl_sync(0xffffffffu, lane_n, s);
-      L = __shfl_sync(0xffffffffu, lane_len, s);
-    } else if (share > 0) {
-      const int j = __popc(__ballot_sync(0xffffffffu, upto <= z));
-      const int rest = z - __shfl_sync(0xffffffffu, before, j & 31);
-      const int at = j * share + lane, mine = lane < share && at < S ? groups(at) : 0, sum = sum_upto(mine);
-      const int i = __popc(__ballot_sync(0xffffffffu, sum <= rest)) & 31;
-      s = j * share + i;
-      t0 = (rest - __shfl_sync(0xffffffffu, sum - mine, i)) * span;
-    } else {
-      int hi = S - 1;
-      s = 0;
-      while (s < hi) {
-        const int mid = (s + hi + 1) / 2;
-        if (p->query_start[mid] / span + mid <= z) s = mid;
-        else hi = mid - 1;
-      }
-      t0 = (z - p->query_start[s] / span - s) * span;
-    }
-    if (share != 1) {
-      q0 = p->query_start[s];
-      n = p->query_start[s + 1] - q0;
-      L = p->context_lens[s];
-    }
-    if (t0 < 0 || t0 >= n || !sequence_ok(*p, q0, n, L)) return make_int4(0, 0, 0, 0);
-    const int tq = p->tile_tokens;
-    const int na = min(tq, n - t0), nb = span > tq ? max(0, min(tq, n - t0 - tq)) : 0;
-    return make_int4(s, g | (na << 12) | (nb << 20), q0 + t0, L - n + t0);
-  }
-  __device__ static __forceinline__ bool sequence_ok(const PrefillParams& p, int q0, int n, int L) {
-    return q0 >= 0 && n >= 0 && n <= p.num_query_tokens - q0 && L >= n && L <= p.max_context_len;
-  }
-  // from item idx on, the first that has tokens
-  __device__ __forceinline__ void settle() {
-    for (; idx < count; idx += gridDim.x) {
-      cur = entry(idx);
-      if (cur.y >> 12) break;
-    }
-  }
-  __device__ __forceinline__ void init(const PrefillParams& params, int span_) {
-    p = &params;
-    span = span_;
-    const int S = p->num_seqs;
-    share = S <= 1024 ? (S + 31) / 32 : 0;
-    if (share > 0) {
-      const int first = static_cast<int>(threadIdx.x % 32) * share;
-      int mine = 0;
-      if (share == 1) {
-        lane_q0 = first < S ? p->query_start[first] : 0;
-        lane_n = first < S ? p->query_start[first + 1] - lane_q0 : 0;
-        lane_len = first < S ? p->context_lens[first] : 0;
-        mine = max(0, (lane_n + span - 1) / span);
-      } else {
-        for (int s = first; s < min(S, first + share); ++s) mine += groups(s);
-      }
-      upto = sum_upto(mine);
-      before = upto - mine;
-      count = __shfl_sync(0xffffffffu, upto, 31) * p->num_kv_heads;
-    } else {
-      count = (p->num_query_tokens / span + S) * p->num_kv_heads;
-    }
-    k = 0;
-    idx = blockIdx.x;
-    settle();
-  }
-  __device__ __forceinline__ bool valid() const { return idx < count; }
-  __device__ __forceinline__ void advance() {
-    ++k;
-    idx += gridDim.x;
-    settle();
-  }
-};
-
-template <Mode kMode>
-struct CursorOf {
-  using type = WindowCursor;
-  __device__ static __forceinline__ void init(type& c, const PrefillParams& p, int) {
-    c.init(p, (kMode == Mode::kShared ? 1 : kGroups) * p.tile_tokens);
-  }
-};
-template <>
-struct CursorOf<Mode::kPlain> {
-  using type = ItemCursor;
-  __device__ static __forceinline__ void init(type& c, const PrefillParams& p, int num_items) {
-    c.init(p.work_list, num_items);
-  }
-};
-
-// The lowest n bits (none below 0, all from 64 on).
-__device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
 // Extreme of a row's 64 raw scores (maximum, or minimum when the scale is negative),
 // keys past `lim` excluded when the chunk crosses the diagonal (overwritten in place
@@ -321,39 +161,14 @@ __device__ __forceinline__ float chunk_extreme(float* sv, bool diagonal, int lim
   return kMin ? fminf(e0, e1) : fmaxf(e0, e1);
 }
 
-// Windowed: a row's 64 scores times the scale, in place; where the mask cuts the chunk, keys
-// without a bit in `seen` become -inf, so that their weights come out as 0 without another test.
-// Returns the maximum.
-__device__ __forceinline__ float scaled_maximum(float* sv, float2 scale, bool cut, uint64_t seen) {
-#pragma unroll
-  for (int i = 0; i < 64; i += 2) {
-    const float2 x = __fmul2_rn(make_float2(sv[i], sv[i + 1]), scale);
-    sv[i] = x.x;
-    sv[i + 1] = x.y;
-  }
-  if (cut) {
-    const uint32_t low = static_cast<uint32_t>(seen), high = static_cast<uint32_t>(seen >> 32);
-#pragma unroll
-    for (int i = 0; i < 64; ++i) sv[i] = ((i < 32 ? low : high) & (1u << (i % 32))) ? sv[i] : -INFINITY;
-  }
-  float e0 = -INFINITY, e1 = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < 64; i += 4) {
-    e0 = fmax3(e0, sv[i], sv[i + 1]);
-    e1 = fmax3(e1, sv[i + 2], sv[i + 3]);
-  }
-  return fmaxf(e0, e1);
-}
-
 // One producer warp's copies of an item's chunks of K (or V) into its ring: per chunk
 // one 4-D box per block (blocks past the pair's last position from outside the tensor:
 // zero fill).  `c` counts the warp's chunks over all items.  Returns false on abort.
-template <int D, Mode kMode>
+template <int D>
 __device__ __forceinline__ bool load_chunks(const PrefillParams& p, const Item& it, const CUtensorMap* map,
                                             unsigned char* ring, uint64_t* full, uint64_t* empty, int& c,
                                             int* issued_slot, uint64_t policy, volatile int* abort_flag) {
-  constexpr int kStages = PfLayout<D, kMode>::kStages, kKVTile = PfLayout<D, kMode>::kKVTile;
-  constexpr bool kWin = kMode != Mode::kPlain;
+  constexpr int kStages = PfLayout<D>::kStages, kKVTile = PfLayout<D>::kKVTile;
   const int lane = threadIdx.x % 32;
   const int bs = p.block_size;
   const int blocks_per_chunk = kKC / bs;
@@ -363,8 +178,7 @@ __device__ __forceinline__ bool load_chunks(const PrefillParams& p, const Item& 
     const int st = c % kStages;
     const int lb = k * blocks_per_chunk + lane;  // logical block of this lane
     const bool live = lane < blocks_per_chunk && lb * bs <= it.last;
-    const int tb = kWin && lb >= p.sink_blocks ? lb + it.shift : lb;  // its table entry
-    int b = live ? (tb < p.max_blocks_per_seq ? table[tb] : -1) : 0;
+    int b = live ? (lb < p.max_blocks_per_seq ? table[lb] : -1) : 0;
     bool ok = true;
     if (lane == 0) {
       ok = c < kStages || wait_role(&empty[st], ((c / kStages) - 1) & 1, abort_flag, p.err, p.wait_limit_ns);
@@ -388,24 +202,23 @@ __device__ __forceinline__ bool load_chunks(const PrefillParams& p, const Item& 
   return true;
 }
 
-template <typename T, int D, Mode kMode>
+template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_constant__ PrefillArgs a) {
-  using L = PfLayout<D, kMode>;
-  using Cursor = typename CursorOf<kMode>::type;
-  constexpr bool kWin = kMode != Mode::kPlain, kShared = kMode == Mode::kShared;
+  using L = PfLayout<D>;
   constexpr int kStages = L::kStages, kGroup = L::kGroup, kKVTile = L::kKVTile;
   constexpr int kQBytes = L::kQBytes, kQItem = L::kQItem, kOffV = L::kOffV, kOffQ = L::kOffQ;
   constexpr int kOffMisc = L::kOffMisc;
   extern __shared__ __align__(1024) unsigned char smem[];
   const PrefillParams& p = a.p;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const Bars bars = carve<L>(smem);
+  const Bars bars = carve<D>(smem);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
   int* kissued_slot = reinterpret_cast<int*>(smem + kOffMisc + 8);
   int* vissued_slot = reinterpret_cast<int*>(smem + kOffMisc + 12);
   int* qissued_slot = reinterpret_cast<int*>(smem + kOffMisc + 16);
   const int G = p.group, TQ = p.tile_tokens;
+  const int num_items = *p.work_count;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -425,10 +238,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         mbar_init(bars.pvdone(g, i), 1);
       }
     }
-    if (kShared) {
-      mbar_init(bars.jfull, 4);
-      mbar_init(bars.jempty, 4);
-    }
     *abort_flag = 0;
     *kissued_slot = 0;
     *vissued_slot = 0;
@@ -440,12 +249,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // windowed: launched while the kernel before may still run; everything above touches this CTA alone
-  if (kWin) {
-    grid_dependency_wait();
-    grid_dependents_launch();
-  }
-  const int num_items = kWin ? 0 : *p.work_count;
 
   if (warp == kProducerWarp) {
     // ============================ producer: Q and K ============================
@@ -460,9 +263,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     const int qhead = qrows / TQ, qtok = qrows % TQ;
     int c = 0, j = 0;
     bool ok = true;
-    Cursor cur;
-    for (CursorOf<kMode>::init(cur, p, num_items); cur.valid() && ok; cur.advance(), ++j) {
-      const Item it = unpack_item<kMode>(cur.cur, p);
+    ItemCursor cur;
+    for (cur.init(p.work_list, num_items); cur.valid() && ok; cur.advance(), ++j) {
+      const Item it = unpack_item(cur.cur, TQ);
       // ---- both tiles' queries into buffer j % kQBufs (free once item j - kQBufs's QKs completed) ----
       const int qb = j % kQBufs;
       if (lane == 0) {
@@ -474,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       __syncwarp();
       if (lane < 16 * L::kBlocks) {
 #pragma unroll
-        for (int g = 0; g < (kShared ? 1 : kGroups); ++g) {
+        for (int g = 0; g < kGroups; ++g) {
           // padding groups (past the G heads) read tokens outside the tensor: zeros
           const int tok = qhead < G ? it.qrow0 + g * TQ + qtok : p.num_query_tokens;
           const int head = it.g * G + min(qhead, G - 1);
@@ -484,23 +287,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       }
       if (lane == 0) *qissued_slot = j + 1;
       // ---- K chunks (a stage is free once both tiles' QKs of its chunk completed) ----
-      ok = load_chunks<D, kMode>(p, it, &a.tk, smem, bars.kfull, bars.kempty, c, kissued_slot, pol_kv, abort_flag);
+      ok = load_chunks<D>(p, it, &a.tk, smem, bars.kfull, bars.kempty, c, kissued_slot, pol_kv, abort_flag);
     }
   } else if (warp == kVWarp) {
     // ============================ producer: V ============================
     if (lane == 0) prefetch_tensormap(&a.tv);
-    if (kWin) {  // sequences out of bounds are skipped; this flags them
-      for (int s = blockIdx.x * 32 + lane; s < p.num_seqs; s += gridDim.x * 32)
-        if (!WindowCursor::sequence_ok(p, p.query_start[s], p.query_start[s + 1] - p.query_start[s], p.context_lens[s]))
-          set_error(p.err, kErrLength);
-    }
     const uint64_t pol_kv = policy_evict_normal();
     int c = 0;
     bool ok = true;
-    Cursor cur;
-    for (CursorOf<kMode>::init(cur, p, num_items); cur.valid() && ok; cur.advance()) {
+    ItemCursor cur;
+    for (cur.init(p.work_list, num_items); cur.valid() && ok; cur.advance()) {
       // a stage is free once both tiles' PVs of its chunk completed
-      ok = load_chunks<D, kMode>(p, unpack_item<kMode>(cur.cur, p), &a.tv, smem + kOffV, bars.vfull, bars.vempty, c,
+      ok = load_chunks<D>(p, unpack_item(cur.cur, TQ), &a.tv, smem + kOffV, bars.vfull, bars.vempty, c,
                           vissued_slot, pol_kv, abort_flag);
     }
   } else if (warp == kMmaWarp) {
@@ -520,16 +318,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       return __all_sync(0xffffffffu, wait_role(bar, parity, abort_flag, p.err, p.wait_limit_ns));
     };
     // QK side: next chunk qc (global), its stage / phase, its place in the item
-    // (shared tiles: a step has a chunk for each warpgroup, in stages qst and qst + 1; chunks,
-    // items' counts and the stages' turns below are then in steps)
-    constexpr int kPer = kShared ? 2 : 1;  // chunks, and stages, of a step
-    auto steps_of = [&](const Cursor& c) { return c.valid() ? unpack_item<kMode>(c.cur, p).nchunks / kPer : 0; };
-    Cursor qcur;
-    CursorOf<kMode>::init(qcur, p, num_items);
-    int qc = 0, qst = 0, qph = 0, qk = 0, qn = steps_of(qcur);
+    ItemCursor qcur;
+    qcur.init(p.work_list, num_items);
+    int qc = 0, qst = 0, qph = 0, qk = 0, qn = qcur.valid() ? unpack_item(qcur.cur, TQ).nchunks : 0;
     // PV side
-    Cursor pcur;
-    CursorOf<kMode>::init(pcur, p, num_items);
+    ItemCursor pcur;
+    pcur.init(p.work_list, num_items);
     int pc = 0, pst = 0, pph = 0, pk = 0, pn = qn;
     bool ok = true;
     // QK of chunk qc for both tiles (k_seen: its K stage was already seen landed)
@@ -537,7 +331,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       const int qj = qcur.k, qb = qj % kQBufs, sb = qc & 1;
       if (qk == 0 && !wait_all(&bars.qfull[qb], (qj / kQBufs) & 1)) return false;
       if (!k_seen && !wait_all(&bars.kfull[qst], qph)) return false;
-      if (kShared && !wait_all(&bars.kfull[qst + 1], qph)) return false;
       const bool last = qk == qn - 1;
       const uint64_t dk = dk0 + ((qst * kKVTile) >> 4);
       const uint64_t dqb = dq0 + ((qb * kQItem) >> 4);
@@ -545,30 +338,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       if (elect_one()) {
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-          const uint64_t dq = dqb + (kShared ? 0 : (g * kQBytes) >> 4);
-          const uint64_t dkg = dk + (kShared ? (g * kKVTile) >> 4 : 0);
+          const uint64_t dq = dqb + ((g * kQBytes) >> 4);
           const uint32_t d = tmem + g * 256 + sb * 64;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
-            mma_f16(d, dq + off, dkg + off, idesc_qk, kk > 0);
+            mma_f16(d, dq + off, dk + off, idesc_qk, kk > 0);
           }
           mma_commit(bars.sfull(g, sb));
-          if (kShared) mma_commit(&bars.kempty[qst + g]);
         }
-        if (!kShared) mma_commit(&bars.kempty[qst]);  // both tiles' QKs of this chunk
+        mma_commit(&bars.kempty[qst]);       // both tiles' QKs of this chunk
         if (last) mma_commit(&bars.qempty[qb]);  // both tiles are done with the item's queries
       }
       __syncwarp();
       ++qc;
-      if ((qst += kPer) == kStages) {
+      if (++qst == kStages) {
         qst = 0;
         qph ^= 1;
       }
       if (++qk == qn) {
         qk = 0;
         qcur.advance();
-        qn = steps_of(qcur);
+        qn = qcur.valid() ? unpack_item(qcur.cur, TQ).nchunks : 0;
       }
       return true;
     };
@@ -582,7 +373,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
           mbar_test_wait4(&bars.vfull[pst], pph, bars.pfull(0, sb), (pc >> 1) & 1, bars.pfull(1, sb),
                           (pc >> 1) & 1, &bars.kfull[qst], qph), 0);
       if (!(seen & 1) && !wait_all(&bars.vfull[pst], pph)) break;
-      if (kShared && !wait_all(&bars.vfull[pst + 1], pph)) break;
       const uint64_t dv = dv0 + ((pst * kKVTile) >> 4);
       const bool acc0 = pk > 0;
 #pragma unroll
@@ -597,26 +387,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
           const uint32_t od = tmem + g * 256 + 128;
 #pragma unroll
           for (int kk = 0; kk < kKC / 16; ++kk) {
-            const uint64_t bd = dv + (((kShared ? g * kKVTile : 0) + kk * 2 * kGroup) >> 4);
+            const uint64_t bd = dv + ((kk * 2 * kGroup) >> 4);
             mma_f16_tmem_a(od, pa + kk * 16, bd, idesc_pv, acc0 || kk > 0);
             mma_f16_tmem_a(od, pa + kk * 16 + 8, bd, idesc_pv, true);
           }
           mma_commit(bars.pvdone(g, sb));
-          if (kShared) mma_commit(&bars.vempty[pst + g]);
-          else if (g == kGroups - 1) mma_commit(&bars.vempty[pst]);  // every tile's PV of this chunk
+          if (g == kGroups - 1) mma_commit(&bars.vempty[pst]);  // every tile's PV of this chunk
         }
         __syncwarp();
       }
       if (!ok) break;
       ++pc;
-      if ((pst += kPer) == kStages) {
+      if (++pst == kStages) {
         pst = 0;
         pph ^= 1;
       }
       if (++pk == pn) {
         pk = 0;
         pcur.advance();
-        pn = steps_of(pcur);
+        pn = pcur.valid() ? unpack_item(pcur.cur, TQ).nchunks : 0;
       }
       if (qcur.valid()) ok = qk_pair((seen & 8u) != 0);
     }
@@ -635,104 +424,48 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
     int c = 0;
     bool ok = true;
     int prev_row = -1, prev_c = -1;
-    float prev_l = 1.f, prev_m = 0.f;
-    int joins = 0;  // shared tiles: hand-overs so far
-    // this row's O, 16 vectors, the i-th at i ^ (t & 7): eight rows at once lie in different banks
-    float4* join = reinterpret_cast<float4*>(smem + L::kOffJoin) + t * 16;
-    float* join_stats = reinterpret_cast<float*>(smem + L::kOffJoin) + kRows * 64 + 2 * t;
+    float prev_l = 1.f;
 
     // Warp-uniform: has this tile's PV of chunk cc completed?
     auto pv_done = [&](int cc) -> bool {
       return __all_sync(0xffffffffu, wait_role(bars.pvdone(grp, cc & 1), (cc >> 1) & 1, abort_flag, p.err, p.wait_limit_ns));
     };
-    // 32 of a finished row's values from dimension q * 32 on, times inv, to its output.
-    auto store_row = [&](int row, int q, const float* o, float inv) {
-      if (p.out_f32) {
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + static_cast<size_t>(row) * D + q * 32);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
-      } else {
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + static_cast<size_t>(row) * D + q * 32);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          dst[i] = make_uint4(pack2<T>(o[8 * i] * inv, o[8 * i + 1] * inv),
-                              pack2<T>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
-                              pack2<T>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
-                              pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
-      }
-    };
-    // A finished item's output rows: O / l (O is final: its last PV was waited for).  Shared
-    // tiles: the second warpgroup hands its rows' O, maxima and sums to the first, which joins
-    // the two.  False: a wait ran out.
-    auto finish = [&](int row, float lsum, float top) -> bool {
+    // A finished item's output rows: O / l (O is final: its last PV was waited for).
+    auto finish = [&](int row, float lsum) {
       tc_fence_after();
-      if constexpr (kShared) {
-#pragma unroll 1
-        for (int h = 0; h < D / 64; ++h, ++joins) {
-          if (grp == 1) {
-            if (joins > 0 && !__all_sync(0xffffffffu, wait_role(bars.jempty, (joins - 1) & 1, abort_flag, p.err, p.wait_limit_ns)))
-              return false;
-            join_stats[0] = top;
-            join_stats[1] = lsum;
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-              float o[32];
-              tmem_load32(obuf + h * 64 + q * 32, o);
+      const float inv = 1.f / lsum;
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                join[(8 * q + i) ^ (t & 7)] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.jfull);
+      for (int q = 0; q < D / 32; ++q) {
+        float o[32];
+        tmem_load32(obuf + q * 32, o);
+        if (row >= 0) {
+          if (p.out_f32) {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + static_cast<size_t>(row) * D + q * 32);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(o[4 * i] * inv, o[4 * i + 1] * inv, o[4 * i + 2] * inv, o[4 * i + 3] * inv);
           } else {
-            if (!__all_sync(0xffffffffu, wait_role(bars.jfull, joins & 1, abort_flag, p.err, p.wait_limit_ns))) return false;
-            // a half that saw none of a row's keys has a maximum of -inf, a sum of 0 and an O of 0
-            const float most = fmaxf(top, join_stats[0]);
-            const float mine = lsum == 0.f ? 0.f : exp2f(top - most), theirs = join_stats[1] == 0.f ? 0.f : exp2f(join_stats[0] - most);
-            const float inv = 1.f / (mine * lsum + theirs * join_stats[1]);
-#pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-              float o[32];
-              tmem_load32(obuf + h * 64 + q * 32, o);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + static_cast<size_t>(row) * D + q * 32);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float4 b = join[(8 * q + i) ^ (t & 7)];
-                o[4 * i] = fmaf(theirs, b.x, mine * o[4 * i]);
-                o[4 * i + 1] = fmaf(theirs, b.y, mine * o[4 * i + 1]);
-                o[4 * i + 2] = fmaf(theirs, b.z, mine * o[4 * i + 2]);
-                o[4 * i + 3] = fmaf(theirs, b.w, mine * o[4 * i + 3]);
-              }
-              if (row >= 0) store_row(row, 2 * h + q, o, inv);
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bars.jempty);
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack2<T>(o[8 * i] * inv, o[8 * i + 1] * inv),
+                                  pack2<T>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                  pack2<T>(o[8 * i + 4] * inv, o[8 * i + 5] * inv),
+                                  pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
           }
-        }
-      } else {
-        const float inv = 1.f / lsum;
-#pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          float o[32];
-          tmem_load32(obuf + q * 32, o);
-          if (row >= 0) store_row(row, q, o, inv);
         }
       }
       tc_fence_before();
-      return true;
     };
 
-    Cursor cur;
-    for (CursorOf<kMode>::init(cur, p, num_items); cur.valid() && ok; cur.advance()) {
-      const Item it = unpack_item<kMode>(cur.cur, p);
-      const int tile = kShared ? 0 : grp;
-      const bool row_valid = head < G && tok < it.ntok(tile);
-      const int qpos = row_valid ? it.pos0 + tile * TQ + tok : it.last;  // padding rows act as the last token
-      const int out_row = row_valid ? (it.qrow0 + tile * TQ + tok) * p.num_q_heads + it.g * G + head : -1;
-      // shared tiles: a warp of padding rows has no scores to weigh (its rows of O are never read)
-      const bool idle = kShared && !__any_sync(0xffffffffu, row_valid);
-      float m = kWin ? -INFINITY : 0.f, l = 0.f;  // max used for this row's probabilities, running row sum
-      for (int k = 0; k < it.nchunks / (kShared ? 2 : 1); ++k, ++c) {
+    ItemCursor cur;
+    for (cur.init(p.work_list, num_items); cur.valid() && ok; cur.advance()) {
+      const Item it = unpack_item(cur.cur, TQ);
+      const bool row_valid = head < G && tok < it.ntok(grp);
+      const int qpos = row_valid ? it.pos0 + grp * TQ + tok : it.last;  // padding rows act as the last token
+      const int out_row = row_valid ? (it.qrow0 + grp * TQ + tok) * p.num_q_heads + it.g * G + head : -1;
+      float m = 0.f, l = 0.f;  // max used for this row's probabilities, running row sum
+      for (int k = 0; k < it.nchunks; ++k, ++c) {
         const int sb = c & 1;
         const uint32_t sbuf = lane_base + sb * 64;
         if (!__all_sync(0xffffffffu, wait_role(bars.sfull(grp, sb), (c >> 1) & 1, abort_flag, p.err, p.wait_limit_ns))) {
@@ -740,29 +473,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
           break;
         }
         tc_fence_after();
-        const int kbase = (kShared ? 2 * k + grp : k) * kKC;
-        // the chunk's stage in the V ring, and the turn of it
-        const int vst = kShared ? 2 * (c & 1) + grp : c % kStages, vturn = kShared ? (c >> 1) & 1 : (c / kStages) & 1;
+        const int kbase = k * kKC;
         const int lim = qpos - kbase;            // keys of the chunk past lim are masked
-        // windowed: so are those before its window, but for the sinks
-        const int low = kWin ? lim - p.window + 1 : 0, sink = kWin ? p.sinks - kbase : 0;
-        const bool diagonal = lim < kKC - 1 || (kWin && low > max(0, sink));  // only then does the mask cut this row
-        const uint64_t seen = kWin ? low_bits(lim + 1) & (~low_bits(low) | low_bits(sink)) : 0;
+        const bool diagonal = lim < kKC - 1;     // only then does the mask cut this row
         // the row's 64 scores, held in registers for both passes
-        float sv[64], cm = -INFINITY;
+        float sv[64];
+        tmem_load64(sbuf, sv);
         // pass 1: the row's chunk maximum of scale * score under the mask
-        if (!kShared || !idle) {
-          tmem_load64(sbuf, sv);
-          if (kWin) cm = scaled_maximum(sv, sc2, diagonal, seen);
-          else cm = (neg_scale ? chunk_extreme<true>(sv, diagonal, lim) : chunk_extreme<false>(sv, diagonal, lim)) * p.scale_log2;
-        }
+        const float cm = (neg_scale ? chunk_extreme<true>(sv, diagonal, lim)
+                                    : chunk_extreme<false>(sv, diagonal, lim)) * p.scale_log2;
         // lazy rescale: keep m unless the chunk brings a score more than the slack above
-        // (a chunk that the mask leaves nothing of gives cm = -inf and changes nothing)
+        // (a chunk entirely past this row's position gives cm = -inf and changes nothing)
         float alpha = 1.f;
-        if (kWin ? m == -INFINITY : k == 0) {
-          // key 0 is never masked: finite.  Windowed, rows whose window starts in a later
-          // chunk stay at -inf until then, with sums and O of zero that need no rescale.
-          m = cm;
+        if (k == 0) {
+          m = cm;  // key 0 is never masked: finite
         } else if (cm > m + kRescaleSlack) {
           alpha = exp2f(m - cm);
           m = cm;
@@ -775,8 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
             ok = false;
             break;
           }
-          ok = finish(prev_row, prev_l, prev_m);
-          if (!ok) break;
+          finish(prev_row, prev_l);
           prev_c = -1;
         }
         if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -796,52 +519,44 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
         }
         // pass 2: probabilities as hi + lo parts, written over the 16 S columns they
         // came from: [hi of 16 keys | lo of 16 keys]
-        if (!kShared || !idle) {
-          float2 acc = make_float2(0.f, 0.f);
-          const float used = kWin && m == -INFINITY ? 0.f : m;  // nothing seen yet: every score is -inf
-          const float2 nm2 = make_float2(-used, -used);
+        float2 acc = make_float2(0.f, 0.f);
+        const float2 nm2 = make_float2(-m, -m);
 #pragma unroll
-          for (int q = 0; q < kKC / 16; ++q) {
-            uint32_t w[16];
+        for (int q = 0; q < kKC / 16; ++q) {
+          uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 s = make_float2(sv[q * 16 + 2 * i], sv[q * 16 + 2 * i + 1]);
-              const float2 x = kWin ? __fadd2_rn(s, nm2) : __ffma2_rn(s, sc2, nm2);
-              float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
-              if (!kWin && diagonal) {
-                p0 = q * 16 + 2 * i <= lim ? p0 : 0.f;
-                p1 = q * 16 + 2 * i + 1 <= lim ? p1 : 0.f;
-              }
-              const float2 pr = make_float2(p0, p1);
-              float h0, h1;
-              w[i] = pack2_split<T>(p0, p1, h0, h1);                               // rounded pair
-              const float2 lo = __ffma2_rn(make_float2(h0, h1), mone2, pr);       // exact remainders
-              w[8 + i] = pack2<T>(lo.x, lo.y);
-              acc = __fadd2_rn(acc, pr);
+          for (int i = 0; i < 8; ++i) {
+            const float2 x = __ffma2_rn(make_float2(sv[q * 16 + 2 * i], sv[q * 16 + 2 * i + 1]), sc2, nm2);
+            float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
+            if (diagonal) {
+              p0 = q * 16 + 2 * i <= lim ? p0 : 0.f;
+              p1 = q * 16 + 2 * i + 1 <= lim ? p1 : 0.f;
             }
-            tmem_store16_words(sbuf + q * 16, w);
+            const float2 pr = make_float2(p0, p1);
+            float h0, h1;
+            w[i] = pack2_split<T>(p0, p1, h0, h1);                               // rounded pair
+            const float2 lo = __ffma2_rn(make_float2(h0, h1), mone2, pr);       // exact remainders
+            w[8 + i] = pack2<T>(lo.x, lo.y);
+            acc = __fadd2_rn(acc, pr);
           }
-          l += acc.x + acc.y;
-          tmem_store_wait();
+          tmem_store16_words(sbuf + q * 16, w);
         }
+        l += acc.x + acc.y;
+        tmem_store_wait();
         tc_fence_before();
-        // V rows past the pair's last position inside loaded blocks, and those of a window's
-        // gap: zero them (a NaN there would survive a zero weight).  Both groups write the
-        // same zeros, but for shared tiles, where each has its own chunk.
+        // V rows past the pair's last position inside loaded blocks: zero them (a NaN
+        // there would survive a zero weight).  Both groups write the same zeros.
         const int rows_needed = it.last + 1 - kbase;
-        const int gap0 = kWin ? max(0, p.sinks - kbase) : 0;
-        const int gap1 = kWin ? min(kKC, p.sinks + it.gap - kbase) : 0;
-        const bool unseen = rows_needed < kKC || (kWin && gap0 < gap1);
-        if (unseen) {  // warp-uniform; V of this chunk must have landed first
-          if (!__all_sync(0xffffffffu, wait_role(&bars.vfull[vst], vturn, abort_flag, p.err, p.wait_limit_ns))) {
+        if (rows_needed < kKC) {  // warp-uniform; V of this chunk must have landed first
+          if (!__all_sync(0xffffffffu, wait_role(&bars.vfull[c % kStages], (c / kStages) & 1, abort_flag, p.err, p.wait_limit_ns))) {
             ok = false;
             break;
           }
         }
-        if (t < kKC && unseen) {
+        if (t < kKC && rows_needed < kKC) {
           const int rows_loaded = min(kKC, (rows_needed + p.block_size - 1) / p.block_size * p.block_size);
-          if ((t >= rows_needed && t < rows_loaded) || (kWin && t >= gap0 && t < gap1)) {
-            unsigned char* vrow = smem + kOffV + vst * kKVTile + (t >> 3) * kGroup + (t & 7) * 128;
+          if (t >= rows_needed && t < rows_loaded) {
+            unsigned char* vrow = smem + kOffV + (c % kStages) * kKVTile + (t >> 3) * kGroup + (t & 7) * 128;
 #pragma unroll
             for (int q = 0; q < 8 * L::kBlocks; ++q)  // 128 bytes per 64-column block, 1 KB apart
               reinterpret_cast<uint4*>(vrow + (q >> 3) * 1024)[q & 7] = make_uint4(0, 0, 0, 0);
@@ -855,9 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_tc_kernel(const __grid_co
       prev_row = out_row;
       prev_c = c - 1;
       prev_l = l;
-      prev_m = m;
     }
-    if (ok && prev_c >= 0 && pv_done(prev_c)) finish(prev_row, prev_l, prev_m);
+    if (ok && prev_c >= 0 && pv_done(prev_c)) finish(prev_row, prev_l);
     __syncwarp();
   }
 
@@ -962,39 +676,12 @@ bool make_query_map(CUtensorMap* m, const void* q, uint32_t heads, uint32_t toke
 
 template <typename T, int D>
 cudaError_t launch_prefill_t(const PrefillArgs& args, int grid, cudaStream_t stream) {
-  constexpr int smem = PfLayout<D, Mode::kPlain>::kSmemBytes;
+  constexpr int smem = PfLayout<D>::kSmemBytes;
   static std::atomic<unsigned long long> configured{0};  // devices whose limit is raised
-  cudaError_t e = ensure_smem_limit(prefill_tc_kernel<T, D, Mode::kPlain>, smem, configured);
+  cudaError_t e = ensure_smem_limit(prefill_tc_kernel<T, D>, smem, configured);
   if (e != cudaSuccess) return e;
-  prefill_tc_kernel<T, D, Mode::kPlain><<<grid, kThreads, smem, stream>>>(args);
+  prefill_tc_kernel<T, D><<<grid, kThreads, smem, stream>>>(args);
   return cudaGetLastError();
-}
-
-template <typename T, int D, Mode kMode>
-cudaError_t launch_window_t(const PrefillArgs& args, int grid, cudaStream_t stream) {
-  constexpr int smem = PfLayout<D, kMode>::kSmemBytes;
-  static std::atomic<unsigned long long> configured{0};  // devices whose limit is raised
-  cudaError_t e = ensure_smem_limit(prefill_tc_kernel<T, D, kMode>, smem, configured);
-  if (e != cudaSuccess) return e;
-  return launch_dependent(prefill_tc_kernel<T, D, kMode>, grid, kThreads, smem, stream, args);
-}
-
-template <typename T>
-cudaError_t launch_window_d(const PrefillArgs& args, bool shared, int grid, cudaStream_t stream) {
-  if (args.p.head_dim == 64)
-    return shared ? launch_window_t<T, 64, Mode::kShared>(args, grid, stream)
-                  : launch_window_t<T, 64, Mode::kWindow>(args, grid, stream);
-  return shared ? launch_window_t<T, 128, Mode::kShared>(args, grid, stream)
-                : launch_window_t<T, 128, Mode::kWindow>(args, grid, stream);
-}
-
-// The kernel's maps, of the pools and the queries.
-bool make_maps(PrefillArgs* args, bool bf16) {
-  const PrefillParams& p = args->p;
-  const uint64_t pool_rows = static_cast<uint64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
-  return make_pool_map(&args->tk, p.k_cache, pool_rows, p.block_size, bf16, p.head_dim) &&
-         make_pool_map(&args->tv, p.v_cache, pool_rows, p.block_size, bf16, p.head_dim) &&
-         make_query_map(&args->tq, p.q, p.num_q_heads, p.num_query_tokens, bf16, p.head_dim);
 }
 
 }  // namespace
@@ -1012,8 +699,12 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, int dtype, cudaStream_t st
   PrefillArgs args;
   args.p = p;
   const bool bf16 = dtype == PKV_BF16;
+  const uint64_t pool_rows = static_cast<uint64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
   if (p.head_dim != 64 && p.head_dim != 128) return cudaErrorInvalidValue;
-  if (!make_maps(&args, bf16)) return cudaErrorInvalidValue;
+  if (!make_pool_map(&args.tk, p.k_cache, pool_rows, p.block_size, bf16, p.head_dim) ||
+      !make_pool_map(&args.tv, p.v_cache, pool_rows, p.block_size, bf16, p.head_dim) ||
+      !make_query_map(&args.tq, p.q, p.num_q_heads, p.num_query_tokens, bf16, p.head_dim))
+    return cudaErrorInvalidValue;
   prefill_list_kernel<<<1, kListThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -1025,24 +716,6 @@ cudaError_t launch_prefill_tc(const PrefillParams& p, int dtype, cudaStream_t st
   if (p.head_dim == 64)
     return bf16 ? launch_prefill_t<__nv_bfloat16, 64>(args, grid, stream) : launch_prefill_t<__half, 64>(args, grid, stream);
   return bf16 ? launch_prefill_t<__nv_bfloat16, 128>(args, grid, stream) : launch_prefill_t<__half, 128>(args, grid, stream);
-}
-
-cudaError_t launch_window_prefill(const PrefillParams& p, bool shared, int dtype, cudaStream_t stream) {
-  PrefillArgs args;
-  args.p = p;
-  const bool bf16 = dtype == PKV_BF16;
-  if (!make_maps(&args, bf16)) return cudaErrorInvalidValue;
-  const int sms = sm_count();
-  if (sms <= 0) return cudaErrorInvalidDevice;
-  const int64_t items = window_prefill_items(p, shared);
-  const int grid = static_cast<int>(items < sms ? items : sms);
-  return bf16 ? launch_window_d<__nv_bfloat16>(args, shared, grid, stream)
-              : launch_window_d<__half>(args, shared, grid, stream);
-}
-
-int64_t window_prefill_items(const PrefillParams& p, bool shared) {
-  const int span = (shared ? 1 : kGroups) * p.tile_tokens;
-  return (static_cast<int64_t>(p.num_query_tokens) / span + p.num_seqs) * p.num_kv_heads;
 }
 
 }  // namespace pkv
