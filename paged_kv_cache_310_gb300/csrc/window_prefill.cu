@@ -45,8 +45,8 @@ namespace pkv {
 namespace {
 
 constexpr int kGroups = 2;                 // tiles per item, one softmax warpgroup each
-constexpr int kThreads = (4 * kGroups + 3) * 32;
-constexpr int kProducerWarp = 4 * kGroups, kMmaWarp = 4 * kGroups + 1, kVWarp = 4 * kGroups + 2;
+constexpr int kThreads = (5 * kGroups + 2) * 32;
+constexpr int kProducerWarp = 4 * kGroups, kVWarp = kProducerWarp + 1, kMmaWarp = kProducerWarp + 2;  // and the next
 constexpr int kRows = 128;                 // query rows per tile (M)
 constexpr int kKC = 64;                    // keys per chunk
 constexpr uint32_t kTmemCols = 512;        // per tile g: S[2] at 256g + 0/64, O at 256g + 128 (D columns)
@@ -69,9 +69,9 @@ struct Layout {
   static constexpr int kOffQ = 2 * kStages * kKVTile;
   static constexpr int kOffBar = kOffQ + kQBufs * kQItem;
   // K ring full/empty, V ring full/empty, qfull[2], qempty[2], then per tile: sfull[2],
-  // pfull[2], pvdone[2]; drain
+  // pfull[2], pvdone[2]; turn and drain of each MMA issuer
   // shared tiles: joined halves full, empty
-  static constexpr int kNumBars = 4 * kStages + 4 + kGroups * 6 + 3;
+  static constexpr int kNumBars = 4 * kStages + 4 + kGroups * 8 + 2;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   // shared tiles: the second warpgroup's O on its way to the first, 64 dimensions at a time, and
   // its rows' maxima and sums
@@ -82,7 +82,7 @@ struct Layout {
 };
 
 struct Bars {
-  uint64_t *kfull, *kempty, *vfull, *vempty, *qfull, *qempty, *grp, *drain, *jfull, *jempty;
+  uint64_t *kfull, *kempty, *vfull, *vempty, *qfull, *qempty, *grp, *turn, *drain, *jfull, *jempty;
   // per tile g (addresses computed, so a runtime tile index needs no local-memory table)
   __device__ __forceinline__ uint64_t* sfull(int g, int i) const { return grp + 6 * g + i; }
   __device__ __forceinline__ uint64_t* pfull(int g, int i) const { return grp + 6 * g + 2 + i; }
@@ -101,8 +101,9 @@ __device__ __forceinline__ Bars carve(unsigned char* smem) {
   r.qfull = b + 4 * kStages;
   r.qempty = r.qfull + 2;
   r.grp = r.qempty + 2;
-  r.drain = r.grp + 6 * kGroups;
-  r.jfull = r.drain + 1;
+  r.turn = r.grp + 6 * kGroups;
+  r.drain = r.turn + kGroups;
+  r.jfull = r.drain + kGroups;
   r.jempty = r.jfull + 1;
   return r;
 }
@@ -346,15 +347,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bars.kfull[i], 1);
-      mbar_init(&bars.kempty[i], 1);
+      mbar_init(&bars.kempty[i], kShared ? 1 : kGroups);
       mbar_init(&bars.vfull[i], 1);
-      mbar_init(&bars.vempty[i], 1);
+      mbar_init(&bars.vempty[i], kShared ? 1 : kGroups);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.qfull[i], 1);
-      mbar_init(&bars.qempty[i], 1);
+      mbar_init(&bars.qempty[i], kGroups);
     }
     for (int g = 0; g < kGroups; ++g) {
+      mbar_init(&bars.turn[g], 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(bars.sfull(g, i), 1);
         mbar_init(bars.pfull(g, i), 4);
@@ -435,62 +437,57 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
       ok = load_chunks<D, kShared>(p, unpack_item<kShared>(cur.cur, p), &a.tv, smem + kOffV, bars.vfull, bars.vempty, c,
                           vissued_slot, pol_kv, abort_flag);
     }
-  } else if (warp == kMmaWarp) {
-    // ============================ MMA issuer ============================
-    // A fixed schedule, per chunk c: PV of tile 0, PV of tile 1, then QK of both tiles
-    // for chunk c + 2 (whose S buffers held the probabilities of chunk c).  The whole
-    // warp runs it with warp-uniform control flow (descriptors and counters stay in
-    // uniform registers); one elected lane issues.
+  } else if (warp >= kMmaWarp) {
+    // ============================ MMA issuers ============================
+    // One per softmax warpgroup, each with a fixed schedule: PV of chunk c, then QK of
+    // chunk c + 2 (whose S buffer held the probabilities of chunk c).  The whole warp runs it
+    // with warp-uniform control flow (descriptors and counters stay in uniform registers); one
+    // elected lane issues.
+    const int g = warp - kMmaWarp;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t idesc_qk = instr_desc_f16(kBf16, false, false, kRows, kKC);
     constexpr uint32_t idesc_pv = instr_desc_f16(kBf16, false, true, kRows, D);
+    // Shared tiles: a step has a chunk for each warpgroup, in stages st and st + 1; chunks,
+    // items' counts and the stages' turns below are then in steps.
+    constexpr int kPer = kShared ? 2 : 1;  // chunks, and stages, of a step
+    const int st0 = kShared ? g : 0;       // this issuer's stage of a step
     // descriptor bases; adding (byte offset >> 4) moves a descriptor's start address
-    const uint64_t dq0 = smem_desc(smem_addr(smem + kOffQ), 16, kGroup, kLayoutSwizzle128);
-    const uint64_t dk0 = smem_desc(smem_addr(smem), 16, kGroup, kLayoutSwizzle128);
-    const uint64_t dv0 = smem_desc(smem_addr(smem + kOffV), 1024, kGroup, kLayoutSwizzle128);
+    const uint64_t dq0 = smem_desc(smem_addr(smem + kOffQ + (kShared ? 0 : g * kQBytes)), 16, kGroup, kLayoutSwizzle128);
+    const uint64_t dk0 = smem_desc(smem_addr(smem + st0 * kKVTile), 16, kGroup, kLayoutSwizzle128);
+    const uint64_t dv0 = smem_desc(smem_addr(smem + kOffV + st0 * kKVTile), 1024, kGroup, kLayoutSwizzle128);
+    const uint32_t sd = tmem + g * 256, od = sd + 128;
     auto wait_all = [&](uint64_t* bar, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, wait_role(bar, parity, abort_flag, p.err, p.wait_limit_ns));
     };
-    // QK side: next chunk qc (global), its stage / phase, its place in the item
-    // (shared tiles: a step has a chunk for each warpgroup, in stages qst and qst + 1; chunks,
-    // items' counts and the stages' turns below are then in steps)
-    constexpr int kPer = kShared ? 2 : 1;  // chunks, and stages, of a step
     auto steps_of = [&](const WindowCursor& c) { return c.valid() ? unpack_item<kShared>(c.cur, p).nchunks / kPer : 0; };
+    // QK side: next chunk qc (global), its stage / phase, its place in the item
     WindowCursor qcur;
     qcur.init(p, span);
     int qc = 0, qst = 0, qph = 0, qk = 0, qn = steps_of(qcur);
+    uint32_t starts = 0;  // bit sb: the chunk in S buffer sb is its item's first, whose PV overwrites O
     // PV side
-    WindowCursor pcur = qcur;
-    int pc = 0, pst = 0, pph = 0, pk = 0, pn = qn;
+    int pc = 0, pst = 0, pph = 0;
     bool ok = true;
-    // QK of chunk qc for both tiles (k_seen: its K stage was already seen landed)
-    auto qk_pair = [&](bool k_seen) -> bool {
+    auto issue_qk = [&](bool k_seen) -> bool {  // k_seen: the K stage was already seen landed
       const int qj = qcur.k, qb = qj % kQBufs, sb = qc & 1;
       if (qk == 0 && !wait_all(&bars.qfull[qb], (qj / kQBufs) & 1)) return false;
-      if (!k_seen && !wait_all(&bars.kfull[qst], qph)) return false;
-      if (kShared && !wait_all(&bars.kfull[qst + 1], qph)) return false;
-      const bool last = qk == qn - 1;
+      if (!k_seen && !wait_all(&bars.kfull[qst + st0], qph)) return false;
+      const bool first = qk == 0, last = qk == qn - 1;
       const uint64_t dk = dk0 + ((qst * kKVTile) >> 4);
-      const uint64_t dqb = dq0 + ((qb * kQItem) >> 4);
+      const uint64_t dq = dq0 + ((qb * kQItem) >> 4);
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          const uint64_t dq = dqb + (kShared ? 0 : (g * kQBytes) >> 4);
-          const uint64_t dkg = dk + (kShared ? (g * kKVTile) >> 4 : 0);
-          const uint32_t d = tmem + g * 256 + sb * 64;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
-            mma_f16(d, dq + off, dkg + off, idesc_qk, kk > 0);
-          }
-          mma_commit(bars.sfull(g, sb));
-          if (kShared) mma_commit(&bars.kempty[qst + g]);
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
+          mma_f16(sd + sb * 64, dq + off, dk + off, idesc_qk, kk > 0);
         }
-        if (!kShared) mma_commit(&bars.kempty[qst]);  // both tiles' QKs of this chunk
-        if (last) mma_commit(&bars.qempty[qb]);  // both tiles are done with the item's queries
+        mma_commit(bars.sfull(g, sb));
+        mma_commit(&bars.kempty[qst + st0]);
+        if (last) mma_commit(&bars.qempty[qb]);  // this issuer is done with the item's queries
       }
       __syncwarp();
+      starts = (starts & ~(1u << sb)) | (static_cast<uint32_t>(first) << sb);
       ++qc;
       if ((qst += kPer) == kStages) {
         qst = 0;
@@ -503,53 +500,40 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
       }
       return true;
     };
-    for (int i = 0; i < 2 && ok && qcur.valid(); ++i) ok = qk_pair(false);
-    while (ok && pcur.valid()) {
+    for (int i = 0; i < 2 && ok && qcur.valid(); ++i) ok = issue_qk(false);
+    for (; ok && pc < qc; ++pc) {
       const int sb = pc & 1;
-      static_assert(kGroups == 2, "the probe below covers two tiles");
-      // one round trip probes everything this iteration needs (V of chunk pc, both
-      // tiles' probabilities, K of chunk pc + 2); only what is not ready yet is waited for
+      // the other issuer's last PV is out
+      uint64_t* turn = &bars.turn[g ^ 1];
+      const uint32_t turn_parity = (pc & 1) ^ (g ^ 1);
+      // one round trip probes everything this step needs; only what is not ready yet is waited for
       const uint32_t seen = __shfl_sync(0xffffffffu,
-          mbar_test_wait4(&bars.vfull[pst], pph, bars.pfull(0, sb), (pc >> 1) & 1, bars.pfull(1, sb),
-                          (pc >> 1) & 1, &bars.kfull[qst], qph), 0);
-      if (!(seen & 1) && !wait_all(&bars.vfull[pst], pph)) break;
-      if (kShared && !wait_all(&bars.vfull[pst + 1], pph)) break;
+          mbar_test_wait4(&bars.vfull[pst + st0], pph, bars.pfull(g, sb), (pc >> 1) & 1, turn, turn_parity,
+                          &bars.kfull[qst + st0], qph), 0);
+      if (!(seen & 1) && !wait_all(&bars.vfull[pst + st0], pph)) break;
+      if (!(seen & 2) && !wait_all(bars.pfull(g, sb), (pc >> 1) & 1)) break;
+      if (!(seen & 4) && !wait_all(turn, turn_parity)) break;
       const uint64_t dv = dv0 + ((pst * kKVTile) >> 4);
-      const bool acc0 = pk > 0;
+      const bool acc0 = !(starts >> sb & 1);
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t pa = sd + sb * 64;  // probabilities: [hi 8 | lo 8] columns per 16 keys
 #pragma unroll
-      for (int g = 0; g < kGroups; ++g) {
-        if (!(seen & (2u << g)) && !wait_all(bars.pfull(g, sb), (pc >> 1) & 1)) {
-          ok = false;
-          break;
+        for (int kk = 0; kk < kKC / 16; ++kk) {
+          const uint64_t bd = dv + ((kk * 2 * kGroup) >> 4);
+          mma_f16_tmem_a(od, pa + kk * 16, bd, idesc_pv, acc0 || kk > 0);
+          mma_f16_tmem_a(od, pa + kk * 16 + 8, bd, idesc_pv, true);
         }
-        tc_fence_after();
-        if (elect_one()) {
-          const uint32_t pa = tmem + g * 256 + sb * 64;  // probabilities: [hi 8 | lo 8] columns per 16 keys
-          const uint32_t od = tmem + g * 256 + 128;
-#pragma unroll
-          for (int kk = 0; kk < kKC / 16; ++kk) {
-            const uint64_t bd = dv + (((kShared ? g * kKVTile : 0) + kk * 2 * kGroup) >> 4);
-            mma_f16_tmem_a(od, pa + kk * 16, bd, idesc_pv, acc0 || kk > 0);
-            mma_f16_tmem_a(od, pa + kk * 16 + 8, bd, idesc_pv, true);
-          }
-          mma_commit(bars.pvdone(g, sb));
-          if (kShared) mma_commit(&bars.vempty[pst + g]);
-          else if (g == kGroups - 1) mma_commit(&bars.vempty[pst]);  // every tile's PV of this chunk
-        }
-        __syncwarp();
+        mma_commit(&bars.vempty[pst + st0]);
+        mma_commit(bars.pvdone(g, sb));
+        mbar_arrive(&bars.turn[g]);
       }
-      if (!ok) break;
-      ++pc;
+      __syncwarp();
       if ((pst += kPer) == kStages) {
         pst = 0;
         pph ^= 1;
       }
-      if (++pk == pn) {
-        pk = 0;
-        pcur.advance();
-        pn = steps_of(pcur);
-      }
-      if (qcur.valid()) ok = qk_pair((seen & 8u) != 0);
+      if (qcur.valid()) ok = issue_qk((seen & 8) != 0);
     }
     __syncwarp();
   } else {
@@ -798,17 +782,18 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
       for (int c = max(0, *vissued_slot - kStages); c < *vissued_slot; ++c)
         if (!mbar_wait(&bars.vfull[c % kStages], (c / kStages) & 1)) break;
     }
-    if (warp == kMmaWarp) {
+    if (warp >= kMmaWarp) {
       // every lane commits (the MMAs went out from whichever lane was elected; a lane
       // that issued none arrives at once), so the barrier completes only when all of
       // the warp's MMAs have
+      uint64_t* drain = bars.drain + (warp - kMmaWarp);
       if (lane == 0) {
-        mbar_init(bars.drain, 32);
+        mbar_init(drain, 32);
         fence_barrier_init();
       }
       __syncwarp();
-      mma_commit(bars.drain);
-      mbar_wait(bars.drain, 0);
+      mma_commit(drain);
+      mbar_wait(drain, 0);
       __syncwarp();
     }
   }
