@@ -260,20 +260,19 @@ struct WindowCursor {
 // The lowest n bits (none below 0, all from 64 on).
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
-// A row's 64 scores times the scale, in place; where the mask cuts the chunk, keys
-// without a bit in `seen` become -inf, so that their weights come out as 0 without another test.
-// Returns the maximum.
-__device__ __forceinline__ float scaled_maximum(float* sv, float2 scale, bool cut, uint64_t seen) {
+// Branches that a chunk rarely takes: their code goes out of the loop's straight line (instruction
+// fetches past them were a tenth of a chunk's time).
+__device__ __forceinline__ bool rare(bool taken) { return __builtin_expect(taken, 0); }
+
+// The maximum of a row's 64 scores. Where the mask cuts the chunk, keys past `lim`, and those
+// before `low` from `sink` on, become -inf in place, so that their weights come out as 0 without
+// another test.
+__device__ __forceinline__ float masked_maximum(float* sv, bool cut, int lim, int low, int sink) {
+  if (rare(cut)) {
+    const uint64_t seen = low_bits(lim + 1) & (~low_bits(low) | low_bits(sink));
+    const uint32_t lower = static_cast<uint32_t>(seen), upper = static_cast<uint32_t>(seen >> 32);
 #pragma unroll
-  for (int i = 0; i < 64; i += 2) {
-    const float2 x = __fmul2_rn(make_float2(sv[i], sv[i + 1]), scale);
-    sv[i] = x.x;
-    sv[i + 1] = x.y;
-  }
-  if (cut) {
-    const uint32_t low = static_cast<uint32_t>(seen), high = static_cast<uint32_t>(seen >> 32);
-#pragma unroll
-    for (int i = 0; i < 64; ++i) sv[i] = ((i < 32 ? low : high) & (1u << (i % 32))) ? sv[i] : -INFINITY;
+    for (int i = 0; i < 64; ++i) sv[i] = ((i < 32 ? lower : upper) & (1u << (i % 32))) ? sv[i] : -INFINITY;
   }
   float e0 = -INFINITY, e1 = -INFINITY;
 #pragma unroll
@@ -282,6 +281,18 @@ __device__ __forceinline__ float scaled_maximum(float* sv, float2 scale, bool cu
     e1 = fmax3(e1, sv[i + 2], sv[i + 3]);
   }
   return fmaxf(e0, e1);
+}
+
+// p minus its rounding h, exact: a mixed-precision h * -1 + p, one instruction for taking the 16-bit
+// value apart and for the difference.
+template <typename T>
+__device__ __forceinline__ float rest_of(uint32_t h, float p) {
+  float d;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value)
+    asm("fma.rn.f32.bf16 %0, %1, %2, %3;" : "=f"(d) : "h"(static_cast<uint16_t>(h)), "h"(static_cast<uint16_t>(0xBF80)), "f"(p));
+  else
+    asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(static_cast<uint16_t>(h)), "h"(static_cast<uint16_t>(0xBC00)), "f"(p));
+  return d;
 }
 
 // One producer warp's copies of an item's chunks of K (or V) into its ring: per chunk
@@ -440,9 +451,19 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
   } else if (warp >= kMmaWarp) {
     // ============================ MMA issuers ============================
     // One per softmax warpgroup, each with a fixed schedule: PV of chunk c, then QK of
-    // chunk c + 2 (whose S buffer held the probabilities of chunk c).  The whole warp runs it
+    // chunk c + 2 (whose S buffer held the probabilities of chunk c).  (One issuer for both left
+    // the tensor cores idle for 600 of a step's 3,050 clocks: an issuer's own instructions between
+    // its products take as long as the 9 products that the hardware queues.)  The whole warp runs it
     // with warp-uniform control flow (descriptors and counters stay in uniform registers); one
     // elected lane issues.
+    // The tiles of a pair take turns: a PV goes out only after the other tile's last one and the
+    // first product of its QK, so that one's products run while the other's issuer and
+    // softmax are between theirs.  (Without turns 267 us against 248 on four prompts of 1,000 to
+    // 2,000 new tokens, window 1,024, 64/8 heads, head_dim 128; 199 against 203 at head_dim 64.
+    // Shared tiles, whose steps have more room: 109 without, 111 with, on 32 sequences with 3 to 8
+    // new tokens, window 4,096.  PV and QK of a tile from warps of their own, with 184 and 72
+    // registers a thread: 257 and 118: 16 warps slow the softmax.)
+    constexpr bool kTurns = !kShared;
     const int g = warp - kMmaWarp;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t idesc_qk = instr_desc_f16(kBf16, false, false, kRows, kKC);
@@ -468,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
     // PV side
     int pc = 0, pst = 0, pph = 0;
     bool ok = true;
-    auto issue_qk = [&](bool k_seen) -> bool {  // k_seen: the K stage was already seen landed
+    auto issue_qk = [&](bool k_seen, bool pass) -> bool {  // k_seen: the K stage was already seen landed; pass: the turn
       const int qj = qcur.k, qb = qj % kQBufs, sb = qc & 1;
       if (qk == 0 && !wait_all(&bars.qfull[qb], (qj / kQBufs) & 1)) return false;
       if (!k_seen && !wait_all(&bars.kfull[qst + st0], qph)) return false;
@@ -481,6 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
           mma_f16(sd + sb * 64, dq + off, dk + off, idesc_qk, kk > 0);
+          if (kTurns && kk == 0 && pass) mbar_arrive(&bars.turn[g]);
         }
         mma_commit(bars.sfull(g, sb));
         mma_commit(&bars.kempty[qst + st0]);
@@ -500,10 +522,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
       }
       return true;
     };
-    for (int i = 0; i < 2 && ok && qcur.valid(); ++i) ok = issue_qk(false);
+    for (int i = 0; i < 2 && ok && qcur.valid(); ++i) ok = issue_qk(false, false);
     for (; ok && pc < qc; ++pc) {
       const int sb = pc & 1;
-      // the other issuer's last PV is out
       uint64_t* turn = &bars.turn[g ^ 1];
       const uint32_t turn_parity = (pc & 1) ^ (g ^ 1);
       // one round trip probes everything this step needs; only what is not ready yet is waited for
@@ -512,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
                           &bars.kfull[qst + st0], qph), 0);
       if (!(seen & 1) && !wait_all(&bars.vfull[pst + st0], pph)) break;
       if (!(seen & 2) && !wait_all(bars.pfull(g, sb), (pc >> 1) & 1)) break;
-      if (!(seen & 4) && !wait_all(turn, turn_parity)) break;
+      if (kTurns && !(seen & 4) && !wait_all(turn, turn_parity)) break;
       const uint64_t dv = dv0 + ((pst * kKVTile) >> 4);
       const bool acc0 = !(starts >> sb & 1);
       tc_fence_after();
@@ -526,14 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
         }
         mma_commit(&bars.vempty[pst + st0]);
         mma_commit(bars.pvdone(g, sb));
-        mbar_arrive(&bars.turn[g]);
       }
       __syncwarp();
       if ((pst += kPer) == kStages) {
         pst = 0;
         pph ^= 1;
       }
-      if (qcur.valid()) ok = issue_qk((seen & 8) != 0);
+      if (qcur.valid()) ok = issue_qk((seen & 8) != 0, true);
+      else if (kTurns && lane == 0) mbar_arrive(&bars.turn[g]);
     }
     __syncwarp();
   } else {
@@ -544,8 +565,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
     const int head = t / TQ, tok = t % TQ;    // head-major rows
     const uint32_t lane_base = tmem + grp * 256 + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t obuf = lane_base + 128;
-    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-    const float2 mone2 = make_float2(-1.f, -1.f);
+    // scores are multiplied where the maximum is subtracted; by a scale that is not positive, which
+    // does not keep their order, before
+    const bool ordered = p.scale_log2 > 0.f;
+    const float scale = ordered ? p.scale_log2 : 1.f;
+    const float2 sc2 = make_float2(scale, scale);
     int c = 0;
     bool ok = true;
     int prev_row = -1, prev_c = -1;
@@ -649,7 +673,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
       for (int k = 0; k < it.nchunks / (kShared ? 2 : 1); ++k, ++c) {
         const int sb = c & 1;
         const uint32_t sbuf = lane_base + sb * 64;
-        if (!__all_sync(0xffffffffu, wait_role(bars.sfull(grp, sb), (c >> 1) & 1, abort_flag, p.err, p.wait_limit_ns))) {
+        if (rare(!__all_sync(0xffffffffu, mbar_test_wait(bars.sfull(grp, sb), (c >> 1) & 1))) &&
+            !__all_sync(0xffffffffu, wait_role(bars.sfull(grp, sb), (c >> 1) & 1, abort_flag, p.err, p.wait_limit_ns))) {
           ok = false;
           break;
         }
@@ -660,27 +685,28 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
         // keys of the chunk past lim are masked, and those before its window but for the sinks
         const int lim = qpos - kbase, low = lim - p.window + 1, sink = p.sinks - kbase;
         const bool cut = lim < kKC - 1 || low > max(0, sink);  // only then does the mask cut this row
-        const uint64_t seen = low_bits(lim + 1) & (~low_bits(low) | low_bits(sink));
         // the row's 64 scores, held in registers for both passes
         float sv[64], cm = -INFINITY;
         // pass 1: the row's chunk maximum of scale * score under the mask
         if (!kShared || !idle) {
           tmem_load64(sbuf, sv);
-          cm = scaled_maximum(sv, sc2, cut, seen);
+          if (rare(!ordered)) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) sv[i] *= p.scale_log2;
+          }
+          cm = scale * masked_maximum(sv, cut, lim, low, sink);
         }
         // lazy rescale: keep m unless the chunk brings a score more than the slack above
         // (a chunk that the mask leaves nothing of gives cm = -inf and changes nothing)
-        float alpha = 1.f;
-        if (m == -INFINITY) {
-          m = cm;  // still -inf where the row's window starts in a later chunk: its sum and O of zero need no rescale
-        } else if (cm > m + kRescaleSlack) {
-          alpha = exp2f(m - cm);
-          m = cm;
-          l *= alpha;
-        }
+        // While the maximum is -inf (the row's window starts in a later chunk) the row's sum and O
+        // are zeros, which need no rescale.
+        const bool grow = cm > m + kRescaleSlack;
+        const float alpha = grow && m != -INFINITY ? exp2_approx(m - cm) : 1.f;
+        m = grow ? cm : m;
+        l *= alpha;
         // O is read out (at an item's first chunk) or rescaled only after the PVs that
         // accumulate it have completed
-        if (k == 0 && prev_c >= 0) {
+        if (rare(k == 0 && prev_c >= 0)) {
           if (!pv_done(prev_c)) {
             ok = false;
             break;
@@ -689,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
           if (!ok) break;
           prev_c = -1;
         }
-        if (k > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        if (rare(k > 0 && __any_sync(0xffffffffu, alpha != 1.f))) {
           if (!pv_done(c - 1)) {
             ok = false;
             break;
@@ -716,13 +742,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float2 s = make_float2(sv[q * 16 + 2 * i], sv[q * 16 + 2 * i + 1]);
-              const float2 x = __fadd2_rn(s, nm2);
+              const float2 x = __ffma2_rn(s, sc2, nm2);
               const float p0 = exp2_approx(x.x), p1 = exp2_approx(x.y);
               const float2 pr = make_float2(p0, p1);
-              float h0, h1;
-              w[i] = pack2_split<T>(p0, p1, h0, h1);                               // rounded pair
-              const float2 lo = __ffma2_rn(make_float2(h0, h1), mone2, pr);       // exact remainders
-              w[8 + i] = pack2<T>(lo.x, lo.y);
+              w[i] = pack2<T>(p0, p1);  // rounded pair
+              w[8 + i] = pack2<T>(rest_of<T>(w[i] & 0xffff, p0), rest_of<T>(w[i] >> 16, p1));
               acc = __fadd2_rn(acc, pr);
             }
             tmem_store16_words(sbuf + q * 16, w);
@@ -738,13 +762,13 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
         const int gap0 = max(0, p.sinks - kbase);
         const int gap1 = min(kKC, p.sinks + it.gap - kbase);
         const bool unseen = rows_needed < kKC || gap0 < gap1;
-        if (unseen) {  // warp-uniform; V of this chunk must have landed first
+        if (rare(unseen)) {  // warp-uniform; V of this chunk must have landed first
           if (!__all_sync(0xffffffffu, wait_role(&bars.vfull[vst], vturn, abort_flag, p.err, p.wait_limit_ns))) {
             ok = false;
             break;
           }
         }
-        if (t < kKC && unseen) {
+        if (rare(t < kKC && unseen)) {
           const int rows_loaded = min(kKC, (rows_needed + p.block_size - 1) / p.block_size * p.block_size);
           if ((t >= rows_needed && t < rows_loaded) || (t >= gap0 && t < gap1)) {
             unsigned char* vrow = smem + kOffV + vst * kKVTile + (t >> 3) * kGroup + (t & 7) * 128;
@@ -805,8 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
 
 // Queries [tokens][heads][head_dim] seen as 3-D (head_dim, heads, tokens); a box is 8
 // tokens x 64 dims of one head, landing as one swizzled 64-column block of an 8-row group.
-bool make_query_map_uncached(CUtensorMap* m, const void* q, uint32_t heads, uint32_t tokens, bool bf16,
-                             int head_dim) {
+bool make_query_map(CUtensorMap* m, const void* q, uint32_t heads, uint32_t tokens, bool bf16, int head_dim) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
@@ -817,12 +840,6 @@ bool make_query_map_uncached(CUtensorMap* m, const void* q, uint32_t heads, uint
   return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(q),
             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool make_query_map(CUtensorMap* m, const void* q, uint32_t heads, uint32_t tokens, bool bf16, int head_dim) {
-  return cached_map(m, MapKey{q, tokens, heads, 4, bf16 ? 2 : 1, head_dim}, [&](CUtensorMap* out) {
-    return make_query_map_uncached(out, q, heads, tokens, bf16, head_dim);
-  });
 }
 
 template <typename T, int D, bool kShared>
@@ -841,12 +858,13 @@ cudaError_t launch_d(const PrefillArgs& args, bool shared, int grid, cudaStream_
   return shared ? launch_t<T, 128, true>(args, grid, stream) : launch_t<T, 128, false>(args, grid, stream);
 }
 
-// The kernel's maps, of the pools and the queries.
+// The kernel's maps, of the pools and the queries: encoded for each call, which a call of 20 us and
+// more hides.
 bool make_maps(PrefillArgs* args, bool bf16) {
   const WindowPrefillParams& p = args->p;
   const uint64_t pool_rows = static_cast<uint64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
-  return make_pool_map(&args->tk, p.k_cache, pool_rows, p.block_size, bf16, p.head_dim) &&
-         make_pool_map(&args->tv, p.v_cache, pool_rows, p.block_size, bf16, p.head_dim) &&
+  return make_pool_map_uncached(&args->tk, p.k_cache, pool_rows, p.block_size, bf16, p.head_dim) &&
+         make_pool_map_uncached(&args->tv, p.v_cache, pool_rows, p.block_size, bf16, p.head_dim) &&
          make_query_map(&args->tq, p.q, p.num_q_heads, p.num_query_tokens, bf16, p.head_dim);
 }
 
