@@ -144,14 +144,17 @@ struct PrefillPlan {
 };
 
 // Which kernel a windowed prefill takes: the one with the shortest estimate, for sequences that
-// share the new tokens out evenly (the host knows no more of them).  Fitted, within a fifth, on
-// calls of 1 to 64 sequences with 3 to 2,000 new tokens each, windows of 130 to 4,096, in us:
-//  * rows: 10 + 0.85 (D 128) or 0.65 (D 64) per 1,000 tiles of 16 tokens for 16 query rows (32
-//    sequences of 4 new tokens, 64/8 heads, D 64, window 1,024: 30 against 47 with shared tiles);
-//  * shared tiles: 12 + 2.1 a step of 128 tokens for one tile (64 sequences of 8, D 128: 100 against
-//    134 with rows, 137 with pairs);
-//  * pairs: 10 + 1.55 a step of 64 tokens for two tiles (4 sequences of 256: 74 against 93 with
-//    shared tiles, 240 with rows).
+// share the new tokens out evenly (the host knows no more of them).  Only the estimates' order
+// matters; on calls of 1 to 64 sequences with 4 to 2,400 new tokens each, windows of 128 to 4,096,
+// head_dim 64 and 128, it was right or within a tenth but for one (32 sequences of 5, D 64, window
+// 4,096: 114 us with rows, 101 with shared tiles).  In us:
+//  * rows: 10 + 0.85 (D 128) or 0.65 (D 64) per 1,000 tiles of 16 tokens for 16 query rows (1
+//    sequence of 4 new tokens, 64/8 heads, window 4,096: 21 against 51 with shared tiles; 64 of 4, D 64,
+//    window 256: 29 against 36);
+//  * shared tiles: 12 + 2.1 a step of 128 tokens for one tile (64 sequences of 8, window 1,024: 82 against
+//    133 with rows, 103 with pairs; 32 of 5, window 4,096: 110 against 160 and 166);
+//  * pairs: 10 + 1.55 a step of 64 tokens for two tiles (4 sequences of 256, window 1,024: 53 against 72
+//    with shared tiles, 240 with rows).
 PrefillPlan plan_prefill(const Args& a) {
   const int64_t S = a.num_seqs, H = a.cache->num_kv_heads, T = a.num_query_tokens;
   const int group = a.num_q_heads / a.cache->num_kv_heads;

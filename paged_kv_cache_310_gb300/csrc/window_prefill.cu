@@ -5,7 +5,7 @@
 // attends to the positions j <= p with j > p - window or j < sinks, through the block table.
 //
 // Tiles, chunks and products are those of prefill_tc.cu: a tile is 128 query rows of one KV
-// head, its G query heads times TQ = 8 * floor(16 / G) consecutive new tokens, head-major; per
+// head, its G query heads times TQ = 8 * floor(16 / G) consecutive new tokens, token by token; per
 // 64-key chunk and tile
 //   S[128 rows x 64 keys] = Q . K^T             (M=128, N=64, K=D dims)
 //   O[128 rows x D dims] += P . V               (M=128, N=D,  K=64 keys), twice: P as a rounded
@@ -25,13 +25,21 @@
 //    that are joined at the item's end: half the steps for tiles that have no partner (a few new
 //    tokens per sequence), twice the items for short batches.
 //
-// Roles (352 threads, persistent CTAs): warps 0-3 and 4-7 the softmax warpgroups (thread = query
-// row = TMEM lane), warp 8 the producer of Q and K, warp 10 of V (4-D TMA boxes, one per block;
-// places past the item's last come from outside the tensor: zeros), warp 9 the MMA issuer with a
-// fixed schedule: PV of both warpgroups' chunks of step c, then QK of step c + 2.
+//  * Rows of a tile are its tokens one after the other, G query heads each, as they lie in memory: one
+//    box of 64 dimensions brings a tile's queries, and a few new tokens leave whole warps without
+//    rows, which skip their weights.
 //
-// Bound: the softmax's chain of dependent instructions, 1.55 us a chunk of two tiles; the tensor
-// cores run 46 % of the time.
+// Roles (384 threads, persistent CTAs): warps 0-3 and 4-7 the softmax warpgroups (thread = query
+// row = TMEM lane), warp 8 the producer of Q and K, warp 9 of V (4-D TMA boxes, one per block;
+// places past the item's last come from outside the tensor: zeros), warps 10 and 11 the MMA issuers
+// of the two warpgroups.
+//
+// Measured (64/8 heads, D 128, bf16): four prompts of 1,000 to 2,000 new tokens, window 1,024: 225 us;
+// 32 sequences with 3 to 8 new tokens, window 4,096: 108 us.
+// Bound: pairs: 2,150 clocks a chunk, of which the softmax's dependent instructions take 1,900 and the
+// tensor cores' products 1,800 (QK with 64 keys runs at 2/3 of their rate: shared memory feeds the
+// 128 query rows), and 3 to 4 us between items.  Shared tiles: the K producer's turns and the
+// softmax, 2,600 clocks a step, and the second round of CTAs.
 #include <climits>
 #include <type_traits>
 
@@ -52,10 +60,12 @@ constexpr int kKC = 64;                    // keys per chunk
 constexpr uint32_t kTmemCols = 512;        // per tile g: S[2] at 256g + 0/64, O at 256g + 128 (D columns)
 constexpr float kRescaleSlack = 8.f;       // log2 units a row's max may grow before O is rescaled
 
+constexpr int kQBlock = kRows * 128;       // 64 dimensions of a tile's queries
 constexpr int kQBufs = 2;                  // query buffers: an item's queries load while the previous one runs
 
-// Shared-memory layout for head_dim D (64 or 128): K, V and Q tiles as [8-row group]
-// [64-column block][8 rows][128 B], 128-byte swizzled.
+// Shared-memory layout for head_dim D (64 or 128): K and V tiles as [8-row group]
+// [64-column block][8 rows][128 B], Q tiles (and outputs in their place) as [64-column block][128
+// rows][128 B], 128-byte swizzled.
 template <int D, bool kShared>
 struct Layout {
   static constexpr int kBlocks = D / 64;                  // 64-column blocks of a row
@@ -69,9 +79,9 @@ struct Layout {
   static constexpr int kOffQ = 2 * kStages * kKVTile;
   static constexpr int kOffBar = kOffQ + kQBufs * kQItem;
   // K ring full/empty, V ring full/empty, qfull[2], qempty[2], then per tile: sfull[2],
-  // pfull[2], pvdone[2]; turn and drain of each MMA issuer
+  // pfull[2], pvdone[2]; turn, staged and drain of each
   // shared tiles: joined halves full, empty
-  static constexpr int kNumBars = 4 * kStages + 4 + kGroups * 8 + 2;
+  static constexpr int kNumBars = 4 * kStages + 4 + kGroups * 9 + 2;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   // shared tiles: the second warpgroup's O on its way to the first, 64 dimensions at a time, and
   // its rows' maxima and sums
@@ -82,7 +92,7 @@ struct Layout {
 };
 
 struct Bars {
-  uint64_t *kfull, *kempty, *vfull, *vempty, *qfull, *qempty, *grp, *turn, *drain, *jfull, *jempty;
+  uint64_t *kfull, *kempty, *vfull, *vempty, *qfull, *qempty, *grp, *turn, *staged, *drain, *jfull, *jempty;
   // per tile g (addresses computed, so a runtime tile index needs no local-memory table)
   __device__ __forceinline__ uint64_t* sfull(int g, int i) const { return grp + 6 * g + i; }
   __device__ __forceinline__ uint64_t* pfull(int g, int i) const { return grp + 6 * g + 2 + i; }
@@ -102,7 +112,8 @@ __device__ __forceinline__ Bars carve(unsigned char* smem) {
   r.qempty = r.qfull + 2;
   r.grp = r.qempty + 2;
   r.turn = r.grp + 6 * kGroups;
-  r.drain = r.turn + kGroups;
+  r.staged = r.turn + kGroups;
+  r.drain = r.staged + kGroups;
   r.jfull = r.drain + kGroups;
   r.jempty = r.jfull + 1;
   return r;
@@ -111,7 +122,8 @@ __device__ __forceinline__ Bars carve(unsigned char* smem) {
 struct PrefillArgs {
   CUtensorMap tk;  // pool 4-D views: one box = one block's tile for one KV head
   CUtensorMap tv;
-  CUtensorMap tq;  // queries (head_dim, heads, tokens): one box = 8 tokens x 64 dims of one head
+  CUtensorMap tq;  // queries (head_dim, heads, tokens): one box = 64 dimensions of a tile
+  CUtensorMap to;  // 16-bit outputs, the same
   WindowPrefillParams p;
 };
 
@@ -260,6 +272,17 @@ struct WindowCursor {
 // The lowest n bits (none below 0, all from 64 on).
 __device__ __forceinline__ uint64_t low_bits(int n) { return n <= 0 ? 0 : n >= 64 ? ~0ull : (1ull << n) - 1; }
 
+// A box of 64 dimensions x 1 head x 8 tokens from shared memory to its place in the outputs, and the
+// waits for a thread's boxes: their reads done, all done.
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int x, int y, int z, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(map), "r"(x), "r"(y),
+               "r"(z), "r"(smem_addr(src))
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
 // Branches that a chunk rarely takes: their code goes out of the loop's straight line (instruction
 // fetches past them were a tenth of a chunk's time).
 __device__ __forceinline__ bool rare(bool taken) { return __builtin_expect(taken, 0); }
@@ -353,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
   int* vissued_slot = reinterpret_cast<int*>(smem + kOffMisc + 12);
   int* qissued_slot = reinterpret_cast<int*>(smem + kOffMisc + 16);
   const int G = p.group, TQ = p.tile_tokens;
-  const int span = (kShared ? 1 : kGroups) * TQ;  // new tokens of an item
+  constexpr int kTiles = kShared ? 1 : kGroups;  // of an item
+  const int span = kTiles * TQ;                  // new tokens of an item
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -364,10 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.qfull[i], 1);
-      mbar_init(&bars.qempty[i], kGroups);
+      mbar_init(&bars.qempty[i], kShared ? kGroups : 5 * kGroups);  // the issuers, and the softmax's warps
     }
     for (int g = 0; g < kGroups; ++g) {
       mbar_init(&bars.turn[g], 1);
+      mbar_init(&bars.staged[g], 4);
       for (int i = 0; i < 2; ++i) {
         mbar_init(bars.sfull(g, i), 1);
         mbar_init(bars.pfull(g, i), 4);
@@ -401,9 +426,6 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
     }
     const uint64_t pol_kv = policy_evict_normal();  // K/V: re-read by the sequence's other items
     const uint64_t pol_q = policy_evict_first();    // Q: read once
-    // this lane's query box of a tile: 8-row group lane / kBlocks, 64-column block lane % kBlocks
-    const int qrows = (lane / L::kBlocks) * 8, qhalf = lane % L::kBlocks;
-    const int qhead = qrows / TQ, qtok = qrows % TQ;
     int c = 0, j = 0;
     bool ok = true;
     WindowCursor cur;
@@ -413,20 +435,15 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
       const int qb = j % kQBufs;
       if (lane == 0) {
         ok = j < kQBufs || wait_role(&bars.qempty[qb], ((j / kQBufs) - 1) & 1, abort_flag, p.err, p.wait_limit_ns);
-        if (ok) mbar_arrive_expect_tx(&bars.qfull[qb], kQItem);
+        if (ok) mbar_arrive_expect_tx(&bars.qfull[qb], kTiles * L::kBlocks * G * TQ * 128);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) break;
       __syncwarp();
-      if (lane < 16 * L::kBlocks) {
-#pragma unroll
-        for (int g = 0; g < (kShared ? 1 : kGroups); ++g) {
-          // padding groups (past the G heads) read tokens outside the tensor: zeros
-          const int tok = qhead < G ? it.qrow0 + g * TQ + qtok : p.num_query_tokens;
-          const int head = it.g * G + min(qhead, G - 1);
-          tma_load_3d(smem + kOffQ + qb * kQItem + g * kQBytes + (lane / L::kBlocks) * kGroup + qhalf * 1024, &a.tq,
-                      qhalf * 64, head, tok, &bars.qfull[qb], pol_q);
-        }
+      if (lane < kTiles * L::kBlocks) {
+        const int tile = lane / L::kBlocks, half = lane % L::kBlocks;
+        tma_load_3d(smem + kOffQ + qb * kQItem + tile * kQBytes + half * kQBlock, &a.tq, half * 64, it.g * G,
+                    it.qrow0 + tile * TQ, &bars.qfull[qb], pol_q);
       }
       if (lane == 0) *qissued_slot = j + 1;
       // ---- K chunks (a stage is free once both tiles' QKs of its chunk completed) ----
@@ -473,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
     constexpr int kPer = kShared ? 2 : 1;  // chunks, and stages, of a step
     const int st0 = kShared ? g : 0;       // this issuer's stage of a step
     // descriptor bases; adding (byte offset >> 4) moves a descriptor's start address
-    const uint64_t dq0 = smem_desc(smem_addr(smem + kOffQ + (kShared ? 0 : g * kQBytes)), 16, kGroup, kLayoutSwizzle128);
+    const uint64_t dq0 = smem_desc(smem_addr(smem + kOffQ + (kShared ? 0 : g * kQBytes)), 16, 1024, kLayoutSwizzle128);
     const uint64_t dk0 = smem_desc(smem_addr(smem + st0 * kKVTile), 16, kGroup, kLayoutSwizzle128);
     const uint64_t dv0 = smem_desc(smem_addr(smem + kOffV + st0 * kKVTile), 1024, kGroup, kLayoutSwizzle128);
     const uint32_t sd = tmem + g * 256, od = sd + 128;
@@ -491,9 +508,12 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
     bool ok = true;
     auto issue_qk = [&](bool k_seen, bool pass) -> bool {  // k_seen: the K stage was already seen landed; pass: the turn
       const int qj = qcur.k, qb = qj % kQBufs, sb = qc & 1;
-      if (qk == 0 && !wait_all(&bars.qfull[qb], (qj / kQBufs) & 1)) return false;
-      if (!k_seen && !wait_all(&bars.kfull[qst + st0], qph)) return false;
       const bool first = qk == 0, last = qk == qn - 1;
+      // pairs: the item's queries wait for the outputs, and so for the other tile's last PV, of the item
+      // before the last: the turn goes first
+      if (kTurns && first && pass && lane == 0) mbar_arrive(&bars.turn[g]);
+      if (first && !wait_all(&bars.qfull[qb], (qj / kQBufs) & 1)) return false;
+      if (!k_seen && !wait_all(&bars.kfull[qst + st0], qph)) return false;
       const uint64_t dk = dk0 + ((qst * kKVTile) >> 4);
       const uint64_t dq = dq0 + ((qb * kQItem) >> 4);
       tc_fence_after();
@@ -501,8 +521,8 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk >> 2) * 1024 + (kk & 3) * 32) >> 4;
-          mma_f16(sd + sb * 64, dq + off, dk + off, idesc_qk, kk > 0);
-          if (kTurns && kk == 0 && pass) mbar_arrive(&bars.turn[g]);
+          mma_f16(sd + sb * 64, dq + (((kk >> 2) * kQBlock + (kk & 3) * 32) >> 4), dk + off, idesc_qk, kk > 0);
+          if (kTurns && kk == 0 && pass && !first) mbar_arrive(&bars.turn[g]);
         }
         mma_commit(bars.sfull(g, sb));
         mma_commit(&bars.kempty[qst + st0]);
@@ -562,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
     const int grp = warp / 4;                 // which tile of the pair
     const int t = threadIdx.x % 128;          // query row of the tile = TMEM lane
     const int wq = warp % 4;                  // lane quarter
-    const int head = t / TQ, tok = t % TQ;    // head-major rows
+    const int head = t % G, tok = t / G;
     const uint32_t lane_base = tmem + grp * 256 + (static_cast<uint32_t>(wq * 32) << 16);
     const uint32_t obuf = lane_base + 128;
     // scores are multiplied where the maximum is subtracted; by a scale that is not positive, which
@@ -573,7 +593,9 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
     int c = 0;
     bool ok = true;
     int prev_row = -1, prev_c = -1;
+    bool prev_full = false;
     float prev_l = 1.f, prev_m = 0.f;
+    int tiles_out = 0;  // tiles that left by TMA
     int joins = 0;  // shared tiles: hand-overs so far
     // this row's O, 16 vectors, the i-th at i ^ (t & 7): eight rows at once lie in different banks
     float4* join = reinterpret_cast<float4*>(smem + L::kOffJoin) + t * 16;
@@ -583,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
     auto pv_done = [&](int cc) -> bool {
       return __all_sync(0xffffffffu, wait_role(bars.pvdone(grp, cc & 1), (cc >> 1) & 1, abort_flag, p.err, p.wait_limit_ns));
     };
-    // 32 of a finished row's values from dimension q * 32 on, times inv, to its output.
+    // Shared tiles: 32 of a finished row's values from dimension q * 32 on, times inv, to its output.
     auto store_row = [&](int row, int q, const float* o, float inv) {
       if (p.out_f32) {
         float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + static_cast<size_t>(row) * D + q * 32);
@@ -600,10 +622,69 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
                               pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
       }
     };
+    // Pairs of tiles: piece q of a finished tile's rows, 32 values from dimension 32 q on, times inv. They go out
+    // through the place of the tile's queries, which lie there done with, in the same layout and in
+    // as many bytes a row (fp32: half a row at a time). A full tile of 16-bit rows leaves by TMA under the
+    // next item's chunks; others are stored by the warps, a row's 16-byte pieces side by side.
+    // (A lane storing its own row touches 32 lines at an instruction, 5,000 clocks an item: 238 us
+    // against 225 on four prompts of 1,000 to 2,000 new tokens, window 1,024, 64/8 heads. Shared
+    // tiles, whose few tokens fill no tile: 109 against 114 on 32 sequences with 3 to 8 new tokens.)
+    auto store_piece = [&](unsigned char* stage, int row, bool full, int q, const float* o, float inv) {
+      constexpr int kPieces = D * 2 / 16;  // 16-byte pieces of a staged row
+      auto place = [&](int r, int i) {     // piece i of row r of this warp
+        return reinterpret_cast<uint4*>(stage + i / 8 * kQBlock + (32 * wq + r) * 128 + ((i ^ r) & 7) * 16);
+      };
+      auto copy_out = [&](int skip, int bytes) {  // staged rows to `skip` of a row of `bytes`
+        __syncwarp();
+#pragma unroll 4
+        for (int r = lane / kPieces; r < 32; r += 32 / kPieces) {
+          const int to = __shfl_sync(0xffffffffu, row, r);
+          const int i = lane % kPieces;
+          const uint4 v = *place(r, i);
+          if (to >= 0) *reinterpret_cast<uint4*>(static_cast<unsigned char*>(p.out) + static_cast<size_t>(to) * bytes + skip + 16 * i) = v;
+        }
+        __syncwarp();
+      };
+      if (p.out_f32) {
+        const int at = q % (D / 64) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *place(lane, at + i) = make_uint4(__float_as_uint(o[4 * i] * inv), __float_as_uint(o[4 * i + 1] * inv),
+                                            __float_as_uint(o[4 * i + 2] * inv), __float_as_uint(o[4 * i + 3] * inv));
+        if ((q + 1) % (D / 64) == 0) copy_out(q / (D / 64) * D * 2, D * 4);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *place(lane, 4 * q + i) = make_uint4(pack2<T>(o[8 * i] * inv, o[8 * i + 1] * inv), pack2<T>(o[8 * i + 2] * inv, o[8 * i + 3] * inv),
+                                               pack2<T>(o[8 * i + 4] * inv, o[8 * i + 5] * inv), pack2<T>(o[8 * i + 6] * inv, o[8 * i + 7] * inv));
+        if (q < D / 32 - 1) return;
+        if (full) {
+          fence_proxy_async_smem();  // for the TMA's reads
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.staged[grp]);
+          const uint32_t parity = tiles_out++ & 1;
+          if (t == 0 && wait_role(&bars.staged[grp], parity, abort_flag, p.err, p.wait_limit_ns)) {  // row 0: the tile's first token and head
+#pragma unroll
+            for (int half = 0; half < L::kBlocks; ++half)
+              tma_store_3d(&a.to, half * 64, row % p.num_q_heads, row / p.num_q_heads, stage + half * kQBlock);
+            bulk_commit();
+          }
+        } else {
+          copy_out(0, D * 2);
+        }
+      }
+    };
+    // The staged rows have left for good: the place is the producer's.
+    auto release = [&](int item) {
+      bulk_wait_read();
+      fence_proxy_async_smem();  // its next writes are the TMA's
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.qempty[item % kQBufs]);
+    };
     // A finished item's output rows: O / l (O is final: its last PV was waited for).  Shared
     // tiles: the second warpgroup hands its rows' O, maxima and sums to the first, which joins
     // the two.  False: a wait ran out.
-    auto finish = [&](int row, float lsum, float top) -> bool {
+    auto finish = [&](int item, int row, bool full, float lsum, float top) -> bool {
       tc_fence_after();
       if constexpr (kShared) {
 #pragma unroll 1
@@ -648,29 +729,32 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
           }
         }
       } else {
+        unsigned char* stage = smem + kOffQ + item % kQBufs * kQItem + grp * kQBytes;
         const float inv = 1.f / lsum;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < D / 32; ++q) {
           float o[32];
           tmem_load32(obuf + q * 32, o);
-          if (row >= 0) store_row(row, q, o, inv);
+          store_piece(stage, row, full, q, o, inv);
         }
       }
       tc_fence_before();
       return true;
     };
 
+    int j = 0;
     WindowCursor cur;
-    for (cur.init(p, span); cur.valid() && ok; cur.advance()) {
+    for (cur.init(p, span); cur.valid() && ok; cur.advance(), ++j) {
       const Item it = unpack_item<kShared>(cur.cur, p);
       const int tile = kShared ? 0 : grp;
-      const bool row_valid = head < G && tok < it.ntok(tile);
+      const bool row_valid = tok < it.ntok(tile);
       const int qpos = row_valid ? it.pos0 + tile * TQ + tok : it.last;  // padding rows act as the last token
       const int out_row = row_valid ? (it.qrow0 + tile * TQ + tok) * p.num_q_heads + it.g * G + head : -1;
       // shared tiles: a warp of padding rows has no scores to weigh (its rows of O are never read)
       const bool idle = kShared && !__any_sync(0xffffffffu, row_valid);
       float m = -INFINITY, l = 0.f;  // max used for this row's probabilities, running row sum
-      for (int k = 0; k < it.nchunks / (kShared ? 2 : 1); ++k, ++c) {
+      const int steps = it.nchunks / (kShared ? 2 : 1);
+      for (int k = 0; k < steps; ++k, ++c) {
         const int sb = c & 1;
         const uint32_t sbuf = lane_base + sb * 64;
         if (rare(!__all_sync(0xffffffffu, mbar_test_wait(bars.sfull(grp, sb), (c >> 1) & 1))) &&
@@ -711,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
             ok = false;
             break;
           }
-          ok = finish(prev_row, prev_l, prev_m);
+          ok = finish(j - 1, prev_row, prev_full, prev_l, prev_m);
           if (!ok) break;
           prev_c = -1;
         }
@@ -780,14 +864,18 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bars.pfull(grp, sb));
+        // the item before's outputs have had two chunks' time to leave
+        if (!kShared && rare(k == min(1, steps - 1) && j > 0)) release(j - 1);
       }
       if (!ok) break;
       prev_row = out_row;
+      prev_full = it.ntok(tile) == TQ;
       prev_c = c - 1;
       prev_l = l;
       prev_m = m;
     }
-    if (ok && prev_c >= 0 && pv_done(prev_c)) finish(prev_row, prev_l, prev_m);
+    if (ok && prev_c >= 0 && pv_done(prev_c)) finish(j - 1, prev_row, prev_full, prev_l, prev_m);
+    if (!kShared) bulk_wait();
     __syncwarp();
   }
 
@@ -827,15 +915,16 @@ __global__ void __launch_bounds__(kThreads, 1) window_prefill_kernel(const __gri
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
 }
 
-// Queries [tokens][heads][head_dim] seen as 3-D (head_dim, heads, tokens); a box is 8
-// tokens x 64 dims of one head, landing as one swizzled 64-column block of an 8-row group.
-bool make_query_map(CUtensorMap* m, const void* q, uint32_t heads, uint32_t tokens, bool bf16, int head_dim) {
+// Queries, or 16-bit outputs, [tokens][heads][head_dim] seen as 3-D (head_dim, heads, tokens); a box is
+// 64 dimensions of a tile: its KV head's `group` query heads and `tile_tokens` tokens.
+bool make_query_map(CUtensorMap* m, const void* q, uint32_t heads, uint32_t tokens, uint32_t group, uint32_t tile_tokens, bool bf16,
+                    int head_dim) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t row = static_cast<cuuint64_t>(head_dim) * 2;
   cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), heads, tokens};
   cuuint64_t strides[2] = {row, static_cast<cuuint64_t>(heads) * row};
-  cuuint32_t box[3] = {64, 1, 8};
+  cuuint32_t box[3] = {64, group, tile_tokens};
   cuuint32_t es[3] = {1, 1, 1};
   return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(q),
             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -865,13 +954,14 @@ bool make_maps(PrefillArgs* args, bool bf16) {
   const uint64_t pool_rows = static_cast<uint64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
   return make_pool_map_uncached(&args->tk, p.k_cache, pool_rows, p.block_size, bf16, p.head_dim) &&
          make_pool_map_uncached(&args->tv, p.v_cache, pool_rows, p.block_size, bf16, p.head_dim) &&
-         make_query_map(&args->tq, p.q, p.num_q_heads, p.num_query_tokens, bf16, p.head_dim);
+         make_query_map(&args->tq, p.q, p.num_q_heads, p.num_query_tokens, p.group, p.tile_tokens, bf16, p.head_dim) &&
+         (p.out_f32 || make_query_map(&args->to, p.out, p.num_q_heads, p.num_query_tokens, p.group, p.tile_tokens, bf16, p.head_dim));
 }
 
 }  // namespace
 
 cudaError_t launch_window_prefill(const WindowPrefillParams& p, bool shared, int dtype, cudaStream_t stream) {
-  PrefillArgs args;
+  PrefillArgs args{};
   args.p = p;
   const bool bf16 = dtype == PKV_BF16;
   if (!make_maps(&args, bf16)) return cudaErrorInvalidValue;
