@@ -9,11 +9,13 @@
 //   shuffles at 4 heads instead of 8).
 //   products: lane = 4 dimensions (at head_dim 64 of one of two tokens at once); a token's weights
 //   are broadcast from shared memory, O stays in registers.
-// A K/V byte takes GM / 2 packed FMAs a lane per 4 bytes, half of the issue slots at copy bandwidth
-// with 16 heads.  (A row spread over all lanes, as in decode_simt.cu, spends a shuffle per two
-// FMAs on the sums: 113 us against 54 on 32 sequences, 64/8 heads, window 1,024.)
+// A K/V byte takes GM / 2 packed FMAs a lane per 4 bytes.  (A row spread over all lanes, as in
+// decode_simt.cu, spends a shuffle per two FMAs on the sums: 113 us against 50 on 32 sequences,
+// 64/8 heads, window 1,024.)
 //
-// Bound: HBM; for few sequences the chain launch -> length -> block table -> K/V -> join.
+// Bound: HBM with up to 8 heads (32 sequences of 0 to 6,000 tokens, window 1,021, 32/8 heads: 44 us, copy
+// bandwidth would take 36); instructions with 16 (32 sequences, 128/8 heads, window 1,024: 82 us,
+// 40); for few sequences the chain launch -> length -> block table -> K/V -> join.
 #include "window_rows.cuh"
 
 namespace pkv {
