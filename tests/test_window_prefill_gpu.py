@@ -199,3 +199,79 @@ def test_binding_refusals():
         with pytest.raises(pkv.PagedKVError):
             pkv.paged_attention_prefill_window(**{**good, **bad})
     assert pkv.device_error() == 0
+
+
+# Cases of the kernels that take whole tiles, full and partial ones: d, group, hkv, lens, new, window, sinks, kernel
+TILES = [(128, 8, 2, [3000, 40], [2700, 3], 600, 5, "pairs"), (64, 5, 4, [2500, 800], [2400, 301], 129, 70, "pairs"),
+         (128, 7, 2, [1200, 900], [600, 31], 600, 0, "shared"), (64, 16, 2, [2500], [300], 700, 33, "shared")]
+
+
+def tiles(i, dtype="bf16"):
+    d, group, hkv, lens, new, window, sinks, kernel = TILES[i]
+    c = Case(314_290 + i, list(lens), window, sinks, group * hkv, hkv, d, 16, dtype, new=new)
+    assert kernel_of(c) == kernel
+    return c
+
+
+@pytest.mark.parametrize("i", range(len(TILES)))
+def test_tiles_with_no_scale_and_a_negative_one(i):
+    c = tiles(i)
+    for c.scale in (0.0, -0.4):
+        c.check(run(c))
+    assert pkv.device_error() == 0
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("i", range(len(TILES)))
+def test_rows_behind_the_last_sequence_and_of_a_bad_one_stay(i, out_dtype):
+    c = tiles(i)
+    ref, tokens = c.reference(), c.q.shape[0]
+    c.q = torch.cat([c.q, torch.full((77, *c.q.shape[1:]), float("nan"), dtype=c.q.dtype)])
+    out = run(c, out_dtype)
+    c.check(out[:tokens], ref)
+    assert (out[tokens:] == 7).all() and pkv.device_error() == 0
+    good, first = out.clone(), c.new[0]
+    c.lens[0] = first - 1                                    # fewer than its new tokens
+    out = run(c, out_dtype)
+    assert pkv.device_error() == 5 and (out[:first] == 7).all() and torch.equal(out[first:], good[first:])
+
+
+@pytest.mark.parametrize("i", range(len(TILES)))
+def test_a_query_that_is_not_a_number_stays_alone(i):
+    c = tiles(i, "f16")
+    good = run(c).clone()
+    for tok, head, x in ((0, 1, float("nan")), (200, 0, float("inf")), (c.q.shape[0] - 1, c.hq - 1, float("nan"))):
+        keep = c.q.clone()
+        c.q[tok, head, 5] = x
+        out = run(c)
+        assert out[tok, head].isnan().all()
+        out[tok, head] = good[tok, head]
+        assert torch.equal(out, good)
+        c.q = keep
+
+
+@pytest.mark.parametrize("i", range(len(TILES)))
+def test_tiles_captured_and_replayed_on_two_streams(i):
+    c = tiles(i).cuda()
+    outs = [torch.empty_like(c.g_q) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in outs]
+    graphs = []
+    run(c)
+    torch.cuda.synchronize()
+    for out, s in zip(outs, streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            pkv.paged_attention_prefill_window(c.g_q, c.g_k, c.g_v, c.g_tables, c.g_lens, c.g_start, c.scale, out,
+                                               window=c.window, sinks=c.sinks, max_context_len=c.max_len)
+    for step in range(2):
+        c.q = torch.randn(c.q.shape, generator=torch.Generator().manual_seed(step)).to(c.q.dtype)
+        c.g_q.copy_(c.q)
+        torch.cuda.synchronize()
+        for _ in range(3):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        ref = c.reference()
+        for out in outs:
+            c.check(out, ref)
