@@ -816,9 +816,18 @@ def paged_kv_append_rotary(q, k, v, positions, slot_mapping, k_cache, v_cache, q
 
 # ---- sliding windows
 
-def _window_args(q, k_cache, v_cache, block_tables, context_lens, out, more):
+_INT32_MAX = 2 ** 31 - 1
+
+
+def _tokens(n: int) -> int:
+    """A window or a number of sinks as 32 bits hold it (ctypes would keep the low 32 bits of a
+    larger number): past the longest sequence either way, or negative for the library to refuse."""
+    return max(-1, min(n, _INT32_MAX))
+
+
+def _window_args(q, k_cache, v_cache, block_tables, context_lens, out, more, max_context_len):
     """Checks that both windowed calls make; (device, descriptor reference, out's dtype code,
-    rows and heads of q, sequences, table width)."""
+    rows and heads of q, sequences, table width, bound of the lengths)."""
     device = _one_device(q, k_cache, v_cache, block_tables, context_lens, out, more)
     dtype, pool, rows, tables = k_cache.dtype, k_cache.shape, q.shape, block_tables.shape
     desc, desc_ref = _desc_of(pool, dtype)
@@ -832,26 +841,29 @@ def _window_args(q, k_cache, v_cache, block_tables, context_lens, out, more):
     S = context_lens.numel()
     if len(tables) != 2 or tables[0] != S:
         raise PagedKVError(1, "block_tables must be [S, max_blocks]")
-    return device, desc_ref, _dtype_code(out, "out"), rows[0], rows[1], S, tables[1]
+    if max_context_len is None:
+        max_context_len = int(context_lens.max()) if S else 0
+    elif not -1 <= max_context_len <= _INT32_MAX:
+        raise PagedKVError(1, f"max_context_len {max_context_len}")
+    return device, desc_ref, _dtype_code(out, "out"), rows[0], rows[1], S, tables[1], max_context_len
 
 
 def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, out, *, window: int,
                                   sinks: int = 0, max_context_len: int | None = None) -> torch.Tensor:
     """out[s, h] = softmax(scale * q[s, h] . K_j) V_j over the last `window` of the
-    context_lens[s] tokens of s and its first `sinks`.
+    context_lens[s] tokens of s and its first `sinks` (of any size; past the sequence they change nothing).
 
     Tensors as in paged_attention_decode; table entries of blocks that hold no such token are
     not read (-1 will do).  max_context_len: host upper bound on context_lens (computed with a
     device sync when omitted).  One kernel, no workspace.
     """
-    device, desc_ref, out_code, T, Hq, S, width = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, None)
+    device, desc_ref, out_code, T, Hq, S, width, longest = _window_args(q, k_cache, v_cache, block_tables, context_lens, out,
+                                                                        None, max_context_len)
     if T != S:
         raise PagedKVError(1, "context_lens must be [S]")
-    if max_context_len is None:
-        max_context_len = int(context_lens.max()) if S else 0
     _call(library().paged_attention_decode_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          block_tables.data_ptr(), width, context_lens.data_ptr(), S, Hq, max_context_len, window, sinks, float(scale),
-          out.data_ptr(), out_code, desc_ref)
+          block_tables.data_ptr(), width, context_lens.data_ptr(), S, Hq, longest, _tokens(window), _tokens(sinks),
+          float(scale), out.data_ptr(), out_code, desc_ref)
     return out
 
 
@@ -860,14 +872,13 @@ def paged_attention_prefill_window(q, k_cache, v_cache, block_tables, context_le
     """paged_attention_prefill with a window: the new token at position p attends to the
     positions j <= p with j > p - window or j < sinks.  Tensors as there; table entries of blocks
     that hold no token attended to are not read.  No workspace."""
-    device, desc_ref, out_code, T, Hq, S, width = _window_args(q, k_cache, v_cache, block_tables, context_lens, out, query_start)
+    device, desc_ref, out_code, T, Hq, S, width, longest = _window_args(q, k_cache, v_cache, block_tables, context_lens, out,
+                                                                        query_start, max_context_len)
     if query_start.dtype is not torch.int32 or query_start.numel() != S + 1:
         raise PagedKVError(1, "query_start must be int32 [S+1]")
-    if max_context_len is None:
-        max_context_len = int(context_lens.max()) if S else 0
     _call(library().paged_attention_prefill_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          block_tables.data_ptr(), width, context_lens.data_ptr(), query_start.data_ptr(), S, Hq, T, max_context_len, window,
-          sinks, float(scale), out.data_ptr(), out_code, desc_ref)
+          block_tables.data_ptr(), width, context_lens.data_ptr(), query_start.data_ptr(), S, Hq, T, longest, _tokens(window),
+          _tokens(sinks), float(scale), out.data_ptr(), out_code, desc_ref)
     return out
 
 
