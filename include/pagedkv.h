@@ -416,6 +416,30 @@ pkv_status paged_attention_prefill_window(const void* q, const void* k_cache, co
                                           int32_t window, int32_t sinks, float scale, void* out, int32_t out_dtype,
                                           const pkv_cache_desc* cache, void* stream);
 
+/* Kernels of a windowed prefill. */
+typedef enum {
+  PKV_WINDOW_ROWS = 0,         /* up to 16 query rows of a KV head, as in windowed decode: a few new tokens */
+  PKV_WINDOW_SHARED_TILES = 1, /* tiles of up to 128 query rows, two halves of their tokens at once */
+  PKV_WINDOW_TILE_PAIRS = 2    /* two such tiles over the same tokens: long chunks */
+} pkv_window_kernel;
+
+/* What paged_attention_prefill_window will do for these sizes. */
+typedef struct {
+  int32_t kernel;          /* pkv_window_kernel */
+  int32_t tokens_per_item; /* new tokens of a sequence that one item covers at most, for one KV head */
+  int32_t ctas_per_item;   /* CTAs that share an item's tokens (0: there is nothing to do) */
+} pkv_window_plan;
+
+/*
+ * paged_attention_prefill_window_plan -- fill *out with the plan that
+ * paged_attention_prefill_window follows for these sizes (host only, no device work): the kernel
+ * with the shortest estimate for sequences that share the new tokens out evenly.  Errors as the
+ * call's checks of its sizes.
+ */
+pkv_status paged_attention_prefill_window_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_query_tokens,
+                                               int32_t max_context_len, int32_t window, int32_t sinks,
+                                               const pkv_cache_desc* cache, pkv_window_plan* out);
+
 /* ----------------------------------------------------------------------------------
  * 4-bit caches.  The pages have no counterpart: a smaller form of the same cache, for more
  * context in the same memory.

@@ -27,6 +27,7 @@ and, for models with rotary positions and sliding windows:
 * :func:`rotary_frequencies`     -- frequencies, also of rotations scaled for long contexts
 * :func:`paged_attention_decode_window`, :func:`paged_attention_prefill_window` -- attention over
   the last tokens and the first few
+* :func:`paged_attention_prefill_window_plan` -- the kernel that the latter takes
 
 If the library has not been built the import still succeeds, but every call raises:
 there is no CPU fallback.
@@ -51,7 +52,7 @@ __all__ = [
     "paged_kv4_append", "paged_kv4_expand", "paged_attention_decode_kv4", "paged_attention_decode_kv4_workspace_bytes",
     "paged_attention_weights", "paged_attention_weights_workspace_bytes", "paged_kv_evict",
     "paged_qk_rotary", "paged_kv_append_rotary", "rotary_frequencies",
-    "paged_attention_decode_window", "paged_attention_prefill_window",
+    "paged_attention_decode_window", "paged_attention_prefill_window", "paged_attention_prefill_window_plan",
     "PreparedCall", "prepare_kv_append", "prepare_block_copy", "prepare_attention_decode", "set_wait_limit",
 ]
 
@@ -87,6 +88,10 @@ class DecodePlan(ctypes.Structure):
     _fields_ = [("path", ctypes.c_int32), ("partition_tokens", ctypes.c_int32),
                 ("max_partitions", ctypes.c_int32), ("kernel_launches", ctypes.c_int32),
                 ("workspace_bytes", ctypes.c_size_t), ("kv_heads_per_item", ctypes.c_int32)]
+
+
+class WindowPlan(ctypes.Structure):
+    _fields_ = [("kernel", ctypes.c_int32), ("tokens_per_item", ctypes.c_int32), ("ctas_per_item", ctypes.c_int32)]
 
 
 class RotaryScaling(ctypes.Structure):
@@ -142,6 +147,7 @@ def library():
                                               desc_p, vp],
             "paged_attention_prefill_window": [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i32, ctypes.c_float,
                                                vp, i32, desc_p, vp],
+            "paged_attention_prefill_window_plan": [i32, i32, i32, i32, i32, i32, desc_p, ctypes.POINTER(WindowPlan)],
             "paged_kv_gather": [vp, vp, vp, i32, vp, i32, i32, vp, vp, desc_p, vp],
             "paged_block_swap_out": [vp, i32, vp, vp, vp, vp, desc_p, vp],
             "paged_attention_prefill": [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, ctypes.c_float, vp, i32,
@@ -880,6 +886,19 @@ def paged_attention_prefill_window(q, k_cache, v_cache, block_tables, context_le
           block_tables.data_ptr(), width, context_lens.data_ptr(), query_start.data_ptr(), S, Hq, T, longest, _tokens(window),
           _tokens(sinks), float(scale), out.data_ptr(), out_code, desc_ref)
     return out
+
+
+_WINDOW_KERNELS = ("rows", "shared_tiles", "tile_pairs")
+
+
+def paged_attention_prefill_window_plan(num_seqs, num_q_heads, num_query_tokens, max_context_len, k_cache, *, window: int,
+                                        sinks: int = 0) -> dict:
+    """The kernel ("rows", "shared_tiles" or "tile_pairs"), new tokens per item and CTAs per item that
+    paged_attention_prefill_window uses for these sizes."""
+    desc, plan = cache_desc(k_cache), WindowPlan()
+    _check(library().paged_attention_prefill_window_plan(num_seqs, num_q_heads, num_query_tokens, max_context_len,
+                                                         _tokens(window), _tokens(sinks), ctypes.byref(desc), ctypes.byref(plan)))
+    return dict(kernel=_WINDOW_KERNELS[plan.kernel], tokens_per_item=plan.tokens_per_item, ctas_per_item=plan.ctas_per_item)
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:

@@ -139,8 +139,8 @@ int rows_cluster(int64_t items, int64_t tokens) {
 }
 
 struct PrefillPlan {
-  enum Kernel { kRows, kShared, kPairs } kernel;
-  int cluster;  // kRows
+  pkv_window_kernel kernel;
+  int cluster;  // CTAs that share an item (rows; 1 for the others)
 };
 
 // Which kernel a windowed prefill takes: the one with the shortest estimate, for sequences that
@@ -165,12 +165,29 @@ PrefillPlan plan_prefill(const Args& a) {
   const double rows = 10. + (a.cache->head_dim == 64 ? 0.65e-3 : 0.85e-3) * static_cast<double>(row_groups * H * (keys_of(a, per) / 16 + 1));
   const double shared = 12. + 2.1 * static_cast<double>(rounds(groups(tq) * H) * (keys_of(a, tq) / 128 + 1));
   const double pairs = 10. + 1.55 * static_cast<double>(rounds(groups(2 * tq) * H) * (keys_of(a, 2 * tq) / 64 + 1));
-  PrefillPlan plan{shared < pairs ? PrefillPlan::kShared : PrefillPlan::kPairs, 1};
+  PrefillPlan plan{shared < pairs ? PKV_WINDOW_SHARED_TILES : PKV_WINDOW_TILE_PAIRS, 1};
   if (rows < std::min(shared, pairs) && T / per + S <= 65535) {  // a grid's third dimension
-    plan.kernel = PrefillPlan::kRows;
+    plan.kernel = PKV_WINDOW_ROWS;
     plan.cluster = rows_cluster(row_groups * H, keys_of(a, per));
   }
   return plan;
+}
+
+// What a windowed prefill refuses by its sizes: before those that leave nothing to do return, and after.
+pkv_status check_prefill(const Args& a) {
+  if (a.num_seqs < 0 || a.num_seqs > (1 << 20)) return fail(PKV_ERR_INVALID_ARG, "num_seqs %d", a.num_seqs);
+  if (pkv_status st = check_sizes(a)) return st;
+  if (a.cache->dtype == PKV_F32) return fail(PKV_ERR_UNSUPPORTED, "windowed prefill needs f16 or bf16 caches");
+  if (a.cache->num_kv_heads > 4095)  // an item packs the KV head into 12 bits
+    return fail(PKV_ERR_UNSUPPORTED, "prefill supports at most 4095 KV heads (%d)", a.cache->num_kv_heads);
+  return PKV_OK;
+}
+pkv_status check_prefill_counts(const Args& a) {
+  if (static_cast<int64_t>(a.cache->num_blocks) * a.cache->num_kv_heads * a.cache->block_size > (int64_t{1} << 30))
+    return fail(PKV_ERR_UNSUPPORTED, "pool too large for 32-bit row coordinates");
+  if (window_prefill_items(prefill_params(a), true) > (int64_t{1} << 30))
+    return fail(PKV_ERR_UNSUPPORTED, "too many (new tokens, KV head) items");
+  return PKV_OK;
 }
 
 }  // namespace
@@ -205,26 +222,45 @@ pkv_status paged_attention_prefill_window(const void* q, const void* k_cache, co
   const Args a{q,           k_cache,          v_cache,         block_tables, max_blocks_per_seq, context_lens, query_start,
                num_seqs,    num_q_heads,      num_query_tokens, max_context_len, window,         sinks,        scale,
                out,         out_dtype,        cache};
-  if (num_seqs < 0 || num_seqs > (1 << 20)) return fail(PKV_ERR_INVALID_ARG, "num_seqs %d", num_seqs);
-  if (pkv_status st = check_sizes(a)) return st;
-  if (cache->dtype == PKV_F32) return fail(PKV_ERR_UNSUPPORTED, "windowed prefill needs f16 or bf16 caches");
-  if (cache->num_kv_heads > 4095)  // an item packs the KV head into 12 bits
-    return fail(PKV_ERR_UNSUPPORTED, "prefill supports at most 4095 KV heads (%d)", cache->num_kv_heads);
+  if (pkv_status st = check_prefill(a)) return st;
   if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
   if (!query_start) return fail(PKV_ERR_INVALID_ARG, "query_start is NULL");
   if (pkv_status st = check_pointers(a)) return st;
-  if (static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size > (int64_t{1} << 30))
-    return fail(PKV_ERR_UNSUPPORTED, "pool too large for 32-bit row coordinates");
+  if (pkv_status st = check_prefill_counts(a)) return st;
   WindowPrefillParams p = prefill_params(a);
-  if (window_prefill_items(p, true) > (int64_t{1} << 30))
-    return fail(PKV_ERR_UNSUPPORTED, "too many (new tokens, KV head) items");
   if (pkv_status st = device_flag(&p.err)) return st;
   const PrefillPlan plan = plan_prefill(a);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = plan.kernel == PrefillPlan::kRows
+  const cudaError_t e = plan.kernel == PKV_WINDOW_ROWS
                             ? launch_window_rows(rows_params(a, plan.cluster, p.err), cache->dtype, s)
-                            : launch_window_prefill(p, plan.kernel == PrefillPlan::kShared, cache->dtype, s);
+                            : launch_window_prefill(p, plan.kernel == PKV_WINDOW_SHARED_TILES, cache->dtype, s);
   return e == cudaSuccess ? PKV_OK : cuda_fail(e, "windowed prefill launch");
+}
+
+pkv_status paged_attention_prefill_window_plan(int32_t num_seqs, int32_t num_q_heads, int32_t num_query_tokens,
+                                               int32_t max_context_len, int32_t window, int32_t sinks,
+                                               const pkv_cache_desc* cache, pkv_window_plan* out) {
+  if (!out) return fail(PKV_ERR_INVALID_ARG, "plan output is NULL");
+  Args a{};
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_query_tokens = num_query_tokens;
+  a.max_context_len = max_context_len;
+  a.window = window;
+  a.sinks = sinks;
+  a.cache = cache;
+  if (pkv_status st = check_prefill(a)) return st;
+  *out = pkv_window_plan{PKV_WINDOW_ROWS, 0, 0};
+  if (num_seqs == 0 || num_query_tokens == 0) return PKV_OK;
+  if (pkv_status st = check_prefill_counts(a)) return st;
+  const PrefillPlan plan = plan_prefill(a);
+  const int per_tile = prefill_tile_tokens(num_q_heads / cache->num_kv_heads);
+  out->kernel = plan.kernel;
+  out->tokens_per_item = plan.kernel == PKV_WINDOW_ROWS           ? kRowsPerGroup / (num_q_heads / cache->num_kv_heads)
+                         : plan.kernel == PKV_WINDOW_SHARED_TILES ? per_tile
+                                                                  : 2 * per_tile;
+  out->ctas_per_item = plan.cluster;
+  return PKV_OK;
 }
 
 }  // extern "C"
