@@ -345,8 +345,10 @@ pkv_status paged_rotary_frequencies(double* inv_freq, int32_t rotary_dim, double
  *   y = x * weight / sqrt(mean(x^2) + eps)  (y = x where the weight is NULL);
  *   each pair (y_a, y_b) of the layout becomes (y_a c - y_b s, y_b c + y_a s), with
  *   c = factor cos(positions[t] * inv_freq[i]), s = factor sin(positions[t] * inv_freq[i]);
- * the other dimensions stay y.  fp32 throughout, but for the angle, which is good to 2^-31
- * turns at any position for frequencies up to 1; one rounding at the end (RNE).
+ * the other dimensions stay y.  fp32 throughout, one rounding at the end (RNE).  The angle is
+ * taken modulo whole turns in integers, good to 2^-31 turns at any position for frequencies up to
+ * 1; what is left of it past the nearest quarter turn is then rounded to fp32, by 2^-28 turns at
+ * most.
  * Negative positions are padding: nothing of the token is written.
  *
  * q, k, q_out, k_out: device, dtype f32, f16 or bf16; a token's heads lie one after the

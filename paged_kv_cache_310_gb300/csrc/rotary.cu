@@ -14,8 +14,9 @@
 // below 2^-32 turns up to position 2^31 (for frequencies up to 1; larger ones lose as many bits
 // more as they are larger).
 // The nearest quarter turn goes off as an integer too, so that only the rest, at most 1/8
-// turn, is rounded to fp32.  No range reduction of large arguments, no table of positions
-// (a table is a dependent load of 512 bytes a token).
+// turn, is rounded to fp32: by 2^-28 turns at most (half a step of 2^-27 from 1/16 turn on).  No
+// range reduction of large arguments, no table of positions (a table is a dependent load of 512
+// bytes a token).
 //
 // Layout.  A row is L = D / (2 V) lanes of two 16-byte vectors (V values each).  A lane
 // holds both halves of its pairs: half layout: vectors l and l + R/2V, interleaved: 2l and
