@@ -129,9 +129,13 @@ int64_t keys_of(const Args& a, int64_t span) {
 constexpr int64_t kSms = 152;
 
 // CTAs that share the tokens of one of `items` (columns, KV head) in the kernels of
-// window_rows.cuh: as many as the GPU holds at once (three an SM), of 64 tokens or more each.
+// window_rows.cuh: up to three an SM in all, of 64 tokens or more each.
 // Clusters start slowly -- about 20 ns each at 2 CTAs, 200 at 8 -- so many items go unshared
-// (64 sequences, 64/8 heads, D 64, window 128: 10 us with one CTA, 25 with two).
+// (64 sequences, 64/8 heads, D 64, window 128: 10 us with one CTA, 25 with two).  Three whatever an SM
+// holds: at four of the 16-bit kernel at D 64, which it does hold, 19 sequences, 64/8 heads, window
+// 1,020 take 25 us instead of 18; at two of the f32 kernel with 16 heads at D 128, the most that it
+// holds, 28 sequences, 96/8 heads take 264 us instead of 213 under a window of 4,092, though 31 instead
+// of 41 under one of 252.
 int rows_cluster(int64_t items, int64_t tokens) {
   int size = 1;
   while (size < 8 && 2 * size * items <= 3 * kSms && tokens > 64 * size) size *= 2;

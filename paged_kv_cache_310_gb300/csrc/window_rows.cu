@@ -42,6 +42,7 @@ struct Rows {
   static constexpr int kOffQ = kOffFactor + kCols * 8 * kWarps * 4;
   static constexpr bool kSharedQ = NT > 1;                  // queries in shared memory, not in registers
   static constexpr int kBytes = kOffQ + (kSharedQ ? kCols * D * 2 : 0);
+  static_assert(kCtas * (kBytes + kCtaReserve) <= kSmShared, "shared memory");
 };
 
 template <typename T>

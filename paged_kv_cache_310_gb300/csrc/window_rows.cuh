@@ -21,6 +21,8 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kSmShared = 228 * 1024;  // shared memory of an SM, and what a CTA takes of it beyond its own
+constexpr int kCtaReserve = 1024;
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");

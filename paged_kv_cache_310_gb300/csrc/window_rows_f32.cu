@@ -37,6 +37,11 @@ struct RowsF32 {
   static constexpr int kOffQ = (kOffFactor + GM * 8 * kWarps * 4 + 15) / 16 * 16;  // [GM][4][kQuarter]
   static constexpr int kOffWeights = kOffQ + GM * 4 * kQuarter * 4;        // [kWarps][kTile][GM]
   static constexpr int kBytes = kOffWeights + kWarps * kTile * GM * 4;
+  // CTAs of an SM, by shared memory: two of 16 heads at head_dim 128, three else.  (Registers for three
+  // there, 168 instead of 248: 86 us against 80 on 32 sequences, 128/8 heads, window 1,020; 135
+  // against 117 on 57; 471 against 401 on 57, 96/8 heads, window 4,092.)
+  static constexpr int kCtas = 3 * (kBytes + kCtaReserve) <= kSmShared ? 3 : 2;
+  static_assert(kCtas * (kBytes + kCtaReserve) <= kSmShared, "shared memory");
 };
 
 // Totals of each v[h] over the four lanes that differ in bits 3 and 4 of their number; returns those
@@ -72,7 +77,7 @@ __device__ __forceinline__ void quarter_sums(float (&v)[GM], float (&out)[kHeads
 }
 
 template <int D, int GM>
-__global__ void __launch_bounds__(kThreads, 3) window_rows_f32_kernel(const __grid_constant__ WindowRowsParams p) {
+__global__ void __launch_bounds__(kThreads, (RowsF32<D, GM>::kCtas)) window_rows_f32_kernel(const __grid_constant__ WindowRowsParams p) {
   using R = RowsF32<D, GM>;
   using Stream = TileStream<float, D, kTile, R::kStages>;
   static_assert(Stream::kRing == R::kRing, "ring");
