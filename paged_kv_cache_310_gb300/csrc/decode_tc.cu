@@ -1063,9 +1063,9 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
 // all-zero output here; lengths outside [0, max_parts * part_tokens] set the flag.
 //
 // Launched as a programmatic dependent: the kernel before on the stream may still run (the
-// library's appends, expansion and attention weights let it start).  Such a kernel has itself
-// waited for all that came before it, and none writes context lengths, so these are read and
-// counted at once.  What is written here may lie in memory that the kernel before still reads
+// library's appends, rotations, expansion, attention weights and windowed attention let it
+// start).  Such a kernel has itself waited for all that came before it, and none writes context
+// lengths, so these are read and counted at once.  What is written here may lie in memory that the kernel before still reads
 // or writes -- the caller's workspace and output can be buffers that its call was given, or
 // freed ones -- so the first write comes after the wait, which also makes the decode kernel's
 // wait on this grid cover the kernel before.
