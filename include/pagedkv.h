@@ -321,8 +321,20 @@ typedef enum {
   PKV_ROTARY_LINEAR = 1,  /* positions interpolated: every frequency divided by `factor` */
   PKV_ROTARY_BASE = 2,    /* base * factor^(rotary_dim / (rotary_dim - 2)): the lowest frequency divided by `factor` */
   PKV_ROTARY_PARTS = 3    /* by turns within original_len: fast_turns or more are kept, slow_turns or fewer divided by
-                             `factor`, linear in between; cosines and sines times 0.1 ln(factor) + 1 */
+                             `factor`, linear in the turns in between; cosines and sines times 0.1 ln(factor) + 1 */
 } pkv_rotary_rule;
+
+/*
+ * A checkpoint wants the rule that it was trained with, and rules by parts are not all alike:
+ *  - many blend linearly in the dimension's index i, between the (rounded) indices at which
+ *    fast_turns and slow_turns are reached, where PKV_ROTARY_PARTS blends linearly in the turns.  In
+ *    between the two differ by up to a factor of 3 (rotary_dim 128, base 10,000, factor 16, 4,096
+ *    original tokens, turns 32 and 1).  No rule here gives those frequencies.
+ *  - some blend as PKV_ROTARY_PARTS does (customarily with turns 4 and 1) but leave cosines and sines
+ *    alone: take the frequencies, and 1 for pkv_rotary.factor.
+ * pkv_rotary.inv_freq and factor take any values: where none of the rules is the checkpoint's,
+ * compute them by its own.
+ */
 
 typedef struct {
   int32_t rule;                   /* pkv_rotary_rule */

@@ -718,7 +718,12 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str |
     base^(-2 i / rotary_dim), and the factor of cosines and sines.  scaling for contexts
     `factor` times as long: "linear" divides every frequency, "base" raises the base so that
     the lowest one is divided, "parts" divides those that make up to slow_turns within
-    original_len, keeps those with fast_turns or more, and blends in between."""
+    original_len, keeps those with fast_turns or more, and blends in between, linearly in the turns.
+
+    A checkpoint wants the rule it was trained with.  Many rules by parts blend linearly in the
+    dimension's index instead, whose frequencies differ from these by up to a factor of 3, and some
+    (fast_turns 4) leave cosines and sines alone (pass factor=1 to the calls then).  The calls take
+    any frequencies and factor: compute those of another rule by its own definition."""
     if scaling not in _ROTARY_RULES:
         raise PagedKVError(1, f"scaling {scaling!r}")
     out = torch.empty(max(0, int(rotary_dim)) // 2, dtype=torch.float64)
