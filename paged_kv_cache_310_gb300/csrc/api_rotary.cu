@@ -175,6 +175,7 @@ pkv_status paged_rotary_frequencies(double* inv_freq, int32_t rotary_dim, double
   if (rule == PKV_ROTARY_BASE) {
     if (rotary_dim == 2) return fail(PKV_ERR_INVALID_ARG, "a base cannot scale the one frequency of rotary_dim 2");
     base *= std::pow(by, rotary_dim / (rotary_dim - 2.));
+    if (!std::isfinite(base)) return fail(PKV_ERR_INVALID_ARG, "the base scaled by a factor of %g is not finite", by);
   }
   if (rule == PKV_ROTARY_PARTS &&
       !(scaling->original_len > 0. && std::isfinite(scaling->original_len) && scaling->slow_turns >= 0. &&
