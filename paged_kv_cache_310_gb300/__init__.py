@@ -709,6 +709,7 @@ def paged_kv_evict(weights, block_tables, context_lens, keep_lens, new_tables, k
 
 # ---- rotary positions
 
+_INT32_MAX = 2 ** 31 - 1
 _ROTARY_RULES = {None: 0, "linear": 1, "base": 2, "parts": 3}
 
 
@@ -726,7 +727,9 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, *, scaling: str |
     any frequencies and factor: compute those of another rule by its own definition."""
     if scaling not in _ROTARY_RULES:
         raise PagedKVError(1, f"scaling {scaling!r}")
-    out = torch.empty(max(0, int(rotary_dim)) // 2, dtype=torch.float64)
+    if not 0 < rotary_dim <= _INT32_MAX:
+        raise PagedKVError(1, f"rotary_dim {rotary_dim}")
+    out = torch.empty(rotary_dim // 2, dtype=torch.float64)
     rule = RotaryScaling(_ROTARY_RULES[scaling], factor, original_len, fast_turns, slow_turns)
     f = ctypes.c_float()
     _check(library().paged_rotary_frequencies(out.data_ptr() or 8, rotary_dim, base, ctypes.byref(rule), ctypes.byref(f)))
@@ -826,9 +829,6 @@ def paged_kv_append_rotary(q, k, v, positions, slot_mapping, k_cache, v_cache, q
 
 
 # ---- sliding windows
-
-_INT32_MAX = 2 ** 31 - 1
-
 
 def _tokens(n: int) -> int:
     """A window or a number of sinks as 32 bits hold it (ctypes would keep the low 32 bits of a
