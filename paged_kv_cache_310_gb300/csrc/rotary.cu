@@ -139,14 +139,16 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const __grid_consta
   for (int u = 0; u < kAhead; ++u) load(u, first + u * step, p.num_q_heads);
 
   const int position = p.positions[t];
+  const int64_t slot = p.slots ? p.slots[t] : 0;
+  if (position < 0 || slot < 0) return;  // padding
   int64_t place = 0;  // in the pools: the row of the token's first KV head
   if (p.slots) {
-    const int64_t slot = p.slots[t];
-    if (slot >= p.num_slots) set_error(p.err, kErrIndex);
-    if (slot < 0 || slot >= p.num_slots) return;
+    if (slot >= p.num_slots) {
+      set_error(p.err, kErrIndex);
+      return;
+    }
     place = slot / p.block_size * p.block_size * p.num_kv_heads + slot % p.block_size;
   }
-  if (position < 0) return;
   for (int n = lane; n < p.rotary_dim / 2; n += 32) {
     const double freq = p.inv_freq[n];
     const float2 cs = cos_sin(turns_of(freq), static_cast<uint32_t>(position));
