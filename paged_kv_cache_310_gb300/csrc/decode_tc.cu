@@ -1064,11 +1064,13 @@ __global__ void __launch_bounds__(TcRoles<GM>::kThreads, 1) decode_tc_kernel(con
 //
 // Launched as a programmatic dependent: the kernel before on the stream may still run (the
 // library's appends, rotations, expansion, attention weights and windowed attention let it
-// start).  Such a kernel has itself waited for all that came before it, and none writes context
-// lengths, so these are read and counted at once.  What is written here may lie in memory that the kernel before still reads
-// or writes -- the caller's workspace and output can be buffers that its call was given, or
-// freed ones -- so the first write comes after the wait, which also makes the decode kernel's
-// wait on this grid cover the kernel before.
+// start), or has ended without its writes being visible yet, and it may be the one that writes the
+// context lengths.  So lengths that are read before the wait are a guess: they are counted, read
+// again after the wait, and counted again where one differs.  (Counted after the wait alone: 159.5 us
+// a call instead of 158.8 on 64 sequences, 32 heads, bf16.)  What is written here may lie in
+// memory that the kernel before still reads or writes -- the caller's workspace and output can
+// be buffers that its call was given, or freed ones -- so the first write comes after the wait,
+// which also makes the decode kernel's wait on this grid cover the kernel before.
 constexpr int kListThreads = 1024;
 constexpr int kMaxChunkCounts = kTcMaxPartition / kChunk;
 
@@ -1079,35 +1081,50 @@ __global__ void __launch_bounds__(kListThreads) work_list_kernel(const __grid_co
   __shared__ int next[kMaxChunkCounts + 1];
   const int full_chunks = p.part_tokens / kChunk;
   const int H = p.num_kv_heads / p.heads_per_item;  // items per (sequence, partition)
-  for (int i = threadIdx.x; i <= kMaxChunkCounts; i += kListThreads) hist[i] = 0;
-  __syncthreads();
-  for (int s = threadIdx.x; s < p.num_seqs; s += kListThreads) {
-    const int L = p.context_lens[s];
-    if (L < 0 || L > p.max_parts * p.part_tokens) {
-      set_error(p.err, kErrLength);
-      continue;
-    }
+  auto counts = [&](int L) { return L >= 0 && L <= p.max_parts * p.part_tokens; };
+  auto clear = [&] {
+    for (int i = threadIdx.x; i <= kMaxChunkCounts; i += kListThreads) hist[i] = 0;
+    __syncthreads();
+  };
+  auto count = [&](int L) {
+    if (!counts(L)) return;
     const int nfull = L / p.part_tokens, rem = L - nfull * p.part_tokens;
     if (nfull) atomicAdd(&hist[full_chunks], nfull * H);
     if (rem) atomicAdd(&hist[(rem + kChunk - 1) / kChunk], H);
-  }
-  __syncthreads();
-  int run = 0;
-  if (threadIdx.x == 0) {
-    for (int c = kMaxChunkCounts; c >= 1; --c) {
-      next[c] = run;
-      run += hist[c];
+  };
+  int run = 0;  // thread 0: the list's entries
+  auto places = [&] {  // of each chunk count's first entry, longest first
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      run = 0;
+      for (int c = kMaxChunkCounts; c >= 1; --c) {
+        next[c] = run;
+        run += hist[c];
+      }
     }
-  }
+  };
+  const bool guess = p.num_seqs <= kListThreads;  // a length per thread
+  const bool mine = guess && static_cast<int>(threadIdx.x) < p.num_seqs;
+  const int guessed = mine ? __ldcg(p.context_lens + threadIdx.x) : 0;  // not through L1, which would keep it past the wait
+  clear();
+  if (mine) count(guessed);
+  places();
   grid_dependency_wait();
+  const int held = mine ? p.context_lens[threadIdx.x] : 0;
+  if (__syncthreads_or(!guess || held != guessed)) {
+    clear();
+    for (int s = threadIdx.x; s < p.num_seqs; s += kListThreads) count(p.context_lens[s]);
+    places();
+    __syncthreads();
+  }
   if (threadIdx.x == 0) {
     *p.work_count = run;
     *p.work_next = 0;  // claims past the decode grid's first items
   }
-  __syncthreads();
   for (int s = threadIdx.x; s < p.num_seqs; s += kListThreads) {
-    const int L = p.context_lens[s];
-    if (L <= 0 || L > p.max_parts * p.part_tokens) continue;
+    const int L = guess ? held : p.context_lens[s];
+    if (!counts(L)) set_error(p.err, kErrLength);
+    if (L <= 0 || !counts(L)) continue;
     const int nparts = (L + p.part_tokens - 1) / p.part_tokens;
     for (int part = 0; part < nparts; ++part) {
       const int t0 = part * p.part_tokens;
