@@ -34,8 +34,8 @@
 // places past the item's last come from outside the tensor: zeros), warps 10 and 11 the MMA issuers
 // of the two warpgroups.
 //
-// Measured (64/8 heads, D 128, bf16): four prompts of 1,000 to 2,000 new tokens, window 1,024: 225 us;
-// 32 sequences with 3 to 8 new tokens, window 4,096: 108 us.
+// Measured (64/8 heads, D 128, bf16): four prompts of 1,000 to 2,000 new tokens, window 1,024:
+// 224 to 235 us; 32 sequences with 3 to 8 new tokens, window 4,096: 107 to 109 us.
 // Bound: pairs: 2,150 clocks a chunk, of which the softmax's dependent instructions take 1,900 and the
 // tensor cores' products 1,800 (QK with 64 keys runs at 2/3 of their rate: shared memory feeds the
 // 128 query rows), and 3 to 4 us between items.  Shared tiles: the K producer's turns and the

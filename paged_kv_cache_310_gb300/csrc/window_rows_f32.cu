@@ -14,7 +14,7 @@
 // 64/8 heads, window 1,024.)
 //
 // Bound: HBM with up to 8 heads (32 sequences of 0 to 6,000 tokens, window 1,021, 32/8 heads: 44 us, copy
-// bandwidth would take 36); instructions with 16 (32 sequences, 128/8 heads, window 1,024: 82 us,
+// bandwidth would take 36); instructions with 16 (32 sequences, 128/8 heads, window 1,024: 76 us,
 // 40); for few sequences the chain launch -> length -> block table -> K/V -> join.
 #include "window_rows.cuh"
 
