@@ -382,7 +382,8 @@ pkv_status paged_qk_rotary(const void* q, int64_t q_stride, const void* k, int64
  * cache's dtype (f32, f16 or bf16) and heads of its head_dim, k and v its KV heads.
  * Tokens with a negative slot or a negative position are padding: nothing of them is
  * written, to q_out neither, and their slot or position does not matter.  Any other token's slot
- * >= num_blocks * block_size sets the device index flag and the token is skipped as well.  Slots must be distinct (duplicates race).
+ * >= num_blocks * block_size sets the device index flag and the token is skipped as well.
+ * Slots must be distinct (duplicates race).
  */
 pkv_status paged_kv_append_rotary(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                                   int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping,

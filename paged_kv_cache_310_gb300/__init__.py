@@ -901,6 +901,9 @@ def paged_attention_prefill_window_plan(num_seqs, num_q_heads, num_query_tokens,
     """The kernel ("rows", "shared_tiles" or "tile_pairs"), new tokens per item and CTAs per item that
     paged_attention_prefill_window uses for these sizes."""
     desc, plan = cache_desc(k_cache), WindowPlan()
+    for n in (num_seqs, num_q_heads, num_query_tokens, max_context_len):
+        if not -1 <= n <= _INT32_MAX:
+            raise PagedKVError(1, f"size {n}")
     _check(library().paged_attention_prefill_window_plan(num_seqs, num_q_heads, num_query_tokens, max_context_len,
                                                          _tokens(window), _tokens(sinks), ctypes.byref(desc), ctypes.byref(plan)))
     return dict(kernel=_WINDOW_KERNELS[plan.kernel], tokens_per_item=plan.tokens_per_item, ctas_per_item=plan.ctas_per_item)

@@ -73,6 +73,15 @@ def test_refusals(lib):
     assert fn(4, 64, 100, 1000, 100, 0, ctypes.byref(d), ctypes.byref(out)) == 0
 
 
+@pytest.mark.parametrize("name", ["seqs", "hq", "tokens", "longest"])
+def test_sizes_past_32_bits_are_refused(lib, name):
+    args = dict(seqs=4, hq=64, tokens=100, longest=1000, window=100)
+    for wide in (2 ** 31, 2 ** 32 + args[name], -2 ** 32 + args[name], 1 << 70):
+        with pytest.raises(pkv.PagedKVError) as e:
+            plan(**{**args, name: wide})
+        assert e.value.status == 1, wide
+
+
 def named_sizes():
     """(kernel, seqs, hq, tokens, longest, window, sinks, hkv, d) of the tests that name their kernel."""
     for d, group, hkv, lens, new, window, sinks, kernel in prefill_tests.TILES:
