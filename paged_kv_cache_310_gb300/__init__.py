@@ -504,6 +504,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # handle alo
 _get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device  # CUDA is up: there are tensors on it
 
 
+_INT32_MAX = 2 ** 31 - 1
+
+
+def _count(n: int) -> int:
+    """A number of tokens that may be past any sequence's (a window, sinks, recent rows) as 32 bits hold
+    it, where ctypes would keep the low 32 bits of a larger one; negative ones are for the library to refuse."""
+    return max(-1, min(n, _INT32_MAX))
+
+
 def _one_device(first, *rest) -> int:
     """The index of the CUDA device that all the (contiguous) tensors are on."""
     device = first.get_device()
@@ -702,14 +711,13 @@ def paged_kv_evict(weights, block_tables, context_lens, keep_lens, new_tables, k
     if max_context_len is None:
         max_context_len = int(context_lens.max()) if S else 0
     _call(library().paged_kv_evict, device, weights.data_ptr(), weights_out.data_ptr(), weights.shape[2],
-          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), keep_lens.data_ptr(), recent,
+          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), keep_lens.data_ptr(), _count(recent),
           new_tables.data_ptr(), new_tables.shape[1], S, max_context_len, kept.shape[2], kept.data_ptr(),
           k_cache.data_ptr(), v_cache.data_ptr(), desc_ref)
 
 
 # ---- rotary positions
 
-_INT32_MAX = 2 ** 31 - 1
 _ROTARY_RULES = {None: 0, "linear": 1, "base": 2, "parts": 3}
 
 
@@ -830,12 +838,6 @@ def paged_kv_append_rotary(q, k, v, positions, slot_mapping, k_cache, v_cache, q
 
 # ---- sliding windows
 
-def _tokens(n: int) -> int:
-    """A window or a number of sinks as 32 bits hold it (ctypes would keep the low 32 bits of a
-    larger number): past the longest sequence either way, or negative for the library to refuse."""
-    return max(-1, min(n, _INT32_MAX))
-
-
 def _window_args(q, k_cache, v_cache, block_tables, context_lens, out, more, max_context_len):
     """Checks that both windowed calls make; (device, descriptor reference, out's dtype code,
     rows and heads of q, sequences, table width, bound of the lengths)."""
@@ -873,7 +875,7 @@ def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_len
     if T != S:
         raise PagedKVError(1, "context_lens must be [S]")
     _call(library().paged_attention_decode_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          block_tables.data_ptr(), width, context_lens.data_ptr(), S, Hq, longest, _tokens(window), _tokens(sinks),
+          block_tables.data_ptr(), width, context_lens.data_ptr(), S, Hq, longest, _count(window), _count(sinks),
           float(scale), out.data_ptr(), out_code, desc_ref)
     return out
 
@@ -888,8 +890,8 @@ def paged_attention_prefill_window(q, k_cache, v_cache, block_tables, context_le
     if query_start.dtype is not torch.int32 or query_start.numel() != S + 1:
         raise PagedKVError(1, "query_start must be int32 [S+1]")
     _call(library().paged_attention_prefill_window, device, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-          block_tables.data_ptr(), width, context_lens.data_ptr(), query_start.data_ptr(), S, Hq, T, longest, _tokens(window),
-          _tokens(sinks), float(scale), out.data_ptr(), out_code, desc_ref)
+          block_tables.data_ptr(), width, context_lens.data_ptr(), query_start.data_ptr(), S, Hq, T, longest, _count(window),
+          _count(sinks), float(scale), out.data_ptr(), out_code, desc_ref)
     return out
 
 
@@ -905,7 +907,7 @@ def paged_attention_prefill_window_plan(num_seqs, num_q_heads, num_query_tokens,
         if not -1 <= n <= _INT32_MAX:
             raise PagedKVError(1, f"size {n}")
     _check(library().paged_attention_prefill_window_plan(num_seqs, num_q_heads, num_query_tokens, max_context_len,
-                                                         _tokens(window), _tokens(sinks), ctypes.byref(desc), ctypes.byref(plan)))
+                                                         _count(window), _count(sinks), ctypes.byref(desc), ctypes.byref(plan)))
     return dict(kernel=_WINDOW_KERNELS[plan.kernel], tokens_per_item=plan.tokens_per_item, ctas_per_item=plan.ctas_per_item)
 
 
