@@ -17,7 +17,7 @@
 //
 // Bound: for few sequences the chain launch -> length -> block table -> K/V -> join (one, window
 // 1,024: 7.0 us in a graph); for many, HBM (128 of 512 to 32,768 tokens, window 4,096, 64/8 heads,
-// D 128, bf16: 298 to 306 us, 6.9 TB/s).
+// D 128, bf16: 298 to 306 us, 6.8 to 7.0 TB/s).
 #include "window_rows.cuh"
 
 namespace pkv {
